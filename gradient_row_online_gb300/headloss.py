@@ -45,13 +45,15 @@ SLOTS = ("total", "ce", "z", "dist_ce", "fkl", "rkl", "grpo_loss", "new_logprob_
          "ratio_mean", "clip_frac", "kl_k3", "adv_mean", "adv_std", "entropy_mean", "n_valid",
          "n_clipped")
 
-# Every function declared in include/headloss.h and include/headloss_lmhead.h.
+# Every function declared in the headers under include/.
 EXPORTS = ("headloss_create", "headloss_forward_backward", "headloss_get_device_error",
            "headloss_plan", "headloss_force_plan", "headloss_launches_per_call",
            "headloss_destroy", "headloss_strerror", "headloss_version",
            "headloss_forward_backward_noalloc", "headloss_forward_backward_ext",
            "headloss_gspo_seam", "headloss_forward_backward_rowstats",
-           "headloss_lmhead_logits", "headloss_lmhead_logits_rowstats")
+           "headloss_lmhead_logits", "headloss_lmhead_logits_rowstats",
+           "headloss_sample", "headloss_clip_create", "headloss_clip_grads",
+           "headloss_clip_destroy")
 
 
 # enum headloss_kernel
@@ -65,6 +67,12 @@ class headloss_call_ext(ctypes.Structure):
     _fields_ = [("new_logprobs", ctypes.c_void_p), ("row_loss", ctypes.c_void_p),
                 ("accumulate", ctypes.c_int), ("divisor", ctypes.c_double),
                 ("token_coeff", ctypes.c_void_p)]
+
+
+class headloss_gradient(ctypes.Structure):
+    """struct headloss_gradient: one tensor of a clipping call."""
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("dtype", ctypes.c_int)]
 
 
 class headloss_plan_desc(ctypes.Structure):
@@ -135,6 +143,16 @@ def load_library(path: str = LIB_PATH):
     lib.headloss_forward_backward_rowstats.argtypes = [vp, vp, i64, i64, i32, vp, vp, vp, vp, vp,
                                                        vp, vp, vp, vp, vp, vp]
     lib.headloss_forward_backward_rowstats.restype = i32
+    lib.headloss_sample.argtypes = [vp, i64, i64, i64, i32, vp, vp, vp, vp, vp, f32, f32, vp, vp,
+                                    vp, vp, vp, vp]
+    lib.headloss_sample.restype = i32
+    lib.headloss_clip_create.argtypes = [i32, ctypes.POINTER(vp)]
+    lib.headloss_clip_create.restype = i32
+    lib.headloss_clip_grads.argtypes = [vp, ctypes.POINTER(headloss_gradient), i32, f32, f32, vp,
+                                        vp]
+    lib.headloss_clip_grads.restype = i32
+    lib.headloss_clip_destroy.argtypes = [vp]
+    lib.headloss_clip_destroy.restype = None
     _lib = lib
     return lib
 
@@ -288,6 +306,38 @@ def headloss_gspo_seam(new_logprobs, old_logprobs, advantages, labels, N, V, seg
         _ptr(token_coeff), _ptr(scalars_out), _stream(stream)), "headloss_gspo_seam")
 
 
+def headloss_sample(logits, N, V, ld, dtype, uniforms, temperature, top_k, top_p, min_p, softcap,
+                    logits_scale, tokens, logprobs, draw_logprobs, n_kept, err,
+                    stream=None) -> None:
+    """One token a row from the head's logits (include/headloss_sample.h); raises
+    HeadlossError on a bad status."""
+    _check(load_library().headloss_sample(
+        _ptr(logits), int(N), int(V), int(ld), int(dtype), _ptr(uniforms), _ptr(temperature),
+        _ptr(top_k), _ptr(top_p), _ptr(min_p), float(softcap), float(logits_scale), _ptr(tokens),
+        _ptr(logprobs), _ptr(draw_logprobs), _ptr(n_kept), _ptr(err), _stream(stream)),
+        "headloss_sample")
+
+
+def headloss_clip_create(max_grads: int) -> int:
+    h = ctypes.c_void_p()
+    _check(load_library().headloss_clip_create(int(max_grads), ctypes.byref(h)),
+           "headloss_clip_create")
+    return h.value
+
+
+def headloss_clip_grads(h, grads, n_grads, max_norm, inv_scale, stats_out, stream=None) -> None:
+    """Global norm and clipping of a list of tensors (include/headloss_clip.h);
+    `grads` is an array of headloss_gradient; raises HeadlossError on a bad status."""
+    _check(load_library().headloss_clip_grads(h, grads, int(n_grads), float(max_norm),
+                                              float(inv_scale), _ptr(stats_out),
+                                              _stream(stream)), "headloss_clip_grads")
+
+
+def headloss_clip_destroy(h) -> None:
+    if h:
+        load_library().headloss_clip_destroy(h)
+
+
 def headloss_get_device_error(h, stream=None) -> int:
     lib = load_library()
     e = ctypes.c_int()
@@ -370,6 +420,121 @@ class HeadLoss:
     def close(self):
         if self.h:
             headloss_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class HeadSampler:
+    """headloss_sample on torch tensors: one token a row of `logits` (N x V, unit
+    column stride, any row stride), from one uniform a row.
+
+    The settings are per-row tensors (temperature, top_p, min_p fp32; top_k
+    int32), numbers for every row, or None (off).  Returns (tokens int64, log p
+    at T = 1 of the whole softmax fp32, log p under the distribution drawn from
+    fp32, tokens that could be drawn int32); `out` gives the four buffers."""
+
+    def __init__(self, softcap: float = 0.0, logits_scale: float = 1.0, device="cuda"):
+        import torch
+        self.softcap, self.logits_scale = float(softcap), float(logits_scale)
+        self.err = torch.zeros(1, dtype=torch.int32, device=device)
+        self._settings = (("temperature", torch.float32), ("top_k", torch.int32),
+                          ("top_p", torch.float32), ("min_p", torch.float32))
+
+    @staticmethod
+    def _given(name, a, dtype, shape, device):
+        import torch
+        if a is None:
+            return None
+        if isinstance(a, (int, float)):
+            return torch.full(shape, a, dtype=dtype, device=device)
+        if a.dtype != dtype or a.shape != shape or a.device != device or not a.is_contiguous():
+            raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                             f"{device} is wanted")
+        return a
+
+    def __call__(self, logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=None,
+                 out=None, stream=None):
+        import torch
+        if logits.dim() != 2 or logits.shape[1] < 1 or logits.device != self.err.device or (
+                logits.shape[1] > 1 and logits.stride(1) != 1):
+            raise ValueError("logits: an N x V tensor with unit column stride on "
+                             f"{self.err.device} is wanted")
+        N, V = logits.shape
+        ld = logits.stride(0) if N > 1 else V
+        if logits.dtype not in (torch.float32, torch.bfloat16, torch.float16):
+            raise HeadlossError(HEADLOSS_ERR_DTYPE, "headloss_sample")
+        device, rows = logits.device, logits.shape[:1]
+        uniforms = self._given("uniforms", uniforms, torch.float64, rows, device)
+        if uniforms is None:
+            raise HeadlossError(HEADLOSS_ERR_MISSING_INPUT, "headloss_sample")
+        given = [self._given(name, a, dtype, rows, device) for (name, dtype), a in
+                 zip(self._settings, (temperature, top_k, top_p, min_p))]
+        wanted = (torch.int64, torch.float32, torch.float32, torch.int32)
+        if out is None:
+            out = tuple(torch.empty(rows, dtype=t, device=device) for t in wanted)
+        else:
+            for name, a, t in zip(("tokens", "logprobs", "draw_logprobs", "n_kept"), out, wanted):
+                self._given(name, a, t, rows, device)
+        headloss_sample(logits, N, V, ld, dtype_code(logits.dtype), uniforms, *given,
+                        self.softcap, self.logits_scale, *out, self.err, stream)
+        return out
+
+    def device_error(self, stream=None) -> int:
+        """Synchronise `stream`, then read and clear the error word (bit 0: settings
+        out of range; bit 1: a copy wait gave up)."""
+        import torch
+        if stream is None:
+            stream = torch.cuda.current_stream()
+        elif isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream)
+        with torch.cuda.stream(stream):
+            e = int(self.err.item())
+            self.err.zero_()
+        return e
+
+
+class GradClipper:
+    """headloss_clip_grads on torch tensors: the global norm over `grads` and one
+    factor on all of them, into `outs` (None: in place).  The tensors are held;
+    `bind` takes others.  Calling it returns the device tensor (norm, factor)."""
+
+    def __init__(self, grads, outs=None, max_grads: int = 0):
+        self.h = None
+        self.max_grads = max(int(max_grads), len(grads), 1)
+        self.bind(grads, outs)
+        self.h = headloss_clip_create(self.max_grads)
+
+    def bind(self, grads, outs=None) -> None:
+        grads = list(grads)
+        outs = grads if outs is None else list(outs)
+        if len(outs) != len(grads) or len(grads) > self.max_grads:
+            raise ValueError(f"{len(grads)} gradients and {len(outs)} outputs (up to "
+                             f"{self.max_grads})")
+        table = (headloss_gradient * max(1, len(grads)))()
+        for e, g, o in zip(table, grads, outs):
+            if not g.is_cuda or not g.is_contiguous() or not o.is_contiguous() or (
+                    o.dtype != g.dtype or o.shape != g.shape or o.device != g.device):
+                raise ValueError("gradients are contiguous CUDA tensors, their outputs of the "
+                                 "same type, shape and device")
+            e.grad, e.out, e.n, e.dtype = g.data_ptr(), o.data_ptr(), g.numel(), dtype_code(g.dtype)
+        self.grads, self.outs, self.table = grads, outs, table
+
+    def __call__(self, max_norm: float, inv_scale: float = 1.0, stats=None, stream=None):
+        import torch
+        if stats is None:
+            device = self.grads[0].device if self.grads else "cuda"
+            stats = torch.empty(2, dtype=torch.float32, device=device)
+        headloss_clip_grads(self.h, self.table, len(self.grads), max_norm, inv_scale, stats, stream)
+        return stats
+
+    def close(self):
+        if self.h:
+            headloss_clip_destroy(self.h)
             self.h = None
 
     def __del__(self):

@@ -1,11 +1,17 @@
 // hl_clip.cu -- the global gradient norm over many tensors, and clipping
 // (headloss_clip_grads in include/headloss_clip.h).
 //
-// The list is cut into chunks of at most CHUNK elements, none across two
-// tensors.  One kernel sums the squares of a chunk (fp32 a thread over
-// CHUNK / THREADS elements, fp64 from there on), a second joins the chunks in
-// a fixed order and scales.  The list goes to the workspace in kernel
-// arguments, a few hundred entries a launch.
+// One cooperative kernel.  The list is cut into tiles of 256 16-byte words, none
+// across two tensors; a CTA takes a contiguous run of tiles, its warps in turn, eight words a
+// lane in flight.
+//   phase 1   squares, in fp32 over a lane's share of one tile (at most 64), in
+//             fp64 from there on, in an order that the sizes and the grid fix;
+//   barrier   over the grid (bounded); the last CTA to arrive joins the CTAs' sums in
+//             their order and publishes the factor;
+//   phase 2   the run again, backwards: the last tile is still in registers, the ones before it
+//             still in L2.  In place with factor 1 it is left out.
+// The factor needs the whole norm first, so gradients beyond what the chip holds are read
+// twice: 3 n bytes where the operator's own floor is 2 n.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math_constants.h>
@@ -19,118 +25,451 @@
 
 namespace hl_clip {
 
-constexpr int THREADS = 256;
-constexpr int CHUNK = 16384;
-constexpr int GRID = 152 * 8;
-constexpr int BATCH = 120;  // list entries a launch of list_kernel carries
+constexpr int THREADS = 512;
+constexpr int WARPS = THREADS / 32;
+constexpr int LANE_WORDS = 8;
+constexpr int TILE = 32 * LANE_WORDS;  // words a tile
+constexpr int MAX_GRID = 512;
+constexpr int BATCH = 512;             // list entries a launch of list_kernel carries
+constexpr unsigned FULL = 0xffffffffu;
+constexpr unsigned long long WAIT_NS = 2000000000ull;
 
 struct Entry {
     const void* grad;
     void* out;
     int64_t n;
-    int64_t first;  // index of the tensor's first chunk
+    uint32_t first;  // index of the tensor's first tile
     int dtype;
+};
+
+// A list in kernel arguments, with the entry each CTA's run starts in (N = 0: the list is in
+// the workspace).
+template <int N>
+struct List {
+    Entry e[N];
+    uint16_t start[MAX_GRID];
+};
+template <>
+struct List<0> {
+    const Entry* e;
 };
 struct Batch {
     Entry e[BATCH];
+};
+
+struct Sync {
+    unsigned arrived, generation;
+    float norm, factor;
+    double parts[MAX_GRID];
+};
+
+struct Call {
+    int n;            // entries
+    uint32_t tiles;
+    double max_norm;
+    float inv_scale;
+    float* stats;
+    Sync* sync;
 };
 
 __global__ void list_kernel(const __grid_constant__ Batch b, Entry* list, int at, int n) {
     for (int i = threadIdx.x; i < n; i += blockDim.x) list[at + i] = b.e[i];
 }
 
-__device__ __forceinline__ float load(const void* p, int64_t i, int dtype) {
-    if (dtype == HEADLOSS_FP32) return static_cast<const float*>(p)[i];
-    if (dtype == HEADLOSS_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-    return __half2float(static_cast<const __half*>(p)[i]);
-}
-__device__ __forceinline__ void store(void* p, int64_t i, int dtype, float v) {
-    if (dtype == HEADLOSS_FP32) static_cast<float*>(p)[i] = v;
-    else if (dtype == HEADLOSS_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-    else static_cast<__half*>(p)[i] = __float2half_rn(v);
-}
+// ---------------------------------------------------------------- elements ----
 
-// The entry of a chunk: the last one whose first chunk is not after it.
-__device__ int entry_of(const Entry* list, int n, int64_t chunk) {
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (list[mid].first <= chunk) lo = mid;
-        else hi = mid;
+template <int DTYPE>
+struct Type;
+template <>
+struct Type<HEADLOSS_FP32> {
+    using T = float;
+    static constexpr int EPW = 4;
+    __device__ static void unpack(const uint4& w, float* v) {
+        v[0] = __uint_as_float(w.x), v[1] = __uint_as_float(w.y);
+        v[2] = __uint_as_float(w.z), v[3] = __uint_as_float(w.w);
     }
-    return lo;
+    __device__ static uint4 pack(const float* v) {
+        return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                          __float_as_uint(v[3]));
+    }
+    __device__ static float up(float x) { return x; }
+    __device__ static float down(float v) { return v; }
+};
+template <>
+struct Type<HEADLOSS_BF16> {
+    using T = __nv_bfloat16;
+    static constexpr int EPW = 8;
+    __device__ static void unpack(const uint4& w, float* v) {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(u[i] << 16);
+            v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    }
+    __device__ static uint4 pack(const float* v) {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        return make_uint4(u[0], u[1], u[2], u[3]);
+    }
+    __device__ static float up(T x) { return __bfloat162float(x); }
+    __device__ static T down(float v) { return __float2bfloat16_rn(v); }
+};
+template <>
+struct Type<HEADLOSS_FP16> {
+    using T = __half;
+    static constexpr int EPW = 8;
+    __device__ static void unpack(const uint4& w, float* v) {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+            v[2 * i] = f.x, v[2 * i + 1] = f.y;
+        }
+    }
+    __device__ static uint4 pack(const float* v) {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        return make_uint4(u[0], u[1], u[2], u[3]);
+    }
+    __device__ static float up(T x) { return __half2float(x); }
+    __device__ static T down(float v) { return __float2half_rn(v); }
+};
+
+// -------------------------------------------------------------------- tiles ----
+
+// Where a tile's words lie: word w of the tensor starts at base + 16 w, base the tensor's
+// address rounded down, head elements of word 0 before it.
+struct Place {
+    const char* base;
+    int64_t w0;      // the tile's first word
+    int words;       // of the tile, 1 .. TILE
+    int head;
+    bool whole;      // every word of the tile lies inside the tensor
+};
+
+template <int D>
+__device__ __forceinline__ Place place_of(const Entry& t, uint32_t tile) {
+    constexpr int EPW = Type<D>::EPW, ES = 16 / EPW;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(t.grad);
+    Place p;
+    p.base = reinterpret_cast<const char*>(at & ~uintptr_t(15));
+    p.head = int(at & 15) / ES;
+    const int64_t all = (p.head + t.n + EPW - 1) / EPW;
+    p.w0 = int64_t(tile - t.first) * TILE;
+    p.words = all - p.w0 < TILE ? int(all - p.w0) : TILE;
+    p.whole = p.words == TILE && (p.w0 > 0 || p.head == 0) &&
+              ((p.w0 + TILE) * EPW <= p.head + t.n);
+    return p;
 }
 
+// A lane's eight words of a whole tile.
+__device__ __forceinline__ void load_tile(const Place& p, int lane, uint4* d) {
+    const uint4* w = reinterpret_cast<const uint4*>(p.base) + p.w0;
+#pragma unroll
+    for (int i = 0; i < LANE_WORDS; ++i) d[i] = w[i * 32 + lane];
+}
+
+// Sum of a lane's squares of a whole tile.
+template <int D>
+__device__ __forceinline__ float squares(const uint4* d) {
+    constexpr int EPW = Type<D>::EPW;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < LANE_WORDS; ++i) {
+        float v[EPW];
+        Type<D>::unpack(d[i], v);
+#pragma unroll
+        for (int e = 0; e < EPW; ++e) s[e & 3] = fmaf(v[e], v[e], s[e & 3]);
+    }
+    return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+// out's words of a whole tile, where out lies on the 16-byte grid as grad does.
+template <int D>
+__device__ __forceinline__ void store_tile(uint4* out, int lane, const uint4* d, float factor) {
+    constexpr int EPW = Type<D>::EPW;
+#pragma unroll
+    for (int i = 0; i < LANE_WORDS; ++i) {
+        float v[EPW];
+        Type<D>::unpack(d[i], v);
+#pragma unroll
+        for (int e = 0; e < EPW; ++e) v[e] *= factor;
+        __stcs(out + i * 32 + lane, Type<D>::pack(v));
+    }
+}
+
+// Any tile word by word: a lane's sum of squares of values times `by` (out = nullptr), or the
+// values times `by` to out.  The ends of a tensor, tensors whose output lies off the
+// gradient's 16-byte grid, and sums that left fp32's range.
+template <int D>
+__device__ __noinline__ float any_tile(const Entry& t, uint32_t tile, int lane, float by, bool store) {
+    constexpr int EPW = Type<D>::EPW;
+    using T = typename Type<D>::T;
+    const Place p = place_of<D>(t, tile);
+    const T* x = static_cast<const T*>(t.grad);
+    T* y = static_cast<T*>(t.out);
+    float s = 0.f;
+    for (int k = lane; k < p.words; k += 32) {
+        const int64_t first = (p.w0 + k) * EPW - p.head;  // element of the tensor
+        float v[EPW];
+        if (first >= 0 && first + EPW <= t.n) {
+            Type<D>::unpack(reinterpret_cast<const uint4*>(p.base)[p.w0 + k], v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < EPW; ++e)
+                v[e] = first + e >= 0 && first + e < t.n ? Type<D>::up(x[first + e]) : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < EPW; ++e) {
+            v[e] *= by;
+            s = fmaf(v[e], v[e], s);
+        }
+        if (!store) continue;
+        if (first >= 0 && first + EPW <= t.n &&
+            (reinterpret_cast<uintptr_t>(y + first) & 15) == 0) {
+            __stcs(reinterpret_cast<uint4*>(y + first), Type<D>::pack(v));
+        } else {
+#pragma unroll
+            for (int e = 0; e < EPW; ++e)
+                if (first + e >= 0 && first + e < t.n) y[first + e] = Type<D>::down(v[e]);
+        }
+    }
+    return s;
+}
+
+// A lane's sum of a tile's squares in fp64, from scaled values where the plain sum left fp32's
+// range or came near its lower end.  Whole tiles stay in d.
+template <int D>
+__device__ __forceinline__ double sum_tile(const Entry& t, uint32_t tile, int lane, uint4* d,
+                                           bool* whole) {
+    const Place p = place_of<D>(t, tile);
+    float s;
+    *whole = p.whole;
+    if (p.whole) {
+        load_tile(p, lane, d);
+        s = squares<D>(d);
+    } else {
+        s = any_tile<D>(t, tile, lane, 1.f, false);
+    }
+    if (s >= 1e-24f && s <= 1e36f) return double(s);
+    const bool low = s < 1e-24f;
+    return double(any_tile<D>(t, tile, lane, low ? 0x1p+60f : 0x1p-70f, false)) *
+           (low ? 0x1p-120 : 0x1p+140);
+}
+
+// The clipped tile; `here`: it is in d.
+template <int D>
+__device__ __forceinline__ void clip_tile(const Entry& t, uint32_t tile, int lane, uint4* d,
+                                          bool here, float factor) {
+    constexpr int EPW = Type<D>::EPW, ES = 16 / EPW;
+    const Place p = place_of<D>(t, tile);
+    char* at = static_cast<char*>(t.out) + (p.w0 * EPW - p.head) * ES;
+    if (!p.whole || (reinterpret_cast<uintptr_t>(at) & 15)) {
+        any_tile<D>(t, tile, lane, factor, true);
+        return;
+    }
+    if (!here) load_tile(p, lane, d);
+    store_tile<D>(reinterpret_cast<uint4*>(at), lane, d, factor);
+}
+
+// ------------------------------------------------------------------- kernel ----
+
+__device__ __forceinline__ unsigned load_acquire(const unsigned* p) {
+    unsigned v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void store_release(unsigned* p, unsigned v) {
+    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ unsigned long long now_ns() {
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+
+// The block's sum, in thread 0 (a fixed order).
 __device__ double block_sum(double v) {
-    __shared__ double red[THREADS / 32];
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __shared__ double red[WARPS];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
     v = 0.0;
-    for (int i = 0; i < THREADS / 32; ++i) v += red[i];
+    if (threadIdx.x == 0)
+        for (int i = 0; i < WARPS; ++i) v += red[i];
     return v;
 }
 
-// The sum of a thread's squares, again from scaled values where the plain sum left
-// fp32's range (or came too near its lower end).
-constexpr float LOW = 1e-24f, HIGH = 1e36f;
+template <int N>
+__global__ void __launch_bounds__(THREADS, 2) clip_kernel(const __grid_constant__ List<N> list,
+                                                          const __grid_constant__ Call c) {
+    __shared__ bool s_last;
+    __shared__ float s_factor;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t t0 = uint32_t(uint64_t(c.tiles) * blockIdx.x / gridDim.x);
+    const uint32_t t1 = uint32_t(uint64_t(c.tiles) * (blockIdx.x + 1) / gridDim.x);
+    int at;
+    if constexpr (N > 0) {
+        at = list.start[blockIdx.x];
+    } else {
+        int lo = 0, hi = c.n;  // the last entry whose first tile is not after t0
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (list.e[mid].first <= t0) lo = mid;
+            else hi = mid;
+        }
+        at = lo;
+    }
 
-__global__ void __launch_bounds__(THREADS) norm_kernel(const Entry* list, int n, int64_t chunks,
-                                                       double* parts) {
+    uint4 d[LANE_WORDS];
     double mine = 0.0;
-    for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-        const Entry& t = list[entry_of(list, n, c)];
-        const int64_t a = (c - t.first) * CHUNK, b = min(t.n, a + CHUNK);
-        const int dtype = t.dtype;
-        float s = 0.f;
-        for (int64_t i = a + threadIdx.x; i < b; i += THREADS) {
-            const float v = load(t.grad, i, dtype);
-            s = fmaf(v, v, s);
-        }
-        if (s >= LOW && s <= HIGH) {
-            mine += double(s);
-        } else {
-            const float up = s < LOW ? 0x1p+60f : 0x1p-70f;
-            s = 0.f;
-            for (int64_t i = a + threadIdx.x; i < b; i += THREADS) {
-                const float v = load(t.grad, i, dtype) * up;
-                s = fmaf(v, v, s);
-            }
-            mine += double(s) / (double(up) * double(up));
-        }
+    uint32_t last = 0xffffffffu;  // the warp's last tile, in d where it is whole
+    bool here = false;
+    for (uint32_t t = t0 + warp; t < t1; t += WARPS) {
+        while (at + 1 < c.n && list.e[at + 1].first <= t) ++at;
+        const Entry& e = list.e[at];
+        if (e.dtype == HEADLOSS_BF16) mine += sum_tile<HEADLOSS_BF16>(e, t, lane, d, &here);
+        else if (e.dtype == HEADLOSS_FP32) mine += sum_tile<HEADLOSS_FP32>(e, t, lane, d, &here);
+        else mine += sum_tile<HEADLOSS_FP16>(e, t, lane, d, &here);
+        last = t;
     }
     mine = block_sum(mine);
-    if (threadIdx.x == 0) parts[blockIdx.x] = mine;
+
+    Sync* s = c.sync;
+    if (threadIdx.x == 0) {
+        s->parts[blockIdx.x] = mine;
+        const unsigned before = load_acquire(&s->generation);
+        __threadfence();
+        s_last = atomicAdd(&s->arrived, 1u) == gridDim.x - 1;
+        __threadfence();
+        if (!s_last) {
+            const unsigned long long began = now_ns();
+            bool given_up = false;
+            while (load_acquire(&s->generation) == before)
+                if (now_ns() - began > WAIT_NS) {
+                    given_up = true;
+                    break;
+                }
+            s_factor = given_up ? 1.f : *reinterpret_cast<volatile float*>(&s->factor);
+            if (given_up) c.stats[0] = c.stats[1] = CUDART_NAN_F;
+        }
+    }
+    __syncthreads();
+    if (s_last) {
+        double v = 0.0;
+        for (int i = threadIdx.x; i < int(gridDim.x); i += THREADS)
+            v += reinterpret_cast<volatile double*>(s->parts)[i];
+        v = block_sum(v);
+        if (threadIdx.x == 0) {
+            const double norm = double(c.inv_scale) * sqrt(v);
+            const float factor = norm > c.max_norm && isfinite(float(norm))
+                                     ? float(double(c.inv_scale) * (c.max_norm / norm))
+                                     : c.inv_scale;
+            c.stats[0] = float(norm), c.stats[1] = factor;
+            s->factor = factor;
+            s->arrived = 0;
+            s_factor = factor;
+            __threadfence();
+            store_release(&s->generation, s->generation + 1);
+        }
+    }
+    __syncthreads();
+    const float factor = s_factor;
+
+    if (last == 0xffffffffu) return;
+    for (uint32_t t = last;; t -= WARPS) {
+        while (list.e[at].first > t) --at;
+        const Entry& e = list.e[at];
+        if (factor != 1.f || e.grad != e.out) {
+            if (e.dtype == HEADLOSS_BF16) clip_tile<HEADLOSS_BF16>(e, t, lane, d, here, factor);
+            else if (e.dtype == HEADLOSS_FP32) clip_tile<HEADLOSS_FP32>(e, t, lane, d, here, factor);
+            else clip_tile<HEADLOSS_FP16>(e, t, lane, d, here, factor);
+        }
+        here = false;
+        if (t < t0 + WARPS) break;
+    }
 }
 
-__global__ void __launch_bounds__(THREADS) scale_kernel(const Entry* list, int n, int64_t chunks,
-                                                        const double* parts, float max_norm,
-                                                        float inv_scale, float* stats) {
-    double total = 0.0;
-    for (int i = threadIdx.x; i < GRID; i += THREADS) total += parts[i];
-    total = block_sum(total);
-    const double norm = double(inv_scale) * sqrt(total);
-    const float factor = norm > double(max_norm) && isfinite(float(norm))
-                             ? float(double(inv_scale) * (double(max_norm) / norm))
-                             : inv_scale;
-    if (blockIdx.x == 0 && threadIdx.x == 0) stats[0] = float(norm), stats[1] = factor;
-    for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-        const Entry& t = list[entry_of(list, n, c)];
-        if (factor == 1.f && t.grad == t.out) continue;
-        const int64_t a = (c - t.first) * CHUNK, b = min(t.n, a + CHUNK);
-        const int dtype = t.dtype;
-        for (int64_t i = a + threadIdx.x; i < b; i += THREADS)
-            store(t.out, i, dtype, load(t.grad, i, dtype) * factor);
+template <int N>
+int launch(const List<N>& list, const Call& call, int grid, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(grid));
+    cfg.blockDim = dim3(THREADS);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void* args[] = {const_cast<List<N>*>(&list), const_cast<Call*>(&call)};
+    if (cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&clip_kernel<N>), args) !=
+        cudaSuccess) {
+        cudaGetLastError();
+        return HEADLOSS_ERR_CUDA;
     }
+    return HEADLOSS_OK;
+}
+
+// The list of a call, put together on the host.
+struct Builder {
+    const headloss_gradient* g;
+    int n, used = 0;
+    uint64_t tiles = 0;
+    static uint64_t tiles_of(const headloss_gradient& t) {
+        const int es = t.dtype == HEADLOSS_FP32 ? 4 : 2, epw = 16 / es;
+        const int64_t head = int64_t(reinterpret_cast<uintptr_t>(t.grad) & 15) / es;
+        const uint64_t words = uint64_t(head + t.n + epw - 1) / epw;
+        return (words + TILE - 1) / TILE;
+    }
+    void count() {
+        for (int i = 0; i < n; ++i)
+            if (g[i].n) ++used, tiles += tiles_of(g[i]);
+    }
+    // calls f(entry) for every tensor that has elements
+    template <typename F>
+    void each(F f) const {
+        uint64_t at = 0;
+        for (int i = 0; i < n; ++i) {
+            if (!g[i].n) continue;
+            f(Entry{g[i].grad, g[i].out, g[i].n, uint32_t(at), g[i].dtype});
+            at += tiles_of(g[i]);
+        }
+    }
+};
+
+template <int N>
+int launch_list(const Builder& b, const Call& call, int grid, cudaStream_t s) {
+    static_assert(sizeof(List<N>) + sizeof(Call) <= 32764, "kernel arguments");
+    List<N> list;
+    int i = 0;
+    b.each([&](const Entry& e) { list.e[i++] = e; });
+    int at = 0;
+    for (int cta = 0; cta < grid; ++cta) {
+        const uint32_t t0 = uint32_t(b.tiles * cta / grid);
+        while (at + 1 < b.used && list.e[at + 1].first <= t0) ++at;
+        list.start[cta] = uint16_t(at);
+    }
+    return launch<N>(list, call, grid, s);
 }
 
 }  // namespace hl_clip
 
 struct headloss_clip {
     int max_grads = 0;
+    int grid = 0;  // CTAs that are resident at once
     void* ws = nullptr;
-    double* parts = nullptr;
+    hl_clip::Sync* sync = nullptr;
     hl_clip::Entry* list = nullptr;
 };
 
@@ -141,17 +480,28 @@ int headloss_clip_create(int max_grads, headloss_clip_t* out) {
     if (!out) return HEADLOSS_ERR_ARG;
     *out = nullptr;
     if (max_grads < 1 || max_grads > (1 << 24)) return HEADLOSS_ERR_ARG;
+    int device = 0, sms = 0, ctas = 0;
+    if (cudaGetDevice(&device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, clip_kernel<1>, THREADS, 0) !=
+            cudaSuccess ||
+        ctas < 1)
+        return HEADLOSS_ERR_CUDA;
     headloss_clip* h = new (std::nothrow) headloss_clip();
     if (!h) return HEADLOSS_ERR_ARG;
     h->max_grads = max_grads;
-    if (cudaMalloc(&h->ws, GRID * sizeof(double) + size_t(max_grads) * sizeof(Entry)) !=
-        cudaSuccess) {
+    h->grid = sms * (ctas < 2 ? ctas : 2);
+    if (h->grid > MAX_GRID) h->grid = MAX_GRID;
+    if (cudaMalloc(&h->ws, sizeof(Sync) + size_t(max_grads) * sizeof(Entry)) != cudaSuccess ||
+        cudaMemset(h->ws, 0, sizeof(Sync)) != cudaSuccess ||
+        cudaStreamSynchronize(nullptr) != cudaSuccess) {
         cudaGetLastError();
+        cudaFree(h->ws);
         delete h;
         return HEADLOSS_ERR_CUDA;
     }
-    h->parts = static_cast<double*>(h->ws);
-    h->list = reinterpret_cast<Entry*>(h->parts + GRID);
+    h->sync = static_cast<Sync*>(h->ws);
+    h->list = reinterpret_cast<Entry*>(h->sync + 1);
     *out = h;
     return HEADLOSS_OK;
 }
@@ -179,26 +529,33 @@ int headloss_clip_grads(headloss_clip_t h, const headloss_gradient* grads, int n
             return HEADLOSS_ERR_ALIGN;
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    int64_t chunks = 0;
-    int used = 0;
-    Batch b;
-    int in_batch = 0;
+    Builder b{grads, n_grads};
+    b.count();
+    if (b.tiles >= (uint64_t(1) << 32) - MAX_GRID * WARPS) return HEADLOSS_ERR_ARG;
+    Call call{b.used, uint32_t(b.tiles), double(max_norm), inv_scale, stats_out, h->sync};
+    // a warp a tile as far as the grid goes
+    const int64_t want = (int64_t(b.tiles) + WARPS - 1) / WARPS;
+    const int grid = int(want < 1 ? 1 : want < h->grid ? want : h->grid);
+    if (b.used <= 1) return launch_list<1>(b, call, grid, s);
+    if (b.used <= 64) return launch_list<64>(b, call, grid, s);
+    if (b.used <= 320) return launch_list<320>(b, call, grid, s);
+    if (b.used <= 960) return launch_list<960>(b, call, grid, s);
+    Batch batch;
+    int in_batch = 0, at = 0;
+    bool ok = true;
     auto flush = [&]() {
-        if (in_batch) list_kernel<<<1, 128, 0, s>>>(b, h->list, used - in_batch, in_batch);
+        if (in_batch) list_kernel<<<1, 256, 0, s>>>(batch, h->list, at, in_batch);
+        ok &= cudaGetLastError() == cudaSuccess;
+        at += in_batch;
         in_batch = 0;
     };
-    for (int i = 0; i < n_grads; ++i) {
-        if (grads[i].n == 0) continue;
-        b.e[in_batch++] = Entry{grads[i].grad, grads[i].out, grads[i].n, chunks, grads[i].dtype};
-        chunks += (grads[i].n + CHUNK - 1) / CHUNK;
-        ++used;
+    b.each([&](const Entry& e) {
+        batch.e[in_batch++] = e;
         if (in_batch == BATCH) flush();
-    }
+    });
     flush();
-    norm_kernel<<<GRID, THREADS, 0, s>>>(h->list, used, chunks, h->parts);
-    scale_kernel<<<GRID, THREADS, 0, s>>>(h->list, used, chunks, h->parts, max_norm, inv_scale,
-                                          stats_out);
-    return cudaGetLastError() == cudaSuccess ? HEADLOSS_OK : HEADLOSS_ERR_CUDA;
+    if (!ok) return HEADLOSS_ERR_CUDA;
+    return launch<0>(List<0>{h->list}, call, grid, s);
 }
 
 }  // extern "C"

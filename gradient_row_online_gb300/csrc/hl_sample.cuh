@@ -3,24 +3,28 @@
 //
 // One thread-block cluster a row, each CTA a contiguous run of the row's 16-byte
 // words in its shared memory, each warp a contiguous segment of that, copied by
-// the warp's own cp.async.bulk.  A logit is read from HBM once; every later pass
-// is over shared memory.  (Rows too long for eight CTAs' shared memory are read from
+// the warp's own cp.async.bulk.  A logit is read from HBM once; every pass is over
+// shared memory.  (Rows too long for eight CTAs' shared memory are read from
 // global memory in every pass: RES = false.)
 //
 // All three filters keep a prefix of the order (x descending, index ascending), so a
 // row's kept set is a cut in that order, and min-p's comparison.  Masses are integers
 // (2^30 the largest logit's): exact sums in any order, so atomics, splits and cluster
-// sizes never change a token.  A row goes one of three ways:
+// sizes never change a token.  After the exchange of the largest logit a row goes one of
+// these ways, each ending in the leader CTA while the others have left:
 //
-//   no top-k, no top-p   one pass sums the masses by warp segment.
-//   a small top-k        the k-th largest of the CTA's thread maxima bounds the cut from
-//                        below (at least k tokens lie at or above it); the few
-//                        tokens at or above the largest CTA's bound go to the leader CTA,
-//                        which ranks them and finishes the row alone.
-//   else                 `resolve`: a histogram of the order (1/32 octave of mass a bin) with
-//                        exact integer masses finds the bin of the cut, whose few tokens go to
-//                        the leader to be ranked; a bin with too many (ties, dense rows) is
-//                        cut into bins of keys again.  Then the segment masses of what is kept.
+//   no top-k, no top-p   every warp sums its segment's masses.
+//   a small top-k        a histogram of the thread maxima bounds the cut from below (as many
+//                        tokens as maxima lie above it); the few tokens above the bound are
+//                        ranked by the leader, which finishes the row alone.
+//   top-p                a histogram of the order (1/16 octave of mass a bin) with exact masses
+//                        finds the bin of the cut; the next pass sums the segments' masses in the
+//                        bins above it and sends the bin's few tokens to be ranked.
+//   else                 `resolve`: the same by count or mass within another cut, where a bin with
+//                        too many tokens (ties, dense rows) is cut into bins of keys again.
+//
+// The leader then knows the segment that holds the drawn target and goes over it once more
+// (from L2) for the token.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -30,6 +34,7 @@
 #include <atomic>
 
 #include "headloss.h"
+#include "hl_pack.cuh"
 #include "hl_rows.cuh"
 
 namespace hl_sample {
@@ -39,15 +44,16 @@ using hl::cluster_ctarank;
 using hl::map_peer;
 using hl::smem_addr;
 
-constexpr int THREADS = 512;
+constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
 constexpr int MAXC = 8;       // CTAs a cluster at most
 constexpr int BINS = 2 * THREADS;
-constexpr int CAP = 2048;     // tokens the leader can rank
-constexpr int RANKED = 512;   // ranked by comparison with all; more are sorted
-constexpr int MAX_TOPK = 256; // longest top-k that takes the thread-maxima bound
+constexpr int CAP = 1024;     // tokens the leader can rank
+constexpr int RANKED = 256;   // ranked by comparison with all; more are sorted
+constexpr int MAX_TOPK = 128; // longest top-k that takes the thread-maxima bound
+constexpr int SEGS = MAXC * WARPS;
+constexpr float PER_OCTAVE = 16.f;  // bins an octave of mass
 constexpr float UNIT = 1073741824.f;  // 2^30, the weight of the largest logit
-constexpr float MODEL_UNIT = 1099511627776.f;  // 2^40
 constexpr float LN2 = 0.69314718055994531f;
 constexpr unsigned FULL = 0xffffffffu;
 constexpr unsigned long long WAIT_NS = 2000000000ull;
@@ -56,6 +62,7 @@ struct Args {
     const void* logits;
     int64_t ld;
     int64_t row0;  // first row of this launch
+    int per;       // 16-byte words a CTA
     int V;
     const double* uniforms;
     const float* temperature;
@@ -74,22 +81,24 @@ typedef unsigned long long u64;
 
 struct Shared {
     u64 bar[WARPS];
-    u64 list[CAP];       // (key << 32 | ~index) of the tokens to rank, a run a CTA (leader)
+    u64 list[CAP];         // (key << 32 | ~index) of the tokens to rank, a run a CTA (leader)
     u64 sorted[RANKED];
-    u64 scratch[BINS];   // the list put together; the histogram's masses (hi, lo halves)
+    uint32_t hi[BINS];     // histogram: masses above and below bit 16, and counts; the
+    uint32_t lo[BINS];     // masses' space is also where the list is put together
     uint32_t cnt[BINS];
-    u64 xch[2][MAXC][4];
-    u64 red[WARPS];
-    u64 seg[WARPS];
-    u64 ored[WARPS];
-    float fred[WARPS];
+    u64 xch[2][MAXC];      // exchanges of one value a CTA
+    u64 seg_mass[SEGS];    // the segments' kept masses, the model's, and counts (leader)
+    u64 seg_model[SEGS];
+    uint32_t seg_kept[SEGS];
     uint32_t list_n[MAXC];
-    u64 list_own[MAXC];
+    u64 red[WARPS];
+    uint32_t ired[WARPS];
     uint32_t n_local;
-    uint32_t pick_bin, pick_n, pick_most;
-    u64 pick_before;
+    uint32_t pick_bin, pick_most;
+    u64 pick_before, pick_total;
     uint32_t cut_key;
     int cut_idx;
+    u64 fin[4];
 };
 
 // A cut of the order: tokens above the key stay, and at the key those up to an index.
@@ -97,7 +106,6 @@ struct Cut {
     uint32_t key;
     int idx;
 };
-constexpr Cut NO_CUT{0u, 0x7fffffff};
 
 // A key whose unsigned order is the order of the floats; -0 as +0.
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -213,11 +221,6 @@ __device__ __forceinline__ u64 warp_add(u64 v) {
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
     return v;
 }
-__device__ __forceinline__ float warp_add(float v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
-    return v;
-}
 __device__ __forceinline__ u64 warp_scan(u64 v, int lane) {  // inclusive
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -245,9 +248,9 @@ __device__ __forceinline__ void st_peer64(uint32_t addr, u64 v) {
 __device__ __forceinline__ void st_peer32(uint32_t addr, uint32_t v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-__device__ __forceinline__ uint32_t ld_peer32(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ uint2 ld_peer_pair(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
     return v;
 }
 __device__ __forceinline__ void cluster_arrive() {
@@ -261,6 +264,13 @@ __device__ __forceinline__ void cluster_barrier() {
     __syncwarp();
     hl::cluster_barrier();
 }
+// The last barrier of a row: the leader waits, the other CTAs need not (their shared memory is
+// read by no one after the barrier before).
+__device__ __forceinline__ void cluster_barrier_or_leave(int rank) {
+    __syncwarp();
+    cluster_arrive();
+    if (rank == 0) cluster_wait();
+}
 
 // -------------------------------------------------------------------- a row ----
 
@@ -268,6 +278,7 @@ template <typename DT, bool CAPPED, bool RES>
 struct Row {
     using E = Elem<DT>;
     static constexpr int EPW = E::EPW;
+    static constexpr int PAIRS = EPW / 2;
 
     const Args& a;
     Shared& s;
@@ -305,38 +316,58 @@ struct Row {
         if constexpr (RES) return words[i];
         else return global_word(w0 + i);
     }
-    __device__ __forceinline__ void values(int i, float* v) const {
-        E::unpack(word(i), v);
-        if constexpr (!RES) {
-            if (inf_row)
-                for (int e = 0; e < EPW; ++e) v[e] = v[e] == CUDART_INF_F ? 0.f : -CUDART_INF_F;
-        }
+    // Of a row whose largest logit is +inf (no softcap): the tokens at +inf share the mass
+    // alike, all others have none.
+    __device__ __forceinline__ void unpack(const uint4& w, float* v, bool mapped) const {
+        E::unpack(w, v);
+        if (mapped && inf_row)
+            for (int e = 0; e < EPW; ++e) v[e] = v[e] == CUDART_INF_F ? 0.f : -CUDART_INF_F;
     }
+    __device__ __forceinline__ void values(int i, float* v) const { unpack(word(i), v, !RES); }
 
     __device__ __forceinline__ float z(float v) const {
         if constexpr (CAPPED) return __fmul_rn(tanhf(__fmul_rn(v, a.inv_cap)), a.cap);
         else return v;
     }
-    // Exponent and mass share of a logit.  Without a softcap -inf and NaN give 0 mass by
-    // themselves.
+    // Exponents of a word's logits, and their mass shares; -inf and NaN have none.  A NaN's share
+    // is NaN without a softcap, which makes the weight 0.
+    __device__ __forceinline__ void shares(const float* v, hl::f2* d, float* sh) const {
+        const hl::f2 nz = hl::pk1(-zm), cc = hl::pk1(c);
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) {
+            d[i] = hl::mul2(hl::add2(hl::pk(z(v[2 * i]), z(v[2 * i + 1])), nz), cc);
+            float x, y;
+            hl::upk(d[i], x, y);
+            sh[2 * i] = ex2f(x), sh[2 * i + 1] = ex2f(y);
+            if constexpr (CAPPED) {
+                if (!(v[2 * i] > -CUDART_INF_F)) sh[2 * i] = 0.f;
+                if (!(v[2 * i + 1] > -CUDART_INF_F)) sh[2 * i + 1] = 0.f;
+            }
+        }
+    }
+    __device__ __forceinline__ void weights(const float* sh, uint32_t* w) const {
+        const hl::f2 unit = hl::pk1(UNIT);
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) {
+            float x, y;
+            hl::upk(hl::mul2(hl::pk(sh[2 * i], sh[2 * i + 1]), unit), x, y);
+            w[2 * i] = __float2uint_rn(x), w[2 * i + 1] = __float2uint_rn(y);
+        }
+    }
     __device__ __forceinline__ float share(float v) const {
         const float e = ex2f(__fmul_rn(__fsub_rn(z(v), zm), c));
         if constexpr (CAPPED) return v > -CUDART_INF_F ? e : 0.f;
         else return e;
     }
-    // The same where +inf may stand (ranked tokens of a row that was not rewritten).
+    // The exponent where +inf may stand.
     __device__ __forceinline__ float exponent(float v) const {
         const float zz = z(v);
         return zz == zm ? 0.f : __fmul_rn(__fsub_rn(zz, zm), c);
     }
-    __device__ __forceinline__ float model_share(float v) const {
-        const float e = ex2f(__fmul_rn(__fsub_rn(z(v), zm), a.K));
-        if constexpr (CAPPED) return v > -CUDART_INF_F ? e : 0.f;
-        else return e;
-    }
+
     // Mass of the whole softmax at T = 1: a word's shares summed in fp32 in one order, the words
-    // in fixed point (2^-40 of the largest logit's), so that it too is the same
-    // however the row is split.
+    // in fixed point (2^-39 of the largest logit's; 2^-28 for a word above 2^-8), so
+    // that it too is the same however the row is split.
     struct Model {
         u64 sum = 0;
         bool odd = false;  // a word with a NaN (or +inf)
@@ -345,14 +376,25 @@ struct Row {
             if constexpr (EPW == 8)
                 t = ((sh[0] + sh[1]) + (sh[2] + sh[3])) + ((sh[4] + sh[5]) + (sh[6] + sh[7]));
             else t = (sh[0] + sh[1]) + (sh[2] + sh[3]);
-            odd |= !(t < 16.f);
-            sum += __float2ull_rn(__fmul_rn(t, MODEL_UNIT));
+            odd |= !(t < 15.f);
+            const bool small = t < 0x1p-8f;
+            const uint32_t n = __float2uint_rn(__fmul_rn(t, small ? 0x1p+39f : 0x1p+28f));
+            sum += small ? u64(n) : u64(n) << 11;
         }
     };
     __device__ __forceinline__ void add_model(Model& m, const float* v) const {
+        const hl::f2 nz = hl::pk1(-zm), kk = hl::pk1(a.K);
         float sh[EPW];
 #pragma unroll
-        for (int e = 0; e < EPW; ++e) sh[e] = model_share(v[e]);
+        for (int i = 0; i < PAIRS; ++i) {
+            float x, y;
+            hl::upk(hl::mul2(hl::add2(hl::pk(z(v[2 * i]), z(v[2 * i + 1])), nz), kk), x, y);
+            sh[2 * i] = ex2f(x), sh[2 * i + 1] = ex2f(y);
+            if constexpr (CAPPED) {
+                if (!(v[2 * i] > -CUDART_INF_F)) sh[2 * i] = 0.f;
+                if (!(v[2 * i + 1] > -CUDART_INF_F)) sh[2 * i + 1] = 0.f;
+            }
+        }
         m.add(sh);
     }
     // The warp's sum; words with a NaN or +inf are gone over again with care.
@@ -374,26 +416,21 @@ struct Row {
         return warp_add(m.sum);
     }
 
-    // Bin of the order: 1/32 octave of mass a bin without a softcap (with one, of the raw
+    // Bin of the order: 1/16 octave of mass a bin without a softcap (with one, of the raw
     // logit's distance); the last takes what is further off.
     __device__ __forceinline__ uint32_t bin_of(float v) const {
         return min(uint32_t(BINS - 1),
-                   __float2uint_rz(__fmul_rn(__fmul_rn(__fsub_rn(top, v), c), 32.f)));
+                   __float2uint_rn(__fmul_rn(__fmul_rn(__fsub_rn(top, v), c), PER_OCTAVE)));
     }
     __device__ __forceinline__ bool inside(float v, int idx, const Cut& k, float kv) const {
         return v > kv || (v == kv && idx <= k.idx);
     }
 
-    // Every CTA's NV values (in warp 0's lanes, all alike) at every CTA.
-    template <int NV>
-    __device__ const u64 (*exchange(const u64 (&v)[NV]))[4] {
-        if (warp == 0 && lane < C) {
-            const uint32_t at = map_peer(smem_addr(&s.xch[par][rank][0]), lane);
-#pragma unroll
-            for (int i = 0; i < NV; ++i) st_peer64(at + 8 * i, v[i]);
-        }
+    // Every CTA's value (of warp 0's lanes, all alike) at every CTA.
+    __device__ const u64* exchange(u64 v) {
+        if (warp == 0 && lane < C) st_peer64(map_peer(smem_addr(&s.xch[par][rank]), lane), v);
         cluster_barrier();
-        const u64(*got)[4] = s.xch[par];
+        const u64* got = s.xch[par];
         par ^= 1;
         return got;
     }
@@ -404,14 +441,14 @@ struct Row {
         if (a.draw_logprobs) a.draw_logprobs[row] = 0.f;
         if (a.n_kept) a.n_kept[row] = 0;
     }
-    __device__ void answer(float v, int idx, u64 W, u64 own, int kept) const {
+    __device__ void answer(float v, int idx, u64 W, u64 model, int kept) const {
         a.tokens[row] = idx;
         const float zz = z(v);
         if (a.logprobs)
             a.logprobs[row] = (zz == zm ? 0.f : __fsub_rn(zz, zm) * a.K * LN2) -
-                              logf(float(double(own) * (1.0 / MODEL_UNIT)));
+                              logf(float(double(model) * 0x1p-39));
         if (a.draw_logprobs)
-            a.draw_logprobs[row] = exponent(v) * LN2 - logf(float(double(W) * (1.0 / UNIT)));
+            a.draw_logprobs[row] = exponent(v) * LN2 - logf(float(double(W) * 0x1p-30));
         if (a.n_kept) a.n_kept[row] = kept;
     }
     __device__ static u64 target_of(double u, u64 W) {
@@ -428,14 +465,11 @@ struct Row {
             st_peer64(map_peer(smem_addr(&s.list[rank * (CAP / C) + at]), 0),
                       (u64(key_of(v)) << 32) | uint32_t(~idx));
     }
-    // After the appends and a block barrier: the CTA's count (and model mass) to the leader.
-    __device__ void send_counts(u64 own) {
-        if (threadIdx.x == 0) {
-            st_peer32(map_peer(smem_addr(&s.list_n[rank]), 0), s.n_local);
-            st_peer64(map_peer(smem_addr(&s.list_own[rank]), 0), own);
-        }
+    // After the appends and a block barrier: the CTA's count to the leader.
+    __device__ void send_count() {
+        if (threadIdx.x == 0) st_peer32(map_peer(smem_addr(&s.list_n[rank]), 0), s.n_local);
     }
-    // Leader: the runs in order, descending; false where a run overflowed.
+    // Leader: the runs put together, descending.
     __device__ const u64* rank_list(int* n_out) {
         const int run = CAP / C;
         int n = 0;
@@ -447,12 +481,14 @@ struct Row {
             return s.list[r * run + i];
         };
         if (n <= RANKED) {
+            u64* all = reinterpret_cast<u64*>(s.hi);
             const u64 mine = int(threadIdx.x) < n ? at(threadIdx.x) : 0;
-            if (int(threadIdx.x) < n) s.scratch[threadIdx.x] = mine;
+            if (int(threadIdx.x) < n) all[threadIdx.x] = mine;
             __syncthreads();
             if (int(threadIdx.x) < n) {
                 int better = 0;
-                for (int j = 0; j < n; ++j) better += s.scratch[j] > mine;
+#pragma unroll 4
+                for (int j = 0; j < n; ++j) better += all[j] > mine;
                 s.sorted[better] = mine;
             }
             __syncthreads();
@@ -482,118 +518,211 @@ struct Row {
         return s.list;
     }
 
-    // -------------------------------------------------------- small top-k ----
-
-    // Top-16 bits of the k-th largest thread maximum's key: at least k of the CTA's
-    // tokens are at or above it.
-    __device__ uint32_t bound_of(float mine, int k) const {
-        const uint32_t key = key_of(mine);
-        uint32_t at = 0;
-        for (int b = 31; b >= 16; --b) {
-            const uint32_t next = at | (1u << b);
-            if (__syncthreads_count(key >= next) >= k) at = next;
+    // Two bins' joined histogram entries, of the thread.
+    __device__ __forceinline__ void join_counts(u64* n, uint32_t* most) const {
+        n[0] = n[1] = 0;
+        most[0] = most[1] = 0;
+        for (int r = 0; r < C; ++r) {
+            const uint2 x = ld_peer_pair(map_peer(smem_addr(&s.cnt[2 * threadIdx.x]), r));
+            n[0] += x.x, n[1] += x.y;
+            most[0] = max(most[0], x.x), most[1] = max(most[1], x.y);
         }
-        return at;
+    }
+    // `most`: a CTA's largest mass in the bin, rounded up to 2^16.
+    __device__ __forceinline__ void join_masses(u64* m, uint32_t* most) const {
+        m[0] = m[1] = 0;
+        most[0] = most[1] = 0;
+        for (int r = 0; r < C; ++r) {
+            const uint2 x = ld_peer_pair(map_peer(smem_addr(&s.hi[2 * threadIdx.x]), r));
+            const uint2 y = ld_peer_pair(map_peer(smem_addr(&s.lo[2 * threadIdx.x]), r));
+            const u64 m0 = (u64(x.x) << 16) + y.x, m1 = (u64(x.y) << 16) + y.y;
+            m[0] += m0, m[1] += m1;
+            most[0] = max(most[0], uint32_t((m0 + 0xffff) >> 16));
+            most[1] = max(most[1], uint32_t((m1 + 0xffff) >> 16));
+        }
+    }
+    // The bin that the target (a count, or `p` times the total) falls in, what lies before
+    // it (over `before`), its `most`; BINS where the target is past them all.  Whole block.
+    __device__ void pick(const u64* m, const uint32_t* most, bool by_mass, double p, double* target,
+                         bool first, u64 before) {
+        if (threadIdx.x == 0) s.pick_bin = BINS;
+        u64 total;
+        u64 at = before + block_scan(m[0] + m[1], s.red, &total);
+        if (first) *target = by_mass ? p * double(total) : p;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            // a target of 0 keeps the first token all the same
+            const bool starts = double(at) < *target || at == 0;
+            if (m[q] && starts && double(at + m[q]) >= *target) {
+                s.pick_bin = 2 * threadIdx.x + q;
+                s.pick_most = most[q];
+                s.pick_before = at;
+            }
+            at += m[q];
+        }
+        __syncthreads();
     }
 
-    // The tokens at or above `bound` to the leader, and the row finished there.  False (in
+    // -------------------------------------------------------- small top-k ----
+
+    // A bound from below of the k-th largest logit: the bin where the histogram of the
+    // cluster's thread maxima reaches k.
+    __device__ float bound_of(float mine, int k) {
+        if (mine > -CUDART_INF_F) atomicAdd(&s.cnt[bin_of(mine)], 1u);
+        cluster_barrier();
+        u64 n[2];
+        uint32_t most[2];
+        join_counts(n, most);
+        double target;
+        pick(n, most, false, double(k), &target, true, 0);
+        const uint32_t bin = s.pick_bin;
+        if (bin >= BINS - 1) return -CUDART_INF_F;
+        // distances of the bin lie below (bin + 1/2) / 16 c; a little more for the roundings
+        const float far = __fmul_ru(__fdiv_ru(float(bin) + 0.5f, __fmul_rd(c, PER_OCTAVE)), 1.00001f);
+        return __fsub_rd(top, far);
+    }
+
+    // The tokens at or above `from` to the leader, and the row finished there.  False (in
     // every CTA) where they are too many.
-    __device__ bool few(uint32_t bound, int k, float p, float least, double u) {
-        const float from = bound > KEY_NONE ? of_key(bound) : -CUDART_INF_F;
-        if (threadIdx.x == 0) s.n_local = 0;
-        __syncthreads();
-        Model model;
+    __device__ bool few(float from, int k, float p, float least, double u) {
         const bool want = a.logprobs != nullptr;
+        Model model;
         for (int i = s0 + lane; i < s1; i += 32) {
             const uint4 w = word(i);
-            if (want || E::top(E::word_max(w)) >= from) {
+            const bool any = E::top(E::word_max(w)) >= from;
+            if (want || any) {
                 float v[EPW];
                 E::unpack(w, v);
                 if (want) add_model(model, v);
-                if (E::top(E::word_max(w)) >= from)
+                if (any)
                     for (int e = 0; e < EPW; ++e)
                         if (v[e] >= from && v[e] > -CUDART_INF_F) append(v[e], index(i, e));
             }
         }
-        u64 own = want ? model_sum(model) : 0;
-        if (lane == 0) s.ored[warp] = own;
+        const u64 mine_model = want ? model_sum(model) : 0;
+        if (lane == 0) st_peer64(map_peer(smem_addr(&s.seg_model[rank * WARPS + warp]), 0), mine_model);
         __syncthreads();
-        own = 0;
-        for (int i = 0; i < WARPS; ++i) own += s.ored[i];
-        send_counts(own);
-        const u64 count[1] = {s.n_local};
-        const u64(*all)[4] = exchange(count);
-        for (int r = 0; r < C; ++r)
-            if (all[r][0] > u64(CAP / C)) return false;
+        send_count();
+        const u64* all = exchange(s.n_local);
+        if (__any_sync(FULL, lane < C && all[lane] > u64(CAP / C))) return false;
         if (rank) return true;
 
         int n;
         const u64* sorted = rank_list(&n);
         k = min(k, n);
         const int t = threadIdx.x;
+        if (t >= MAX_TOPK) return true;  // (warps beyond: nothing left to rank)
         const u64 mine = t < k ? sorted[t] : 0;
         const float v = of_key(uint32_t(mine >> 32));
         const int idx = int(~uint32_t(mine));
         const float e = t < k ? ex2f(exponent(v)) : 0.f;
         uint32_t w = t < k ? weight_of(e) : 0u;
-        u64 W;
-        const u64 before = block_scan(w, s.red, &W);
+        // mass before it in the order, over the first warps
+        constexpr int RW = MAX_TOPK / 32;
+        u64 before = warp_scan(w, lane), W = 0;
+        if (lane == 31) s.red[warp] = before;
+        named_barrier();
+        before -= w;
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+            if (i < warp) before += s.red[i];
+            W += s.red[i];
+        }
         if (p < 1.f && t > 0 && !(double(before) < double(p) * double(W))) w = 0;
         if (!(e >= least)) w = 0;
         // the kept masses by index
-        block_scan((u64(w > 0) << 48) + w, s.seg, &W);
+        u64* by_index = reinterpret_cast<u64*>(s.hi);
+        if (t < k) by_index[t] = (u64(uint32_t(idx)) << 32) | w;
+        const u64 part = warp_add((u64(w > 0) << 48) + w);
+        if (lane == 0) s.seg_mass[warp] = part;
+        named_barrier();
+        W = 0;
+#pragma unroll
+        for (int i = 0; i < RW; ++i) W += s.seg_mass[i];
         const int kept = int(W >> 48);
         W &= (u64(1) << 48) - 1;
-        if (t < k) s.scratch[t] = (u64(uint32_t(idx)) << 32) | w;
-        __syncthreads();
         if (w) {
             u64 lower = 0;
+#pragma unroll 4
             for (int j = 0; j < k; ++j) {
-                const u64 o = s.scratch[j];
+                const u64 o = by_index[j];
                 if (int(o >> 32) < idx) lower += uint32_t(o);
             }
             const u64 at = target_of(u, W);
             if (at >= lower && at < lower + w) {
-                u64 all_own = 0;
-                for (int r = 0; r < C; ++r) all_own += s.list_own[r];
-                answer(v, idx, W, all_own, kept);
+                u64 all_model = 0;
+                for (int i = 0; i < C * WARPS; ++i) all_model += s.seg_model[i];
+                answer(v, idx, W, all_model, kept);
             }
         }
         return true;
     }
+    __device__ static void named_barrier() {
+        asm volatile("bar.sync 1, %0;" ::"n"(MAX_TOPK) : "memory");
+    }
 
     // ------------------------------------------------------------ the cut ----
 
+    __device__ void clear_histogram() {
+        for (int i = threadIdx.x; i < BINS; i += THREADS) s.cnt[i] = 0, s.hi[i] = 0, s.lo[i] = 0;
+    }
+    __device__ __forceinline__ void add_bin(uint32_t b, uint32_t w) {
+        atomicAdd(&s.hi[b], w >> 16);
+        atomicAdd(&s.lo[b], w & 0xffffu);
+    }
+
+    // The histogram of masses of all tokens; the model's mass on the way where `model` is
+    // given.  Without a softcap the bin comes from the exponent: 2^23 - 16 d rounds to it.
+    __device__ void histogram(Model* model) {
+        const bool same = c == a.K;
+        const hl::f2 slope = hl::pk1(-PER_OCTAVE), magic = hl::pk1(8388608.f);
+        for (int i = s0 + lane; i < s1; i += 32) {
+            float v[EPW], sh[EPW];
+            hl::f2 d[PAIRS];
+            uint32_t w[EPW];
+            values(i, v);
+            shares(v, d, sh);
+            if (model) {
+                if (same) model->add(sh);
+                else add_model(*model, v);
+            }
+            weights(sh, w);
+#pragma unroll
+            for (int j = 0; j < PAIRS; ++j) {
+                uint32_t b[2];
+                if constexpr (CAPPED) {
+                    b[0] = bin_of(v[2 * j]), b[1] = bin_of(v[2 * j + 1]);
+                } else {
+                    float x, y;
+                    hl::upk(hl::fma2(d[j], slope, magic), x, y);
+                    b[0] = __float_as_uint(x) - 0x4b000000u, b[1] = __float_as_uint(y) - 0x4b000000u;
+                }
+                if (w[2 * j]) add_bin(b[0], w[2 * j]);
+                if (w[2 * j + 1]) add_bin(b[1], w[2 * j + 1]);
+            }
+        }
+    }
+
     // The cut after the first tokens of the order, among those inside `within`, before which
-    // the count is below k (by_mass = false) or the mass below p times theirs.  The histograms
-    // hold the tokens with a mass alone: one without is never drawn.
-    // Collective over the cluster.  Model mass is summed on the way where own is given.
-    __device__ Cut resolve(bool by_mass, int64_t k, float p, const Cut& within, u64* own) {
+    // the count is below k (by_mass = false) or the mass below p times theirs.  Tokens
+    // without a mass are left out: they are never drawn.  Collective over the cluster.
+    __device__ Cut resolve(bool by_mass, int k, float p, const Cut& within) {
         const float wv = of_key(within.key);
         const bool all = within.key == 0u;
-        uint32_t* hi = reinterpret_cast<uint32_t*>(s.scratch);
-        uint32_t* lo = hi + BINS;
         u64 before = 0;
         double target = 0.0;
         uint32_t bin = 0, k0 = 0, k1 = 0;  // after level 0: keys k0 <= key <= k1
         int shift = 0;
         bool ties = false;
         for (int level = 0;; ++level) {
-            for (int i = threadIdx.x; i < BINS; i += THREADS) s.cnt[i] = 0, hi[i] = 0, lo[i] = 0;
+            cluster_barrier();  // the last histogram's readers are done
+            clear_histogram();
             __syncthreads();
-            Model model;
             for (int i = s0 + lane; i < s1; i += 32) {
-                float v[EPW], sh[EPW];
+                float v[EPW];
                 values(i, v);
-#pragma unroll
-                for (int e = 0; e < EPW; ++e) sh[e] = share(v[e]);
-                if (level == 0 && own) {
-                    if (c == a.K) model.add(sh);
-                    else add_model(model, v);
-                }
-#pragma unroll
                 for (int e = 0; e < EPW; ++e) {
-                    const uint32_t w = weight_of(sh[e]);
+                    const uint32_t w = weight_of(share(v[e]));
                     if (!w || !(all || inside(v[e], index(i, e), within, wv))) continue;
                     uint32_t b;
                     if (level == 0) {
@@ -604,49 +733,16 @@ struct Row {
                         b = (k1 - key) >> shift;
                     }
                     atomicAdd(&s.cnt[b], 1u);
-                    if (by_mass) {
-                        atomicAdd(&hi[b], w >> 16);
-                        atomicAdd(&lo[b], w & 0xffffu);
-                    }
+                    if (by_mass) add_bin(b, w);
                 }
             }
-            if (level == 0 && own) *own = model_sum(model);
             cluster_barrier();
-            // every CTA joins all histograms, two bins a thread
-            u64 m[2] = {0, 0};
-            uint32_t n[2] = {0, 0}, most[2] = {0, 0};
-            for (int r = 0; r < C; ++r) {
-                const uint32_t pc = map_peer(smem_addr(&s.cnt[2 * threadIdx.x]), r);
-                const uint32_t ph = map_peer(smem_addr(&hi[2 * threadIdx.x]), r);
-                const uint32_t pl = map_peer(smem_addr(&lo[2 * threadIdx.x]), r);
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const uint32_t x = ld_peer32(pc + 4 * q);
-                    n[q] += x;
-                    most[q] = max(most[q], x);
-                    if (by_mass)
-                        m[q] += (u64(ld_peer32(ph + 4 * q)) << 16) + ld_peer32(pl + 4 * q);
-                }
-            }
-            if (!by_mass) m[0] = n[0], m[1] = n[1];
-            u64 total;
-            u64 at = before + block_scan(m[0] + m[1], s.red, &total);
-            if (level == 0) target = by_mass ? double(p) * double(total) : double(k);
-            if (threadIdx.x == 0) s.pick_bin = BINS;
-            __syncthreads();
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                // the first bin with a token that the target does not pass
-                const bool starts = double(at) < target || (at == before && n[q] && before == 0);
-                if (n[q] && starts && double(at + m[q]) >= target) {
-                    s.pick_bin = 2 * threadIdx.x + q;
-                    s.pick_n = n[q];
-                    s.pick_most = most[q];
-                    s.pick_before = at;
-                }
-                at += m[q];
-            }
-            __syncthreads();
+            u64 n[2], m[2];
+            uint32_t most[2], unused[2];
+            join_counts(n, most);
+            if (by_mass) join_masses(m, unused);
+            pick(by_mass ? m : n, most, by_mass, by_mass ? double(p) : double(k), &target, level == 0,
+                 before);
             bin = s.pick_bin;
             if (bin == BINS) {  // the target is past all of them
                 cluster_barrier();
@@ -670,23 +766,22 @@ struct Row {
                     }
                 }
                 least = __reduce_min_sync(FULL, least), largest = __reduce_max_sync(FULL, largest);
+                __syncthreads();
                 if (lane == 0) s.red[warp] = (u64(~least) << 32) | largest;
                 __syncthreads();
                 for (int i = 0; i < WARPS; ++i)
                     least = min(least, ~uint32_t(s.red[i] >> 32)),
                     largest = max(largest, uint32_t(s.red[i]));
-                const u64 mine[1] = {(u64(~least) << 32) | largest};
-                const u64(*got)[4] = exchange(mine);
+                const u64* got = exchange((u64(~least) << 32) | largest);
                 for (int r = 0; r < C; ++r)
-                    least = min(least, ~uint32_t(got[r][0] >> 32)),
-                    largest = max(largest, uint32_t(got[r][0]));
+                    least = min(least, ~uint32_t(got[r] >> 32)),
+                    largest = max(largest, uint32_t(got[r]));
                 k0 = least, k1 = largest;
             } else {
                 k1 = k1 - (bin << shift);
                 const uint32_t span = (1u << shift) - 1;
                 k0 = k1 - k0 > span ? k1 - span : k0;
                 if (some <= uint32_t(CAP / C)) break;
-                cluster_barrier();
             }
             if (k0 == k1) {
                 ties = true;
@@ -698,12 +793,12 @@ struct Row {
         const bool by_bin = k1 == 0;
 
         if (!ties) {
+            __syncthreads();
             if (threadIdx.x == 0) s.n_local = 0;
             __syncthreads();
             for (int i = s0 + lane; i < s1; i += 32) {
                 float v[EPW];
                 values(i, v);
-#pragma unroll
                 for (int e = 0; e < EPW; ++e) {
                     bool in;
                     if (by_bin) in = bin_of(v[e]) == bin;
@@ -714,31 +809,15 @@ struct Row {
                 }
             }
             __syncthreads();
-            send_counts(0);
+            send_count();
             cluster_barrier();
             if (rank == 0) {
                 int n;
                 const u64* sorted = rank_list(&n);
-                u64 w[CAP / THREADS], mine = 0;
-                const int i0 = threadIdx.x * (CAP / THREADS);
-#pragma unroll
-                for (int q = 0; q < CAP / THREADS; ++q) {
-                    w[q] = i0 + q < n ? (by_mass ? weight_of(share(of_key(uint32_t(sorted[i0 + q] >> 32)))) : 1u) : 0u;
-                    mine += w[q];
-                }
-                u64 total;
-                u64 at = before + block_scan(mine, s.red, &total);
-                u64 stay = 0;
-#pragma unroll
-                for (int q = 0; q < CAP / THREADS; ++q) {
-                    stay += i0 + q < n && (double(at) < target || (at == 0 && i0 + q == 0));
-                    at += w[q];
-                }
-                block_scan(stay, s.red, &total);
-                const u64 last = sorted[total - 1];
+                const Cut cut = cut_of(sorted, n, by_mass, before, target);
                 if (warp == 0 && lane < C) {
-                    st_peer32(map_peer(smem_addr(&s.cut_key), lane), uint32_t(last >> 32));
-                    st_peer32(map_peer(smem_addr(&s.cut_idx), lane), ~uint32_t(last));
+                    st_peer32(map_peer(smem_addr(&s.cut_key), lane), cut.key);
+                    st_peer32(map_peer(smem_addr(&s.cut_idx), lane), uint32_t(cut.idx));
                 }
             }
             cluster_barrier();
@@ -769,15 +848,15 @@ struct Row {
         }
         mine = __reduce_add_sync(FULL, mine);
         __syncthreads();
-        if (lane == 0) s.seg[warp] = mine;
+        if (lane == 0) s.red[warp] = mine;
         __syncthreads();
-        u64 lower = 0, count[1] = {0};
+        u64 lower = 0, count = 0;
         for (int i = 0; i < WARPS; ++i) {
-            if (i < warp) lower += s.seg[i];
-            count[0] += s.seg[i];
+            if (i < warp) lower += s.red[i];
+            count += s.red[i];
         }
-        const u64(*got)[4] = exchange(count);
-        for (int r = 0; r < rank; ++r) lower += got[r][0];
+        const u64* got = exchange(count);
+        for (int r = 0; r < rank; ++r) lower += got[r];
         if (stay > lower && stay <= lower + mine) {
             for (int i = s0; i < s1; i += 32) {
                 float v[EPW];
@@ -806,98 +885,195 @@ struct Row {
         return Cut{k0, s.cut_idx};
     }
 
-    // ----------------------------------------------------------- the draw ----
-
-    // Mass of the logit as the cut and min-p leave it.
-    template <bool CUTS>
-    __device__ __forceinline__ uint32_t kept_mass(float v, float sh, int idx, const Cut& cut,
-                                                  float kv, float least) const {
-        uint32_t w = weight_of(sh);
-        if constexpr (CUTS) {
-            if (!(sh >= least && inside(v, idx, cut, kv))) w = 0;
+    // Leader: the last of a ranked list's tokens that stay (whole block).
+    __device__ Cut cut_of(const u64* sorted, int n, bool by_mass, u64 before, double target) {
+        constexpr int Q = CAP / THREADS;
+        u64 w[Q], mine = 0;
+        const int i0 = threadIdx.x * Q;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            w[q] = 0;
+            if (i0 + q < n)
+                w[q] = by_mass ? weight_of(share(of_key(uint32_t(sorted[i0 + q] >> 32)))) : 1u;
+            mine += w[q];
         }
-        return w;
+        u64 total;
+        u64 at = before + block_scan(mine, s.red, &total);
+        u64 stay = 0;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            stay += i0 + q < n && (double(at) < target || (at == 0 && i0 + q == 0));
+            at += w[q];
+        }
+        block_scan(stay, s.red, &total);
+        const u64 last = sorted[total - 1];
+        return Cut{uint32_t(last >> 32), int(~uint32_t(last))};
     }
 
-    // Masses by segment, the target's segment, the token.  OWN: the model's mass is summed on
-    // the way (else own is the warp's already).
-    template <bool CUTS>
-    __device__ void draw(const Cut& cut, float least, double u, u64 own, bool sum_own) {
-        const float kv = of_key(cut.key);
-        const float kvc = cut.key ? kv : -CUDART_INF_F;
-        u64 mass = 0;
-        uint32_t kept = 0;
-        Model model;
-        const bool same = c == a.K;
-        for (int i = s0 + lane; i < s1; i += 32) {
-            float v[EPW], sh[EPW];
-            values(i, v);
-#pragma unroll
-            for (int e = 0; e < EPW; ++e) sh[e] = share(v[e]);
-            if (sum_own) {
-                if (same) model.add(sh);
-                else add_model(model, v);
-            }
-#pragma unroll
-            for (int e = 0; e < EPW; e += 2) {
-                const uint32_t wa = kept_mass<CUTS>(v[e], sh[e], index(i, e), cut, kvc, least);
-                const uint32_t wb =
-                    kept_mass<CUTS>(v[e + 1], sh[e + 1], index(i, e + 1), cut, kvc, least);
-                mass += wa + wb;  // at most 2^31 and a little
-                kept += (wa != 0) + (wb != 0);
-            }
-        }
+    // ----------------------------------------------------------- the draw ----
+
+    // A segment's sums to the leader.
+    __device__ void send_segment(u64 mass, uint32_t kept, u64 model) {
         mass = warp_add(mass);
         kept = __reduce_add_sync(FULL, kept);
-        if (sum_own) own = model_sum(model);
-        __syncthreads();
-        if (lane == 0) s.seg[warp] = mass, s.red[warp] = kept, s.ored[warp] = own;
-        __syncthreads();
-        u64 lower = 0, cta[3] = {0, 0, 0};
-        for (int i = 0; i < WARPS; ++i) {
-            if (i < warp) lower += s.seg[i];
-            cta[0] += s.seg[i], cta[1] += s.red[i], cta[2] += s.ored[i];
+        if (lane == 0) {
+            const int g = rank * WARPS + warp;
+            st_peer64(map_peer(smem_addr(&s.seg_mass[g]), 0), mass);
+            st_peer32(map_peer(smem_addr(&s.seg_kept[g]), 0), kept);
+            st_peer64(map_peer(smem_addr(&s.seg_model[g]), 0), model);
         }
-        const u64(*got)[4] = exchange(cta);
-        u64 W = 0, all_own = 0;
-        int all_kept = 0;
-        for (int r = 0; r < C; ++r) {
-            if (r < rank) lower += got[r][0];
-            W += got[r][0], all_kept += int(got[r][1]);
-            all_own += got[r][2];
+    }
+
+    // No filter: the masses of everything.
+    __device__ void sum_all(bool want, u64 model) {
+        const bool same = c == a.K;
+        Model m;
+        u64 mass = 0;
+        uint32_t kept = 0;
+        for (int i = s0 + lane; i < s1; i += 32) {
+            float v[EPW], sh[EPW];
+            hl::f2 d[PAIRS];
+            uint32_t w[EPW];
+            values(i, v);
+            shares(v, d, sh);
+            if (want) {
+                if (same) m.add(sh);
+                else add_model(m, v);
+            }
+            weights(sh, w);
+#pragma unroll
+            for (int j = 0; j < EPW; j += 2) {
+                mass += w[j] + w[j + 1];  // at most 2^31 and a little
+                kept += min(w[j], 1u) + min(w[j + 1], 1u);
+            }
         }
-        const u64 t = target_of(u, W);
-        if (t < lower || t >= lower + mass) return;
-        for (int i = s0; i < s1; i += 32) {
+        send_segment(mass, kept, want ? model_sum(m) : model);
+    }
+
+    // The masses of what the cut and min-p leave.
+    __device__ void sum_kept(const Cut& cut, float least, bool want, u64 model) {
+        const float kv = cut.key ? of_key(cut.key) : -CUDART_INF_F;
+        const bool same = c == a.K;
+        Model m;
+        u64 mass = 0;
+        uint32_t kept = 0;
+        for (int i = s0 + lane; i < s1; i += 32) {
+            float v[EPW], sh[EPW];
+            hl::f2 d[PAIRS];
+            uint32_t w[EPW];
+            values(i, v);
+            shares(v, d, sh);
+            if (want) {
+                if (same) m.add(sh);
+                else add_model(m, v);
+            }
+            weights(sh, w);
+#pragma unroll
+            for (int e = 0; e < EPW; ++e) {
+                const bool in = sh[e] >= least && inside(v[e], index(i, e), cut, kv) && w[e];
+                mass += in ? w[e] : 0u;
+                kept += in;
+            }
+        }
+        send_segment(mass, kept, want ? model_sum(m) : model);
+    }
+
+    // The masses of the bins above `bin` (and of min-p), the bin's tokens to the leader.
+    __device__ void sum_above(uint32_t bin, float least, u64 model) {
+        const hl::f2 slope = hl::pk1(-PER_OCTAVE), magic = hl::pk1(8388608.f);
+        const float edge = 8388608.f + float(bin);
+        u64 mass = 0;
+        uint32_t kept = 0;
+        for (int i = s0 + lane; i < s1; i += 32) {
+            float v[EPW], sh[EPW];
+            hl::f2 d[PAIRS];
+            uint32_t w[EPW];
+            values(i, v);
+            shares(v, d, sh);
+            weights(sh, w);
+#pragma unroll
+            for (int j = 0; j < PAIRS; ++j) {
+                float at[2];
+                if constexpr (CAPPED) {
+                    at[0] = 8388608.f + float(bin_of(v[2 * j]));
+                    at[1] = 8388608.f + float(bin_of(v[2 * j + 1]));
+                } else {
+                    hl::upk(hl::fma2(d[j], slope, magic), at[0], at[1]);
+                }
+                uint32_t both = 0;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int e = 2 * j + q;
+                    const bool in = at[q] < edge && sh[e] >= least;
+                    both += in ? w[e] : 0u;
+                    kept += in && (!CAPPED || w[e]);
+                    if (at[q] == edge && w[e]) append(v[e], index(i, e));
+                }
+                mass += both;
+            }
+        }
+        send_segment(mass, kept, model);
+    }
+
+    // Leader, whole block: the target's segment from the segments' masses, and the token by going
+    // over the segment again.
+    __device__ void finish(const Cut& cut, float least, double u) {
+        if (warp == 0) {
+            static_assert(SEGS == 64, "two segments a lane");
+            const int n = C * WARPS, g = 2 * lane;
+            const u64 m0 = g < n ? s.seg_mass[g] : 0, m1 = g + 1 < n ? s.seg_mass[g + 1] : 0;
+            const uint32_t kept = __reduce_add_sync(
+                FULL, (g < n ? s.seg_kept[g] : 0) + (g + 1 < n ? s.seg_kept[g + 1] : 0));
+            const u64 model = warp_add((g < n ? s.seg_model[g] : 0) + (g + 1 < n ? s.seg_model[g + 1] : 0));
+            const u64 inc = warp_scan(m0 + m1, lane), W = __shfl_sync(FULL, inc, 31);
+            const u64 t = target_of(u, W), from = inc - m0 - m1;
+            if (t >= from && t < inc) {
+                const bool second = t >= from + m0;
+                s.fin[0] = t - from - (second ? m0 : 0);
+                s.fin[1] = u64(g + second);
+            }
+            if (lane == 0) s.fin[2] = W, s.fin[3] = model, s.pick_most = kept;
+        }
+        __syncthreads();
+        const u64 t = s.fin[0], W = s.fin[2], model = s.fin[3];
+        const int g = int(s.fin[1]), kept = int(s.pick_most);
+        // the segment's words of the row, as the kernel cut them
+        const int from = min(nw, (g / WARPS) * a.per), mine = min(nw, from + a.per) - from;
+        const int seg = (mine + WARPS - 1) / WARPS;
+        const int b0 = from + min(mine, (g % WARPS) * seg), b1 = from + min(mine, (g % WARPS + 1) * seg);
+        const float kv = cut.key ? of_key(cut.key) : -CUDART_INF_F;
+        u64 lower = 0;
+        for (int b = b0; b < b1; b += THREADS) {
+            const int i = b + threadIdx.x;
             float v[EPW];
             uint32_t w[EPW];
             u64 here = 0;
-            if (i + lane < s1) {
-                values(i + lane, v);
+            if (i < b1) {
+                unpack(global_word(i), v, true);
 #pragma unroll
                 for (int e = 0; e < EPW; ++e) {
-                    w[e] = kept_mass<CUTS>(v[e], share(v[e]), index(i + lane, e), cut, kvc, least);
+                    const float sh = share(v[e]);
+                    w[e] = sh >= least && inside(v[e], i * EPW + e - head, cut, kv) ? weight_of(sh) : 0u;
                     here += w[e];
                 }
             }
-            const u64 inc = warp_scan(here, lane);
-            const u64 from = lower + inc - here;
-            if (t >= from && t < from + here) {
-                u64 at = from;
+            u64 total;
+            u64 at = lower + block_scan(here, s.red, &total);
+            if (t >= at && t < at + here) {
 #pragma unroll
                 for (int e = 0; e < EPW; ++e) {
-                    if (t >= at && t < at + w[e]) answer(v[e], index(i + lane, e), W, all_own, all_kept);
+                    if (t >= at && t < at + w[e]) answer(v[e], i * EPW + e - head, W, model, kept);
                     at += w[e];
                 }
             }
-            lower += __shfl_sync(FULL, inc, 31);
+            lower += total;
             if (t < lower) return;
         }
     }
 };
 
 template <typename DT, bool CAPPED, bool RES>
-__global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(THREADS, 4) sample_kernel(const __grid_constant__ Args a) {
     __shared__ Shared s;
     extern __shared__ __align__(16) uint4 words[];
     using R = Row<DT, CAPPED, RES>;
@@ -909,25 +1085,25 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
     r.C = int(C);
     r.rank = int(cluster_ctarank());
     r.lane = threadIdx.x & 31, r.warp = threadIdx.x >> 5;
-    r.row = a.row0 + blockIdx.x / C;
+    r.row = a.row0 + hl::cluster_id_x();
     r.words = words;
     const uintptr_t base = reinterpret_cast<uintptr_t>(a.logits) + uint64_t(r.row * a.ld) * sizeof(DT);
     r.gwords = reinterpret_cast<const uint4*>(base & ~uintptr_t(15));
     r.head = int((base & 15) / sizeof(DT));
     r.nw = (r.head + a.V + EPW - 1) / EPW;
-    const int per = (r.nw + r.C - 1) / r.C;
-    r.w0 = min(r.nw, r.rank * per);
-    const int mine = min(r.nw, r.w0 + per) - r.w0, seg = (mine + WARPS - 1) / WARPS;
+    r.w0 = min(r.nw, r.rank * a.per);
+    const int mine = min(r.nw, r.w0 + a.per) - r.w0, seg = (mine + WARPS - 1) / WARPS;
     r.s0 = min(mine, r.warp * seg), r.s1 = min(mine, r.s0 + seg);
     const int lane = r.lane, warp = r.warp;
 
     // the warp's words: whole ones by a bulk copy, those that reach outside the row by element
     bool lost = false;
+    int f0 = 0, f1 = 0;
+    const uint32_t bar = smem_addr(&s.bar[warp]);
     if constexpr (RES) {
-        const int f0 = r.w0 == 0 && r.s0 == 0 && r.head ? 1 : r.s0;  // first whole word
+        f0 = r.w0 == 0 && r.s0 == 0 && r.head ? 1 : r.s0;  // first whole word
         const bool ragged = (r.head + a.V) % EPW != 0;
-        const int f1 = ragged && r.w0 + r.s1 == r.nw && r.s1 > r.s0 ? r.s1 - 1 : r.s1;
-        const uint32_t bar = smem_addr(&s.bar[warp]);
+        f1 = ragged && r.w0 + r.s1 == r.nw && r.s1 > r.s0 ? r.s1 - 1 : r.s1;
         if (lane == 0) {
             hl::mbar_init(bar, 1);
             hl::fence_mbar_init();
@@ -940,19 +1116,15 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
         __syncwarp();
         if (lane == 1 && r.s0 < r.s1 && f0 > r.s0) words[r.s0] = r.global_word(r.w0 + r.s0);
         if (lane == 2 && f1 < r.s1 && f1 >= f0) words[f1] = r.global_word(r.w0 + f1);
-        if (f1 > f0 && !hl::mbar_wait_bounded(bar, 0, WAIT_NS)) {
-            lost = true;
-            hl::mbar_wait_bounded(bar, 0, WAIT_NS);  // so that the copy does not land later
-        }
-        __syncwarp();
     }
-
-    // settings, the largest logit
+    // meanwhile: the settings, an empty histogram
     const float temp = a.temperature ? a.temperature[r.row] : 1.f;
     const double u = a.uniforms[r.row];
     const int want_k = a.top_k ? a.top_k[r.row] : 0;
     const float p = a.top_p ? a.top_p[r.row] : 1.f;
     const float least = a.min_p ? a.min_p[r.row] : 0.f;
+    r.clear_histogram();
+    if (threadIdx.x == 0) s.n_local = 0;
     const bool bad = !(temp >= 0.f && temp < CUDART_INF_F) || !(u >= 0.0 && u < 1.0) ||
                      !(p >= 0.f) || !(least >= 0.f && least <= 1.f);
     r.c = __fdiv_rn(a.K, temp);
@@ -960,28 +1132,28 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
     if (greedy) r.c = a.K;
     const int k = greedy ? 1 : want_k <= 0 || want_k > a.V ? a.V : want_k;
     const bool small_k = k < a.V && k <= MAX_TOPK;
+    if constexpr (RES) {
+        if (f1 > f0 && !hl::mbar_wait_bounded(bar, 0, WAIT_NS)) {
+            lost = true;
+            hl::mbar_wait_bounded(bar, 0, WAIT_NS);  // so that the copy does not land later
+        }
+        __syncwarp();
+    }
 
+    // the largest logit
     uint32_t m2 = R::E::LOWEST;
+#pragma unroll 4
     for (int i = r.s0 + lane; i < r.s1; i += 32) m2 = R::E::max2(m2, R::E::word_max(r.word(i)));
     const float mine_top = R::E::top(m2);
-    float top = mine_top;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
-    if (lane == 0) s.fred[warp] = top;
+    const uint32_t warp_top = __reduce_max_sync(FULL, key_of(mine_top));
+    if (lane == 0) s.ired[warp] = warp_top;
     const bool any_lost = __syncthreads_or(lost);
-    for (int i = 0; i < WARPS; ++i) top = fmaxf(top, s.fred[i]);
-    uint32_t bound = 0;
-    if (small_k && !bad) bound = k == 1 ? key_of(top) : r.bound_of(mine_top, k);
+    const uint32_t cta_top = __reduce_max_sync(FULL, s.ired[lane % WARPS]);
     cluster_wait();
-    const u64 own_max[2] = {(u64(any_lost) << 32) | key_of(top), bound};
-    const u64(*got)[4] = r.exchange(own_max);
-    uint32_t topkey = 0;
-    bool given_up = false;
-    for (int i = 0; i < r.C; ++i) {
-        topkey = max(topkey, uint32_t(got[i][0]));
-        bound = max(bound, uint32_t(got[i][1]));
-        given_up |= (got[i][0] >> 32) != 0;
-    }
+    const u64* got = r.exchange((u64(any_lost) << 32) | cta_top);
+    const u64 other = got[lane < r.C ? lane : 0];
+    const uint32_t topkey = __reduce_max_sync(FULL, uint32_t(other));
+    const bool given_up = __any_sync(FULL, (other >> 32) != 0);
     r.top = of_key(topkey);
     if (bad || given_up || topkey == KEY_NONE) {
         if (r.rank == 0 && threadIdx.x == 0) {
@@ -992,9 +1164,11 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
     }
     r.zm = r.z(r.top);
 
-    if (small_k && r.few(bound, k, p, least, u)) return;
+    if (small_k) {
+        const float from = k == 1 ? r.top : r.bound_of(mine_top, k);
+        if (r.few(from, k, p, least, u)) return;
+    }
 
-    // +inf without a softcap: the tokens at +inf share the mass alike, all others have none
     if (!CAPPED && r.top == CUDART_INF_F) {
         if constexpr (RES) {
             DT* x = reinterpret_cast<DT*>(words);
@@ -1008,21 +1182,75 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const __grid_constan
         r.inf_row = true;
         r.top = r.zm = 0.f;
     }
+    const Cut none{0u, 0x7fffffff};
     const bool want = a.logprobs != nullptr;
-    u64 own = 0;
-    bool have = !want;
-    Cut cut = NO_CUT;
-    if (k < a.V) cut = r.resolve(false, k, 1.f, cut, have ? nullptr : &own), have = true;
-    if (p < 1.f) cut = r.resolve(true, 0, p, cut, have ? nullptr : &own), have = true;
-    if (cut.key == 0u && least == 0.f) r.template draw<false>(cut, 0.f, u, own, !have);
-    else r.template draw<true>(cut, least, u, own, !have);
+    if (k == a.V && !(p < 1.f)) {
+        if (least == 0.f) r.sum_all(want, 0);
+        else r.sum_kept(none, least, want, 0);
+        cluster_barrier_or_leave(r.rank);
+        if (r.rank == 0) r.finish(none, least, u);
+        return;
+    }
+    if (k == a.V) {
+        typename R::Model m;
+        r.histogram(want ? &m : nullptr);
+        const u64 model = want ? r.model_sum(m) : 0;
+        cluster_barrier();
+        u64 n[2];
+        uint32_t most[2];
+        r.join_masses(n, most);
+        double target;
+        r.pick(n, most, true, double(p), &target, true, 0);
+        const uint32_t bin = s.pick_bin;
+        // how many tokens a CTA may have in it, by the least weight of the bin
+        const float light = fmaxf(1.f, UNIT * ex2f(-(float(bin) + 0.5f) / PER_OCTAVE) * 0.999f - 1.f);
+        const bool fits = bin < BINS - 1 &&
+                          float(s.pick_most) * 65536.f <= float(CAP / r.C) * light;
+        if (fits) {
+            const u64 before = s.pick_before;
+            r.sum_above(bin, least, model);
+            __syncthreads();
+            r.send_count();
+            cluster_barrier();  // (a wait for all: the histograms were read until here)
+            if (r.rank) return;
+            int count;
+            const u64* sorted = r.rank_list(&count);
+            const Cut cut = r.cut_of(sorted, count, true, before, target);
+            const float kv = of_key(cut.key);
+            for (int i = threadIdx.x; i < count; i += THREADS) {
+                const float v = of_key(uint32_t(sorted[i] >> 32));
+                const int idx = int(~uint32_t(sorted[i]));
+                const float sh = r.share(v);
+                if (!r.inside(v, idx, cut, kv) || !(sh >= least)) continue;
+                // its segment
+                const int w = (idx + r.head) / EPW, cta = w / a.per;
+                const int have = min(r.nw, (cta + 1) * a.per) - cta * a.per;
+                const int g = cta * WARPS + (w - cta * a.per) / ((have + WARPS - 1) / WARPS);
+                atomicAdd(&s.seg_mass[g], u64(weight_of(sh)));
+                atomicAdd(&s.seg_kept[g], 1u);
+            }
+            __syncthreads();
+            r.finish(cut, least, u);
+            return;
+        }
+        const Cut cut = r.resolve(true, 0, p, none);
+        r.sum_kept(cut, least, false, model);
+        cluster_barrier_or_leave(r.rank);
+        if (r.rank == 0) r.finish(cut, least, u);
+        return;
+    }
+    Cut cut = r.resolve(false, k, 1.f, none);
+    if (p < 1.f) cut = r.resolve(true, 0, p, cut);
+    r.sum_kept(cut, least, want, 0);
+    cluster_barrier_or_leave(r.rank);
+    if (r.rank == 0) r.finish(cut, least, u);
 }
 
 // -------------------------------------------------------------------- launch ----
 
-// Shared memory of a CTA's words at most: two CTAs an SM beside the fixed part.
-constexpr int SLICE = 72 * 1024;
-constexpr int SLICE_MOST = 160 * 1024;
+// Shared memory of a CTA's words: four CTAs an SM beside the fixed part, and the most.
+constexpr int SLICE = 38 * 1024;
+constexpr int SLICE_MOST = 192 * 1024;
 
 template <typename DT, bool CAPPED>
 int launch(Args a, int64_t N, int device, int sms, cudaStream_t st) {
@@ -1031,10 +1259,11 @@ int launch(Args a, int64_t N, int device, int sms, cudaStream_t st) {
     int C = 1;
     while (C < MAXC && slice(C) > SLICE) ++C;
     // few rows: more CTAs a row, while each warp has a few words a lane
-    while (C < MAXC && N * (C + 1) <= sms && slice(C) > 16 * 1024) ++C;
+    while (C < MAXC && N * (C + 1) <= 2 * sms && slice(C) > 8 * 1024) ++C;
     const bool resident = slice(C) <= SLICE_MOST;
     const void* kernel = resident ? reinterpret_cast<const void*>(&sample_kernel<DT, CAPPED, true>)
                                   : reinterpret_cast<const void*>(&sample_kernel<DT, CAPPED, false>);
+    a.per = int(slice(C) / 16);
     const int smem = resident ? int(slice(C)) : 0;
     if (resident) {
         static std::atomic<uint64_t> done{0};  // devices whose limit is raised

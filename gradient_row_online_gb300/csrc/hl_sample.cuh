@@ -32,6 +32,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "headloss.h"
 #include "hl_pack.cuh"
@@ -53,6 +54,10 @@ constexpr int RANKED = 256;   // ranked by comparison with all; more are sorted
 constexpr int MAX_TOPK = 128; // longest top-k that takes the thread-maxima bound
 constexpr int SEGS = MAXC * WARPS;
 constexpr float PER_OCTAVE = 16.f;  // bins an octave of mass
+constexpr int TOPS = 128;           // bins of the thread maxima,
+constexpr float TOPS_PER_OCTAVE = 4.f;
+constexpr int SPLIT = 15;  // a mass is added as its bits above and below this one: either sum
+                           // stays below 2^32 for up to 2^17 tokens a CTA
 constexpr float UNIT = 1073741824.f;  // 2^30, the weight of the largest logit
 constexpr float LN2 = 0.69314718055994531f;
 constexpr unsigned FULL = 0xffffffffu;
@@ -90,6 +95,11 @@ struct Shared {
     u64 seg_mass[SEGS];    // the segments' kept masses, the model's, and counts (leader)
     u64 seg_model[SEGS];
     uint32_t seg_kept[SEGS];
+    u64 my_mass[WARPS];    // the CTA's own segments
+    u64 my_model[WARPS];
+    uint32_t my_kept[WARPS];
+    uint32_t tops[TOPS];   // histogram of the thread maxima
+    float from;
     uint32_t list_n[MAXC];
     u64 red[WARPS];
     uint32_t ired[WARPS];
@@ -253,6 +263,14 @@ __device__ __forceinline__ uint2 ld_peer_pair(uint32_t addr) {
     asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
     return v;
 }
+__device__ __forceinline__ uint4 ld_peer_quad(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
 __device__ __forceinline__ void cluster_arrive() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
@@ -260,18 +278,14 @@ __device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// Arrival of a warp that wrote nothing another CTA reads (no fence).
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_barrier() {
     __syncwarp();
     hl::cluster_barrier();
 }
-// The last barrier of a row: the leader waits, the other CTAs need not (their shared memory is
-// read by no one after the barrier before).
-__device__ __forceinline__ void cluster_barrier_or_leave(int rank) {
-    __syncwarp();
-    cluster_arrive();
-    if (rank == 0) cluster_wait();
-}
-
 // -------------------------------------------------------------------- a row ----
 
 template <typename DT, bool CAPPED, bool RES>
@@ -366,20 +380,27 @@ struct Row {
     }
 
     // Mass of the whole softmax at T = 1: a word's shares summed in fp32 in one order, the words
-    // in fixed point (2^-39 of the largest logit's; 2^-28 for a word above 2^-8), so
-    // that it too is the same however the row is split.
+    // in fixed point, so that it too is the same however the row is split.  A word's sum t < 16 is
+    // taken apart by adding and subtracting 1.5 * 2^23 units: H units of 2^-13, and the
+    // exact remainder in units of 2^-36; the integers are the low bits of the sums.
     struct Model {
-        u64 sum = 0;
+        std::conditional_t<RES, int, int64_t> high = 0, low = 0;
         bool odd = false;  // a word with a NaN (or +inf)
         __device__ __forceinline__ void add(const float* sh) {
+            constexpr float HIGH = 12582912.f * 0x1p-13f, LOW = 12582912.f;
             float t;
             if constexpr (EPW == 8)
                 t = ((sh[0] + sh[1]) + (sh[2] + sh[3])) + ((sh[4] + sh[5]) + (sh[6] + sh[7]));
             else t = (sh[0] + sh[1]) + (sh[2] + sh[3]);
             odd |= !(t < 15.f);
-            const bool small = t < 0x1p-8f;
-            const uint32_t n = __float2uint_rn(__fmul_rn(t, small ? 0x1p+39f : 0x1p+28f));
-            sum += small ? u64(n) : u64(n) << 11;
+            const float h = __fadd_rn(t, HIGH);
+            const float l = __fmaf_rn(__fsub_rn(t, __fsub_rn(h, HIGH)), 0x1p+36f, LOW);
+            high += __float_as_int(h) - 0x44c00000;
+            low += __float_as_int(l) - 0x4b400000;
+        }
+        // in units of 2^-36
+        __device__ __forceinline__ u64 sum() const {
+            return u64(int64_t(high) * (1 << 23) + int64_t(low));
         }
     };
     __device__ __forceinline__ void add_model(Model& m, const float* v) const {
@@ -413,7 +434,7 @@ struct Row {
                 m.add(v);
             }
         }
-        return warp_add(m.sum);
+        return warp_add(m.sum());
     }
 
     // Bin of the order: 1/16 octave of mass a bin without a softcap (with one, of the raw
@@ -426,10 +447,21 @@ struct Row {
         return v > kv || (v == kv && idx <= k.idx);
     }
 
-    // Every CTA's value (of warp 0's lanes, all alike) at every CTA.
+    // Every CTA's value (of warp 0's lanes, all alike) at every CTA.  ALONE: the other warps
+    // wrote nothing that another CTA reads after it.
+    template <bool ALONE>
     __device__ const u64* exchange(u64 v) {
-        if (warp == 0 && lane < C) st_peer64(map_peer(smem_addr(&s.xch[par][rank]), lane), v);
-        cluster_barrier();
+        __syncwarp();
+        if (warp == 0) {
+            if (lane < C) st_peer64(map_peer(smem_addr(&s.xch[par][rank]), lane), v);
+            __syncwarp();
+            cluster_arrive();
+        } else if constexpr (ALONE) {
+            cluster_arrive_relaxed();
+        } else {
+            cluster_arrive();
+        }
+        cluster_wait();
         const u64* got = s.xch[par];
         par ^= 1;
         return got;
@@ -446,9 +478,9 @@ struct Row {
         const float zz = z(v);
         if (a.logprobs)
             a.logprobs[row] = (zz == zm ? 0.f : __fsub_rn(zz, zm) * a.K * LN2) -
-                              logf(float(double(model) * 0x1p-39));
+                              logf(float(model) * 0x1p-36f);
         if (a.draw_logprobs)
-            a.draw_logprobs[row] = exponent(v) * LN2 - logf(float(double(W) * 0x1p-30));
+            a.draw_logprobs[row] = exponent(v) * LN2 - logf(float(W) * 0x1p-30f);
         if (a.n_kept) a.n_kept[row] = kept;
     }
     __device__ static u64 target_of(double u, u64 W) {
@@ -528,17 +560,21 @@ struct Row {
             most[0] = max(most[0], x.x), most[1] = max(most[1], x.y);
         }
     }
-    // `most`: a CTA's largest mass in the bin, rounded up to 2^16.
+    // A bin's mass from its two sums.
+    __device__ __forceinline__ static u64 joined(uint32_t hi, uint32_t lo) {
+        return (u64(hi) << (RES ? SPLIT : 32)) + lo;
+    }
+    // `most`: the largest of a CTA's masses in the bin, in 2^SPLIT rounded up.
     __device__ __forceinline__ void join_masses(u64* m, uint32_t* most) const {
         m[0] = m[1] = 0;
         most[0] = most[1] = 0;
         for (int r = 0; r < C; ++r) {
             const uint2 x = ld_peer_pair(map_peer(smem_addr(&s.hi[2 * threadIdx.x]), r));
             const uint2 y = ld_peer_pair(map_peer(smem_addr(&s.lo[2 * threadIdx.x]), r));
-            const u64 m0 = (u64(x.x) << 16) + y.x, m1 = (u64(x.y) << 16) + y.y;
+            const u64 m0 = joined(x.x, y.x), m1 = joined(x.y, y.y);
             m[0] += m0, m[1] += m1;
-            most[0] = max(most[0], uint32_t((m0 + 0xffff) >> 16));
-            most[1] = max(most[1], uint32_t((m1 + 0xffff) >> 16));
+            most[0] = max(most[0], uint32_t(min((m0 >> SPLIT) + 1, u64(0xffffffffu))));
+            most[1] = max(most[1], uint32_t(min((m1 >> SPLIT) + 1, u64(0xffffffffu))));
         }
     }
     // The bin that the target (a count, or `p` times the total) falls in, what lies before
@@ -565,21 +601,44 @@ struct Row {
 
     // -------------------------------------------------------- small top-k ----
 
-    // A bound from below of the k-th largest logit: the bin where the histogram of the
-    // cluster's thread maxima reaches k.
+    // A bound from below of the k-th largest logit: the lower edge of the bin where the
+    // histogram of the cluster's thread maxima reaches k.
     __device__ float bound_of(float mine, int k) {
-        if (mine > -CUDART_INF_F) atomicAdd(&s.cnt[bin_of(mine)], 1u);
+        if (mine > -CUDART_INF_F)
+            atomicAdd(&s.tops[min(uint32_t(TOPS - 1), __float2uint_rn(__fmul_rn(
+                                                          __fmul_rn(__fsub_rn(top, mine), c),
+                                                          TOPS_PER_OCTAVE)))],
+                      1u);
         cluster_barrier();
-        u64 n[2];
-        uint32_t most[2];
-        join_counts(n, most);
-        double target;
-        pick(n, most, false, double(k), &target, true, 0);
-        const uint32_t bin = s.pick_bin;
-        if (bin >= BINS - 1) return -CUDART_INF_F;
-        // distances of the bin lie below (bin + 1/2) / 16 c; a little more for the roundings
-        const float far = __fmul_ru(__fdiv_ru(float(bin) + 0.5f, __fmul_rd(c, PER_OCTAVE)), 1.00001f);
-        return __fsub_rd(top, far);
+        if (warp == 0) {
+            static_assert(TOPS == 128, "four bins a lane");
+            uint4 n = make_uint4(0, 0, 0, 0);
+            for (int r = 0; r < C; ++r) {
+                const uint4 x = ld_peer_quad(map_peer(smem_addr(&s.tops[4 * lane]), r));
+                n.x += x.x, n.y += x.y, n.z += x.z, n.w += x.w;
+            }
+            const uint32_t sum = n.x + n.y + n.z + n.w;
+            uint32_t inc = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t m = __shfl_up_sync(FULL, inc, o);
+                if (lane >= o) inc += m;
+            }
+            const unsigned past = __ballot_sync(FULL, inc >= uint32_t(k));
+            if (lane == (past ? __ffs(past) - 1 : 0)) {
+                uint32_t at = inc - sum + n.x;
+                int bin = 4 * lane;
+                if (at < uint32_t(k)) ++bin, at += n.y;
+                if (at < uint32_t(k)) ++bin, at += n.z;
+                if (at < uint32_t(k)) ++bin;
+                // distances of the bin lie below (bin + 1/2) / 4 c; a little more for the roundings
+                const float far = __fmul_ru(
+                    __fdiv_ru(float(bin) + 0.5f, __fmul_rd(c, TOPS_PER_OCTAVE)), 1.00001f);
+                s.from = !past || bin == TOPS - 1 ? -CUDART_INF_F : __fsub_rd(top, far);
+            }
+        }
+        __syncthreads();
+        return s.from;
     }
 
     // The tokens at or above `from` to the leader, and the row finished there.  False (in
@@ -599,11 +658,17 @@ struct Row {
                         if (v[e] >= from && v[e] > -CUDART_INF_F) append(v[e], index(i, e));
             }
         }
-        const u64 mine_model = want ? model_sum(model) : 0;
-        if (lane == 0) st_peer64(map_peer(smem_addr(&s.seg_model[rank * WARPS + warp]), 0), mine_model);
+        if (want) {
+            const u64 m = model_sum(model);
+            if (lane == 0) s.my_model[warp] = m;
+        }
         __syncthreads();
-        send_count();
-        const u64* all = exchange(s.n_local);
+        if (warp == 0) {
+            if (want && lane < WARPS)
+                st_peer64(map_peer(smem_addr(&s.seg_model[rank * WARPS + lane]), 0), s.my_model[lane]);
+            if (lane == 0) st_peer32(map_peer(smem_addr(&s.list_n[rank]), 0), s.n_local);
+        }
+        const u64* all = exchange<false>(s.n_local);
         if (__any_sync(FULL, lane < C && all[lane] > u64(CAP / C))) return false;
         if (rank) return true;
 
@@ -628,7 +693,8 @@ struct Row {
             if (i < warp) before += s.red[i];
             W += s.red[i];
         }
-        if (p < 1.f && t > 0 && !(double(before) < double(p) * double(W))) w = 0;
+        // (before < p W as integers: before < ceil(p W))
+        if (p < 1.f && t > 0 && before >= u64(__double2ull_ru(double(p) * double(W)))) w = 0;
         if (!(e >= least)) w = 0;
         // the kept masses by index
         u64* by_index = reinterpret_cast<u64*>(s.hi);
@@ -641,19 +707,20 @@ struct Row {
         for (int i = 0; i < RW; ++i) W += s.seg_mass[i];
         const int kept = int(W >> 48);
         W &= (u64(1) << 48) - 1;
-        if (w) {
-            u64 lower = 0;
+        if (!__any_sync(FULL, w > 0)) return true;
+        const u64 at = target_of(u, W);
+        u64 lower = 0;
 #pragma unroll 4
-            for (int j = 0; j < k; ++j) {
-                const u64 o = by_index[j];
-                if (int(o >> 32) < idx) lower += uint32_t(o);
-            }
-            const u64 at = target_of(u, W);
-            if (at >= lower && at < lower + w) {
-                u64 all_model = 0;
-                for (int i = 0; i < C * WARPS; ++i) all_model += s.seg_model[i];
-                answer(v, idx, W, all_model, kept);
-            }
+        for (int j = 0; j < k; ++j) {
+            const u64 o = by_index[j];
+            if (int(o >> 32) < idx) lower += uint32_t(o);
+        }
+        const bool it = w && at >= lower && at < lower + w;
+        if (__any_sync(FULL, it)) {
+            u64 all_model = 0;
+            for (int i = lane; i < C * WARPS; i += 32) all_model += s.seg_model[i];
+            all_model = warp_add(all_model);
+            if (it) answer(v, idx, W, all_model, kept);
         }
         return true;
     }
@@ -666,9 +733,20 @@ struct Row {
     __device__ void clear_histogram() {
         for (int i = threadIdx.x; i < BINS; i += THREADS) s.cnt[i] = 0, s.hi[i] = 0, s.lo[i] = 0;
     }
+    // Adds a mass (none where it is 0) to a bin.
     __device__ __forceinline__ void add_bin(uint32_t b, uint32_t w) {
-        atomicAdd(&s.hi[b], w >> 16);
-        atomicAdd(&s.lo[b], w & 0xffffu);
+        if constexpr (RES) {
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\t"
+                "setp.ne.u32 p, %1, 0;\n\tsetp.ne.u32 q, %2, 0;\n\t"
+                "@p red.shared.add.u32 [%0], %1;\n\t"
+                "@q red.shared.add.u32 [%3], %2;\n\t}" ::"r"(smem_addr(s.lo) + 4 * b),
+                "r"(w & ((1u << SPLIT) - 1)), "r"(w >> SPLIT), "r"(smem_addr(s.hi) + 4 * b)
+                : "memory");
+        } else if (w) {  // any number of tokens a CTA: 64 bits, the carry by hand
+            const uint32_t old = atomicAdd(&s.lo[b], w);
+            if (old + w < old) atomicAdd(&s.hi[b], 1u);
+        }
     }
 
     // The histogram of masses of all tokens; the model's mass on the way where `model` is
@@ -697,8 +775,8 @@ struct Row {
                     hl::upk(hl::fma2(d[j], slope, magic), x, y);
                     b[0] = __float_as_uint(x) - 0x4b000000u, b[1] = __float_as_uint(y) - 0x4b000000u;
                 }
-                if (w[2 * j]) add_bin(b[0], w[2 * j]);
-                if (w[2 * j + 1]) add_bin(b[1], w[2 * j + 1]);
+                add_bin(b[0], w[2 * j]);
+                add_bin(b[1], w[2 * j + 1]);
             }
         }
     }
@@ -772,7 +850,7 @@ struct Row {
                 for (int i = 0; i < WARPS; ++i)
                     least = min(least, ~uint32_t(s.red[i] >> 32)),
                     largest = max(largest, uint32_t(s.red[i]));
-                const u64* got = exchange((u64(~least) << 32) | largest);
+                const u64* got = exchange<true>((u64(~least) << 32) | largest);
                 for (int r = 0; r < C; ++r)
                     least = min(least, ~uint32_t(got[r] >> 32)),
                     largest = max(largest, uint32_t(got[r]));
@@ -855,7 +933,7 @@ struct Row {
             if (i < warp) lower += s.red[i];
             count += s.red[i];
         }
-        const u64* got = exchange(count);
+        const u64* got = exchange<true>(count);
         for (int r = 0; r < rank; ++r) lower += got[r];
         if (stay > lower && stay <= lower + mine) {
             for (int i = s0; i < s1; i += 32) {
@@ -912,16 +990,35 @@ struct Row {
 
     // ----------------------------------------------------------- the draw ----
 
-    // A segment's sums to the leader.
-    __device__ void send_segment(u64 mass, uint32_t kept, u64 model) {
+    // A segment's sums; then, after a block barrier, the CTA's to the leader (warp 0).
+    __device__ void keep_segment(u64 mass, uint32_t kept, u64 model) {
         mass = warp_add(mass);
         kept = __reduce_add_sync(FULL, kept);
-        if (lane == 0) {
-            const int g = rank * WARPS + warp;
-            st_peer64(map_peer(smem_addr(&s.seg_mass[g]), 0), mass);
-            st_peer32(map_peer(smem_addr(&s.seg_kept[g]), 0), kept);
-            st_peer64(map_peer(smem_addr(&s.seg_model[g]), 0), model);
+        if (lane == 0) s.my_mass[warp] = mass, s.my_kept[warp] = kept, s.my_model[warp] = model;
+    }
+    __device__ void send_segments() {
+        if (lane < WARPS) {
+            const int g = rank * WARPS + lane;
+            st_peer64(map_peer(smem_addr(&s.seg_mass[g]), 0), s.my_mass[lane]);
+            st_peer32(map_peer(smem_addr(&s.seg_kept[g]), 0), s.my_kept[lane]);
+            st_peer64(map_peer(smem_addr(&s.seg_model[g]), 0), s.my_model[lane]);
         }
+        __syncwarp();
+    }
+    // The last step of a row: the sums to the leader, which waits for all; the others leave
+    // (their shared memory is read by no one after the barrier before).
+    __device__ bool leave() {
+        __syncthreads();
+        if (warp == 0) {
+            send_segments();
+            cluster_arrive();
+        } else {
+            if (rank) return true;
+            cluster_arrive_relaxed();
+        }
+        if (rank) return true;
+        cluster_wait();
+        return false;
     }
 
     // No filter: the masses of everything.
@@ -947,7 +1044,7 @@ struct Row {
                 kept += min(w[j], 1u) + min(w[j + 1], 1u);
             }
         }
-        send_segment(mass, kept, want ? model_sum(m) : model);
+        keep_segment(mass, kept, want ? model_sum(m) : model);
     }
 
     // The masses of what the cut and min-p leave.
@@ -975,7 +1072,7 @@ struct Row {
                 kept += in;
             }
         }
-        send_segment(mass, kept, want ? model_sum(m) : model);
+        keep_segment(mass, kept, want ? model_sum(m) : model);
     }
 
     // The masses of the bins above `bin` (and of min-p), the bin's tokens to the leader.
@@ -991,6 +1088,8 @@ struct Row {
             values(i, v);
             shares(v, d, sh);
             weights(sh, w);
+            bool on_edge = false;
+            [[maybe_unused]] float bins[EPW];
 #pragma unroll
             for (int j = 0; j < PAIRS; ++j) {
                 float at[2];
@@ -1007,12 +1106,19 @@ struct Row {
                     const bool in = at[q] < edge && sh[e] >= least;
                     both += in ? w[e] : 0u;
                     kept += in && (!CAPPED || w[e]);
-                    if (at[q] == edge && w[e]) append(v[e], index(i, e));
+                    on_edge |= at[q] == edge;
+                    if constexpr (CAPPED) bins[e] = at[q];
                 }
                 mass += both;
             }
+            if (on_edge)
+                for (int e = 0; e < EPW; ++e) {
+                    const float x = CAPPED ? bins[e]
+                                           : __fmaf_rn(__fmul_rn(__fsub_rn(v[e], zm), c), -PER_OCTAVE, 8388608.f);
+                    if (x == edge && w[e]) append(v[e], index(i, e));
+                }
         }
-        send_segment(mass, kept, model);
+        keep_segment(mass, kept, model);
     }
 
     // Leader, whole block: the target's segment from the segments' masses, and the token by going
@@ -1079,7 +1185,7 @@ __global__ void __launch_bounds__(THREADS, 4) sample_kernel(const __grid_constan
     using R = Row<DT, CAPPED, RES>;
     constexpr int EPW = R::EPW;
     R r(a, s);
-    cluster_arrive();  // before the first write to a peer: every CTA has started
+    cluster_arrive_relaxed();  // waited for before the first write to a peer: every CTA has started
     uint32_t C;
     asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(C));
     r.C = int(C);
@@ -1123,15 +1229,21 @@ __global__ void __launch_bounds__(THREADS, 4) sample_kernel(const __grid_constan
     const int want_k = a.top_k ? a.top_k[r.row] : 0;
     const float p = a.top_p ? a.top_p[r.row] : 1.f;
     const float least = a.min_p ? a.min_p[r.row] : 0.f;
-    r.clear_histogram();
     if (threadIdx.x == 0) s.n_local = 0;
-    const bool bad = !(temp >= 0.f && temp < CUDART_INF_F) || !(u >= 0.0 && u < 1.0) ||
+    const u64 ubits = u64(__double_as_longlong(u));  // in [0, 1): below 1.0's bits (or -0)
+    const bool bad = !(temp >= 0.f && temp < CUDART_INF_F) ||
+                     !(ubits < 0x3ff0000000000000ull || ubits == 0x8000000000000000ull) ||
                      !(p >= 0.f) || !(least >= 0.f && least <= 1.f);
     r.c = __fdiv_rn(a.K, temp);
     const bool greedy = !(r.c < CUDART_INF_F);
     if (greedy) r.c = a.K;
     const int k = greedy ? 1 : want_k <= 0 || want_k > a.V ? a.V : want_k;
     const bool small_k = k < a.V && k <= MAX_TOPK;
+    if (small_k) {
+        if (threadIdx.x < TOPS) s.tops[threadIdx.x] = 0;
+    } else if (p < 1.f) {
+        r.clear_histogram();
+    }
     if constexpr (RES) {
         if (f1 > f0 && !hl::mbar_wait_bounded(bar, 0, WAIT_NS)) {
             lost = true;
@@ -1150,7 +1262,7 @@ __global__ void __launch_bounds__(THREADS, 4) sample_kernel(const __grid_constan
     const bool any_lost = __syncthreads_or(lost);
     const uint32_t cta_top = __reduce_max_sync(FULL, s.ired[lane % WARPS]);
     cluster_wait();
-    const u64* got = r.exchange((u64(any_lost) << 32) | cta_top);
+    const u64* got = r.template exchange<true>((u64(any_lost) << 32) | cta_top);
     const u64 other = got[lane < r.C ? lane : 0];
     const uint32_t topkey = __reduce_max_sync(FULL, uint32_t(other));
     const bool given_up = __any_sync(FULL, (other >> 32) != 0);
@@ -1187,8 +1299,7 @@ __global__ void __launch_bounds__(THREADS, 4) sample_kernel(const __grid_constan
     if (k == a.V && !(p < 1.f)) {
         if (least == 0.f) r.sum_all(want, 0);
         else r.sum_kept(none, least, want, 0);
-        cluster_barrier_or_leave(r.rank);
-        if (r.rank == 0) r.finish(none, least, u);
+        if (!r.leave()) r.finish(none, least, u);
         return;
     }
     if (k == a.V) {
@@ -1205,11 +1316,12 @@ __global__ void __launch_bounds__(THREADS, 4) sample_kernel(const __grid_constan
         // how many tokens a CTA may have in it, by the least weight of the bin
         const float light = fmaxf(1.f, UNIT * ex2f(-(float(bin) + 0.5f) / PER_OCTAVE) * 0.999f - 1.f);
         const bool fits = bin < BINS - 1 &&
-                          float(s.pick_most) * 65536.f <= float(CAP / r.C) * light;
+                          float(s.pick_most) * float(1 << SPLIT) <= float(CAP / r.C) * light;
         if (fits) {
             const u64 before = s.pick_before;
             r.sum_above(bin, least, model);
             __syncthreads();
+            if (warp == 0) r.send_segments();
             r.send_count();
             cluster_barrier();  // (a wait for all: the histograms were read until here)
             if (r.rank) return;
@@ -1235,15 +1347,13 @@ __global__ void __launch_bounds__(THREADS, 4) sample_kernel(const __grid_constan
         }
         const Cut cut = r.resolve(true, 0, p, none);
         r.sum_kept(cut, least, false, model);
-        cluster_barrier_or_leave(r.rank);
-        if (r.rank == 0) r.finish(cut, least, u);
+        if (!r.leave()) r.finish(cut, least, u);
         return;
     }
     Cut cut = r.resolve(false, k, 1.f, none);
     if (p < 1.f) cut = r.resolve(true, 0, p, cut);
     r.sum_kept(cut, least, want, 0);
-    cluster_barrier_or_leave(r.rank);
-    if (r.rank == 0) r.finish(cut, least, u);
+    if (!r.leave()) r.finish(cut, least, u);
 }
 
 // -------------------------------------------------------------------- launch ----

@@ -17,7 +17,7 @@
 //   a small top-k        a histogram of the thread maxima bounds the cut from below (as many
 //                        tokens as maxima lie above it); the few tokens above the bound are
 //                        ranked by the leader, which finishes the row alone.
-//   top-p                a histogram of the order (1/16 octave of mass a bin) with exact masses
+//   top-p                a histogram of the order (1/32 octave of mass a bin) with exact masses
 //                        finds the bin of the cut; the next pass sums the segments' masses in the
 //                        bins above it and sends the bin's few tokens to be ranked.
 //   else                 `resolve`: the same by count or mass within another cut, where a bin with
@@ -48,12 +48,12 @@ using hl::smem_addr;
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
 constexpr int MAXC = 8;       // CTAs a cluster at most
-constexpr int BINS = 2 * THREADS;
+constexpr int BINS = 4 * THREADS;
 constexpr int CAP = 1024;     // tokens the leader can rank
 constexpr int RANKED = 256;   // ranked by comparison with all; more are sorted
 constexpr int MAX_TOPK = 128; // longest top-k that takes the thread-maxima bound
 constexpr int SEGS = MAXC * WARPS;
-constexpr float PER_OCTAVE = 16.f;  // bins an octave of mass
+constexpr float PER_OCTAVE = 32.f;  // bins an octave of mass
 constexpr int TOPS = 128;           // bins of the thread maxima,
 constexpr float TOPS_PER_OCTAVE = 4.f;
 constexpr int SPLIT = 15;  // a mass is added as its bits above and below this one: either sum
@@ -86,11 +86,12 @@ typedef unsigned long long u64;
 
 struct Shared {
     u64 bar[WARPS];
-    u64 list[CAP];         // (key << 32 | ~index) of the tokens to rank, a run a CTA (leader)
-    u64 sorted[RANKED];
-    uint32_t hi[BINS];     // histogram: masses above and below bit 16, and counts; the
-    uint32_t lo[BINS];     // masses' space is also where the list is put together
-    uint32_t cnt[BINS];
+    union {
+        u64 list[CAP];     // (key << 32 | ~index) of the tokens to rank, a run a CTA (leader)
+        uint32_t cnt[BINS];  // histogram of counts
+    };
+    uint32_t hi[BINS];     // histogram of masses, above and below bit SPLIT; afterwards the
+    uint32_t lo[BINS];     // place where lists are ranked
     u64 xch[2][MAXC];      // exchanges of one value a CTA
     u64 seg_mass[SEGS];    // the segments' kept masses, the model's, and counts (leader)
     u64 seg_model[SEGS];
@@ -257,11 +258,6 @@ __device__ __forceinline__ void st_peer64(uint32_t addr, u64 v) {
 }
 __device__ __forceinline__ void st_peer32(uint32_t addr, uint32_t v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-__device__ __forceinline__ uint2 ld_peer_pair(uint32_t addr) {
-    uint2 v;
-    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
-    return v;
 }
 __device__ __forceinline__ uint4 ld_peer_quad(uint32_t addr) {
     uint4 v;
@@ -437,11 +433,17 @@ struct Row {
         return warp_add(m.sum());
     }
 
-    // Bin of the order: 1/16 octave of mass a bin without a softcap (with one, of the raw
+    // Bin of the order: 1/32 octave of mass a bin without a softcap (with one, of the raw
     // logit's distance); the last takes what is further off.
     __device__ __forceinline__ uint32_t bin_of(float v) const {
         return min(uint32_t(BINS - 1),
                    __float2uint_rn(__fmul_rn(__fmul_rn(__fsub_rn(top, v), c), PER_OCTAVE)));
+    }
+    // Below every logit of a bin (of `per` an octave): distances lie below (bin + 1/2) / (per c),
+    // and a little more for the roundings.
+    __device__ float lower_edge(float bin, float per) const {
+        const float far = __fmul_ru(__fdiv_ru(bin + 0.5f, __fmul_rd(c, per)), 1.00001f);
+        return __fsub_rd(top, far);
     }
     __device__ __forceinline__ bool inside(float v, int idx, const Cut& k, float kv) const {
         return v > kv || (v == kv && idx <= k.idx);
@@ -514,6 +516,7 @@ struct Row {
         };
         if (n <= RANKED) {
             u64* all = reinterpret_cast<u64*>(s.hi);
+            u64* sorted = all + RANKED;
             const u64 mine = int(threadIdx.x) < n ? at(threadIdx.x) : 0;
             if (int(threadIdx.x) < n) all[threadIdx.x] = mine;
             __syncthreads();
@@ -521,10 +524,10 @@ struct Row {
                 int better = 0;
 #pragma unroll 4
                 for (int j = 0; j < n; ++j) better += all[j] > mine;
-                s.sorted[better] = mine;
+                sorted[better] = mine;
             }
             __syncthreads();
-            return s.sorted;
+            return sorted;
         }
         u64 v[CAP / THREADS];
 #pragma unroll
@@ -550,14 +553,14 @@ struct Row {
         return s.list;
     }
 
-    // Two bins' joined histogram entries, of the thread.
+    // The thread's four bins of the joined histograms.
     __device__ __forceinline__ void join_counts(u64* n, uint32_t* most) const {
-        n[0] = n[1] = 0;
-        most[0] = most[1] = 0;
+        for (int q = 0; q < 4; ++q) n[q] = most[q] = 0;
         for (int r = 0; r < C; ++r) {
-            const uint2 x = ld_peer_pair(map_peer(smem_addr(&s.cnt[2 * threadIdx.x]), r));
-            n[0] += x.x, n[1] += x.y;
-            most[0] = max(most[0], x.x), most[1] = max(most[1], x.y);
+            const uint4 x = ld_peer_quad(map_peer(smem_addr(&s.cnt[4 * threadIdx.x]), r));
+            const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) n[q] += y[q], most[q] = max(most[q], y[q]);
         }
     }
     // A bin's mass from its two sums.
@@ -566,15 +569,16 @@ struct Row {
     }
     // `most`: the largest of a CTA's masses in the bin, in 2^SPLIT rounded up.
     __device__ __forceinline__ void join_masses(u64* m, uint32_t* most) const {
-        m[0] = m[1] = 0;
-        most[0] = most[1] = 0;
+        for (int q = 0; q < 4; ++q) m[q] = most[q] = 0;
         for (int r = 0; r < C; ++r) {
-            const uint2 x = ld_peer_pair(map_peer(smem_addr(&s.hi[2 * threadIdx.x]), r));
-            const uint2 y = ld_peer_pair(map_peer(smem_addr(&s.lo[2 * threadIdx.x]), r));
-            const u64 m0 = joined(x.x, y.x), m1 = joined(x.y, y.y);
-            m[0] += m0, m[1] += m1;
-            most[0] = max(most[0], uint32_t(min((m0 >> SPLIT) + 1, u64(0xffffffffu))));
-            most[1] = max(most[1], uint32_t(min((m1 >> SPLIT) + 1, u64(0xffffffffu))));
+            const uint4 x = ld_peer_quad(map_peer(smem_addr(&s.hi[4 * threadIdx.x]), r));
+            const uint4 y = ld_peer_quad(map_peer(smem_addr(&s.lo[4 * threadIdx.x]), r));
+            const u64 n[4] = {joined(x.x, y.x), joined(x.y, y.y), joined(x.z, y.z), joined(x.w, y.w)};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                m[q] += n[q];
+                most[q] = max(most[q], uint32_t(min((n[q] >> SPLIT) + 1, u64(0xffffffffu))));
+            }
         }
     }
     // The bin that the target (a count, or `p` times the total) falls in, what lies before
@@ -583,14 +587,14 @@ struct Row {
                          bool first, u64 before) {
         if (threadIdx.x == 0) s.pick_bin = BINS;
         u64 total;
-        u64 at = before + block_scan(m[0] + m[1], s.red, &total);
+        u64 at = before + block_scan((m[0] + m[1]) + (m[2] + m[3]), s.red, &total);
         if (first) *target = by_mass ? p * double(total) : p;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < 4; ++q) {
             // a target of 0 keeps the first token all the same
             const bool starts = double(at) < *target || at == 0;
             if (m[q] && starts && double(at + m[q]) >= *target) {
-                s.pick_bin = 2 * threadIdx.x + q;
+                s.pick_bin = 4 * threadIdx.x + q;
                 s.pick_most = most[q];
                 s.pick_before = at;
             }
@@ -631,10 +635,8 @@ struct Row {
                 if (at < uint32_t(k)) ++bin, at += n.y;
                 if (at < uint32_t(k)) ++bin, at += n.z;
                 if (at < uint32_t(k)) ++bin;
-                // distances of the bin lie below (bin + 1/2) / 4 c; a little more for the roundings
-                const float far = __fmul_ru(
-                    __fdiv_ru(float(bin) + 0.5f, __fmul_rd(c, TOPS_PER_OCTAVE)), 1.00001f);
-                s.from = !past || bin == TOPS - 1 ? -CUDART_INF_F : __fsub_rd(top, far);
+                s.from = !past || bin == TOPS - 1 ? -CUDART_INF_F
+                                                  : lower_edge(float(bin), TOPS_PER_OCTAVE);
             }
         }
         __syncthreads();
@@ -697,7 +699,7 @@ struct Row {
         if (p < 1.f && t > 0 && before >= u64(__double2ull_ru(double(p) * double(W)))) w = 0;
         if (!(e >= least)) w = 0;
         // the kept masses by index
-        u64* by_index = reinterpret_cast<u64*>(s.hi);
+        u64* by_index = reinterpret_cast<u64*>(s.lo);
         if (t < k) by_index[t] = (u64(uint32_t(idx)) << 32) | w;
         const u64 part = warp_add((u64(w > 0) << 48) + w);
         if (lane == 0) s.seg_mass[warp] = part;
@@ -731,7 +733,9 @@ struct Row {
     // ------------------------------------------------------------ the cut ----
 
     __device__ void clear_histogram() {
-        for (int i = threadIdx.x; i < BINS; i += THREADS) s.cnt[i] = 0, s.hi[i] = 0, s.lo[i] = 0;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        reinterpret_cast<uint4*>(s.hi)[threadIdx.x] = zero;
+        reinterpret_cast<uint4*>(s.lo)[threadIdx.x] = zero;
     }
     // Adds a mass (none where it is 0) to a bin.
     __device__ __forceinline__ void add_bin(uint32_t b, uint32_t w) {
@@ -749,21 +753,28 @@ struct Row {
         }
     }
 
-    // The histogram of masses of all tokens; the model's mass on the way where `model` is
-    // given.  Without a softcap the bin comes from the exponent: 2^23 - 16 d rounds to it.
-    __device__ void histogram(Model* model) {
-        const bool same = c == a.K;
+    // How a pass sums the model's mass: not at all, from the row's own shares (T = 1), or from
+    // its own exponentials.
+    enum { NO_MODEL, SAME, APART };
+    template <int MODEL>
+    __device__ __forceinline__ void model_of(Model& m, const float* v, const float* sh) const {
+        if constexpr (MODEL == SAME) m.add(sh);
+        if constexpr (MODEL == APART) add_model(m, v);
+    }
+
+    // The histogram of masses of all tokens.  Without a softcap the bin comes from the
+    // exponent: 2^23 - 32 d rounds to it.
+    template <int MODEL>
+    __device__ u64 histogram() {
         const hl::f2 slope = hl::pk1(-PER_OCTAVE), magic = hl::pk1(8388608.f);
+        Model m;
         for (int i = s0 + lane; i < s1; i += 32) {
             float v[EPW], sh[EPW];
             hl::f2 d[PAIRS];
             uint32_t w[EPW];
             values(i, v);
             shares(v, d, sh);
-            if (model) {
-                if (same) model->add(sh);
-                else add_model(*model, v);
-            }
+            model_of<MODEL>(m, v, sh);
             weights(sh, w);
 #pragma unroll
             for (int j = 0; j < PAIRS; ++j) {
@@ -779,6 +790,7 @@ struct Row {
                 add_bin(b[1], w[2 * j + 1]);
             }
         }
+        return MODEL == NO_MODEL ? 0 : model_sum(m);
     }
 
     // The cut after the first tokens of the order, among those inside `within`, before which
@@ -795,6 +807,7 @@ struct Row {
         for (int level = 0;; ++level) {
             cluster_barrier();  // the last histogram's readers are done
             clear_histogram();
+            reinterpret_cast<uint4*>(s.cnt)[threadIdx.x] = make_uint4(0, 0, 0, 0);
             __syncthreads();
             for (int i = s0 + lane; i < s1; i += 32) {
                 float v[EPW];
@@ -815,10 +828,11 @@ struct Row {
                 }
             }
             cluster_barrier();
-            u64 n[2], m[2];
-            uint32_t most[2], unused[2];
+            u64 n[4], m[4];
+            uint32_t most[4], unused[4];
             join_counts(n, most);
             if (by_mass) join_masses(m, unused);
+            cluster_barrier();  // the counts were read: the list's place is free
             pick(by_mass ? m : n, most, by_mass, by_mass ? double(p) : double(k), &target, level == 0,
                  before);
             bin = s.pick_bin;
@@ -1022,8 +1036,8 @@ struct Row {
     }
 
     // No filter: the masses of everything.
-    __device__ void sum_all(bool want, u64 model) {
-        const bool same = c == a.K;
+    template <int MODEL>
+    __device__ void sum_all() {
         Model m;
         u64 mass = 0;
         uint32_t kept = 0;
@@ -1033,10 +1047,7 @@ struct Row {
             uint32_t w[EPW];
             values(i, v);
             shares(v, d, sh);
-            if (want) {
-                if (same) m.add(sh);
-                else add_model(m, v);
-            }
+            model_of<MODEL>(m, v, sh);
             weights(sh, w);
 #pragma unroll
             for (int j = 0; j < EPW; j += 2) {
@@ -1044,7 +1055,7 @@ struct Row {
                 kept += min(w[j], 1u) + min(w[j + 1], 1u);
             }
         }
-        keep_segment(mass, kept, want ? model_sum(m) : model);
+        keep_segment(mass, kept, MODEL == NO_MODEL ? 0 : model_sum(m));
     }
 
     // The masses of what the cut and min-p leave.
@@ -1075,21 +1086,24 @@ struct Row {
         keep_segment(mass, kept, want ? model_sum(m) : model);
     }
 
-    // The masses of the bins above `bin` (and of min-p), the bin's tokens to the leader.
+    // The masses of the bins above `bin` (and of min-p), the bin's tokens to the leader.  Words
+    // with nothing at or above the bin's lower edge are passed over.
     __device__ void sum_above(uint32_t bin, float least, u64 model) {
         const hl::f2 slope = hl::pk1(-PER_OCTAVE), magic = hl::pk1(8388608.f);
         const float edge = 8388608.f + float(bin);
+        const float from = lower_edge(float(bin), PER_OCTAVE);
         u64 mass = 0;
         uint32_t kept = 0;
-        for (int i = s0 + lane; i < s1; i += 32) {
+        for (int i0 = s0; i0 < s1; i0 += 32) {
+            const int i = i0 + lane;
+            const uint4 q4 = i < s1 ? word(i) : make_uint4(E::LOWEST, E::LOWEST, E::LOWEST, E::LOWEST);
+            if (!__any_sync(FULL, E::top(E::word_max(q4)) >= from)) continue;
             float v[EPW], sh[EPW];
             hl::f2 d[PAIRS];
             uint32_t w[EPW];
-            values(i, v);
+            unpack(q4, v, !RES);
             shares(v, d, sh);
             weights(sh, w);
-            bool on_edge = false;
-            [[maybe_unused]] float bins[EPW];
 #pragma unroll
             for (int j = 0; j < PAIRS; ++j) {
                 float at[2];
@@ -1106,17 +1120,10 @@ struct Row {
                     const bool in = at[q] < edge && sh[e] >= least;
                     both += in ? w[e] : 0u;
                     kept += in && (!CAPPED || w[e]);
-                    on_edge |= at[q] == edge;
-                    if constexpr (CAPPED) bins[e] = at[q];
+                    if (at[q] == edge && w[e]) append(v[e], index(i, e));
                 }
                 mass += both;
             }
-            if (on_edge)
-                for (int e = 0; e < EPW; ++e) {
-                    const float x = CAPPED ? bins[e]
-                                           : __fmaf_rn(__fmul_rn(__fsub_rn(v[e], zm), c), -PER_OCTAVE, 8388608.f);
-                    if (x == edge && w[e]) append(v[e], index(i, e));
-                }
         }
         keep_segment(mass, kept, model);
     }
@@ -1297,18 +1304,20 @@ __global__ void __launch_bounds__(THREADS, 4) sample_kernel(const __grid_constan
     const Cut none{0u, 0x7fffffff};
     const bool want = a.logprobs != nullptr;
     if (k == a.V && !(p < 1.f)) {
-        if (least == 0.f) r.sum_all(want, 0);
-        else r.sum_kept(none, least, want, 0);
+        if (least != 0.f) r.sum_kept(none, least, want, 0);
+        else if (!want) r.template sum_all<R::NO_MODEL>();
+        else if (r.c == a.K) r.template sum_all<R::SAME>();
+        else r.template sum_all<R::APART>();
         if (!r.leave()) r.finish(none, least, u);
         return;
     }
     if (k == a.V) {
-        typename R::Model m;
-        r.histogram(want ? &m : nullptr);
-        const u64 model = want ? r.model_sum(m) : 0;
+        const u64 model = !want           ? r.template histogram<R::NO_MODEL>()
+                          : r.c == a.K ? r.template histogram<R::SAME>()
+                                       : r.template histogram<R::APART>();
         cluster_barrier();
-        u64 n[2];
-        uint32_t most[2];
+        u64 n[4];
+        uint32_t most[4];
         r.join_masses(n, most);
         double target;
         r.pick(n, most, true, double(p), &target, true, 0);

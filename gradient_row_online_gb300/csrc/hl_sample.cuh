@@ -49,7 +49,7 @@ constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
 constexpr int MAXC = 8;       // CTAs a cluster at most
 constexpr int BINS = 4 * THREADS;
-constexpr int CAP = 1024;     // tokens the leader can rank
+constexpr int CAP = 832;      // tokens the leader can rank
 constexpr int RANKED = 256;   // ranked by comparison with all; more are sorted
 constexpr int MAX_TOPK = 128; // longest top-k that takes the thread-maxima bound
 constexpr int SEGS = MAXC * WARPS;
@@ -90,8 +90,15 @@ struct Shared {
         u64 list[CAP];     // (key << 32 | ~index) of the tokens to rank, a run a CTA (leader)
         uint32_t cnt[BINS];  // histogram of counts
     };
-    uint32_t hi[BINS];     // histogram of masses, above and below bit SPLIT; afterwards the
-    uint32_t lo[BINS];     // place where lists are ranked
+    u64 groups[MAXC][32];  // the CTAs' histograms by groups of 32 bins
+    union {
+        struct {
+            uint32_t hi[BINS];  // histogram of masses, above and below bit SPLIT
+            uint32_t lo[BINS];
+        };
+        uint32_t tops[TOPS];  // histogram of the thread maxima
+        u64 rank[BINS];       // where lists are ranked
+    };
     u64 xch[2][MAXC];      // exchanges of one value a CTA
     u64 seg_mass[SEGS];    // the segments' kept masses, the model's, and counts (leader)
     u64 seg_model[SEGS];
@@ -99,14 +106,14 @@ struct Shared {
     u64 my_mass[WARPS];    // the CTA's own segments
     u64 my_model[WARPS];
     uint32_t my_kept[WARPS];
-    uint32_t tops[TOPS];   // histogram of the thread maxima
     float from;
+    double target;
     uint32_t list_n[MAXC];
     u64 red[WARPS];
     uint32_t ired[WARPS];
     uint32_t n_local;
     uint32_t pick_bin, pick_most;
-    u64 pick_before, pick_total;
+    u64 pick_before;
     uint32_t cut_key;
     int cut_idx;
     u64 fin[4];
@@ -258,6 +265,11 @@ __device__ __forceinline__ void st_peer64(uint32_t addr, u64 v) {
 }
 __device__ __forceinline__ void st_peer32(uint32_t addr, uint32_t v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_peer32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
 }
 __device__ __forceinline__ uint4 ld_peer_quad(uint32_t addr) {
     uint4 v;
@@ -515,90 +527,93 @@ struct Row {
             return s.list[r * run + i];
         };
         if (n <= RANKED) {
-            u64* all = reinterpret_cast<u64*>(s.hi);
-            u64* sorted = all + RANKED;
+            u64* sorted = s.rank + RANKED;
             const u64 mine = int(threadIdx.x) < n ? at(threadIdx.x) : 0;
-            if (int(threadIdx.x) < n) all[threadIdx.x] = mine;
+            if (int(threadIdx.x) < n) s.rank[threadIdx.x] = mine;
             __syncthreads();
             if (int(threadIdx.x) < n) {
                 int better = 0;
 #pragma unroll 4
-                for (int j = 0; j < n; ++j) better += all[j] > mine;
+                for (int j = 0; j < n; ++j) better += s.rank[j] > mine;
                 sorted[better] = mine;
             }
             __syncthreads();
             return sorted;
         }
-        u64 v[CAP / THREADS];
-#pragma unroll
-        for (int q = 0; q < CAP / THREADS; ++q) {
-            const int i = q * THREADS + threadIdx.x;
-            v[q] = i < n ? at(i) : 0;
-        }
-        __syncthreads();
+        static_assert(CAP <= BINS, "a list fits the histograms' place");
         int m = 2 * RANKED;
         while (m < n) m <<= 1;
-#pragma unroll
-        for (int q = 0; q < CAP / THREADS; ++q) s.list[q * THREADS + threadIdx.x] = v[q];
+        for (int i = threadIdx.x; i < m; i += THREADS) s.rank[i] = i < n ? at(i) : 0;
         __syncthreads();
         for (int size = 2; size <= m; size <<= 1)
             for (int step = size >> 1; step; step >>= 1) {
                 for (int i = threadIdx.x; i < m / 2; i += THREADS) {
                     const int lo = 2 * i - (i & (step - 1)), hi = lo + step;
-                    const u64 x = s.list[lo], y = s.list[hi];
-                    if ((x < y) == ((lo & size) == 0)) s.list[lo] = y, s.list[hi] = x;
+                    const u64 x = s.rank[lo], y = s.rank[hi];
+                    if ((x < y) == ((lo & size) == 0)) s.rank[lo] = y, s.rank[hi] = x;
                 }
                 __syncthreads();
             }
-        return s.list;
+        return s.rank;
     }
 
-    // The thread's four bins of the joined histograms.
-    __device__ __forceinline__ void join_counts(u64* n, uint32_t* most) const {
-        for (int q = 0; q < 4; ++q) n[q] = most[q] = 0;
-        for (int r = 0; r < C; ++r) {
-            const uint4 x = ld_peer_quad(map_peer(smem_addr(&s.cnt[4 * threadIdx.x]), r));
-            const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) n[q] += y[q], most[q] = max(most[q], y[q]);
-        }
-    }
     // A bin's mass from its two sums.
     __device__ __forceinline__ static u64 joined(uint32_t hi, uint32_t lo) {
         return (u64(hi) << (RES ? SPLIT : 32)) + lo;
     }
-    // `most`: the largest of a CTA's masses in the bin, in 2^SPLIT rounded up.
-    __device__ __forceinline__ void join_masses(u64* m, uint32_t* most) const {
-        for (int q = 0; q < 4; ++q) m[q] = most[q] = 0;
-        for (int r = 0; r < C; ++r) {
-            const uint4 x = ld_peer_quad(map_peer(smem_addr(&s.hi[4 * threadIdx.x]), r));
-            const uint4 y = ld_peer_quad(map_peer(smem_addr(&s.lo[4 * threadIdx.x]), r));
-            const u64 n[4] = {joined(x.x, y.x), joined(x.y, y.y), joined(x.z, y.z), joined(x.w, y.w)};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                m[q] += n[q];
-                most[q] = max(most[q], uint32_t(min((n[q] >> SPLIT) + 1, u64(0xffffffffu))));
-            }
+    // The bin of the cluster's histograms that the target (a count k, or p times the total, formed
+    // where `first`) falls in: s.pick_bin (BINS where the target is past them all), what lies
+    // before it over `before`, and the largest count of a CTA in it (COUNTS: where the
+    // counts were taken).  Every CTA tells the others its sums over groups of 32 bins and then
+    // reads the bins of one group from them: the histograms themselves would be
+    // twice the slice's bytes.  Collective; the peers' bins are read until the next barrier.
+    template <bool MASS, bool COUNTS>
+    __device__ void locate(double p, bool first, u64 before) {
+        __syncthreads();
+        const int t = threadIdx.x;
+        u64 sum;
+        if constexpr (MASS) {
+            const uint4 x = reinterpret_cast<const uint4*>(s.hi)[t], y = reinterpret_cast<const uint4*>(s.lo)[t];
+            sum = joined(x.x, y.x) + joined(x.y, y.y) + joined(x.z, y.z) + joined(x.w, y.w);
+        } else {
+            const uint4 x = reinterpret_cast<const uint4*>(s.cnt)[t];
+            sum = u64(x.x) + x.y + x.z + x.w;
         }
-    }
-    // The bin that the target (a count, or `p` times the total) falls in, what lies before
-    // it (over `before`), its `most`; BINS where the target is past them all.  Whole block.
-    __device__ void pick(const u64* m, const uint32_t* most, bool by_mass, double p, double* target,
-                         bool first, u64 before) {
-        if (threadIdx.x == 0) s.pick_bin = BINS;
-        u64 total;
-        u64 at = before + block_scan((m[0] + m[1]) + (m[2] + m[3]), s.red, &total);
-        if (first) *target = by_mass ? p * double(total) : p;
+        static_assert(BINS == 4 * THREADS && BINS == 32 * 32 && MAXC == 8, "eight threads a group");
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(FULL, sum, o);
+        if ((lane & 7) < C) st_peer64(map_peer(smem_addr(&s.groups[rank][t >> 3]), lane & 7), sum);
+        cluster_barrier();
+        if (warp == 0) {
+            u64 g = 0;
+            for (int r = 0; r < C; ++r) g += s.groups[r][lane];
+            u64 inc = warp_scan(g, lane);
+            const double target = !first ? s.target : MASS ? p * double(__shfl_sync(FULL, inc, 31)) : p;
+            if (lane == 0) s.pick_bin = BINS, s.target = target;
             // a target of 0 keeps the first token all the same
-            const bool starts = double(at) < *target || at == 0;
-            if (m[q] && starts && double(at + m[q]) >= *target) {
-                s.pick_bin = 4 * threadIdx.x + q;
-                s.pick_most = most[q];
-                s.pick_before = at;
+            auto holds = [&](u64 at, u64 m) {
+                return m && (double(at) < target || at == 0) && double(at + m) >= target;
+            };
+            u64 at = before + inc - g;
+            const unsigned hit = __ballot_sync(FULL, holds(at, g));
+            if (hit) {
+                const int group = __ffs(hit) - 1, bin = group * 32 + lane;
+                at = __shfl_sync(FULL, at, group);
+                u64 m = 0;
+                uint32_t most = 0;
+                for (int r = 0; r < C; ++r) {
+                    uint32_t n = 0;
+                    if constexpr (!MASS || COUNTS) n = ld_peer32(map_peer(smem_addr(&s.cnt[bin]), r));
+                    most = max(most, n);
+                    if constexpr (MASS)
+                        m += joined(ld_peer32(map_peer(smem_addr(&s.hi[bin]), r)),
+                                    ld_peer32(map_peer(smem_addr(&s.lo[bin]), r)));
+                    else m += n;
+                }
+                inc = warp_scan(m, lane);
+                at += inc - m;
+                if (holds(at, m)) s.pick_bin = uint32_t(bin), s.pick_most = most, s.pick_before = at;
             }
-            at += m[q];
         }
         __syncthreads();
     }
@@ -699,7 +714,7 @@ struct Row {
         if (p < 1.f && t > 0 && before >= u64(__double2ull_ru(double(p) * double(W)))) w = 0;
         if (!(e >= least)) w = 0;
         // the kept masses by index
-        u64* by_index = reinterpret_cast<u64*>(s.lo);
+        u64* by_index = s.rank;  // (the ranked list was read before the barrier)
         if (t < k) by_index[t] = (u64(uint32_t(idx)) << 32) | w;
         const u64 part = warp_add((u64(w > 0) << 48) + w);
         if (lane == 0) s.seg_mass[warp] = part;
@@ -827,19 +842,12 @@ struct Row {
                     if (by_mass) add_bin(b, w);
                 }
             }
-            cluster_barrier();
-            u64 n[4], m[4];
-            uint32_t most[4], unused[4];
-            join_counts(n, most);
-            if (by_mass) join_masses(m, unused);
+            if (by_mass) locate<true, true>(double(p), level == 0, before);
+            else locate<false, true>(double(k), level == 0, before);
             cluster_barrier();  // the counts were read: the list's place is free
-            pick(by_mass ? m : n, most, by_mass, by_mass ? double(p) : double(k), &target, level == 0,
-                 before);
+            target = s.target;
             bin = s.pick_bin;
-            if (bin == BINS) {  // the target is past all of them
-                cluster_barrier();
-                return within;
-            }
+            if (bin == BINS) return within;  // the target is past all of them
             const uint32_t some = s.pick_most;
             before = s.pick_before;
             if (level == 0) {
@@ -979,7 +987,7 @@ struct Row {
 
     // Leader: the last of a ranked list's tokens that stay (whole block).
     __device__ Cut cut_of(const u64* sorted, int n, bool by_mass, u64 before, double target) {
-        constexpr int Q = CAP / THREADS;
+        constexpr int Q = (CAP + THREADS - 1) / THREADS;
         u64 w[Q], mine = 0;
         const int i0 = threadIdx.x * Q;
 #pragma unroll
@@ -1126,6 +1134,28 @@ struct Row {
             }
         }
         keep_segment(mass, kept, model);
+    }
+
+    // Leader, whole block: the same once the bin of the cut is listed, with `before` the mass
+    // above it: the listed tokens inside the cut join their segments.
+    __device__ void finish_bin(u64 before, float least, double u) {
+        int count;
+        const u64* sorted = rank_list(&count);
+        const Cut cut = cut_of(sorted, count, true, before, s.target);
+        const float kv = of_key(cut.key);
+        for (int i = threadIdx.x; i < count; i += THREADS) {
+            const float v = of_key(uint32_t(sorted[i] >> 32));
+            const int idx = int(~uint32_t(sorted[i]));
+            const float sh = share(v);
+            if (!inside(v, idx, cut, kv) || !(sh >= least)) continue;
+            const int w = (idx + head) / EPW, cta = w / a.per;
+            const int have = min(nw, (cta + 1) * a.per) - cta * a.per;
+            const int g = cta * WARPS + (w - cta * a.per) / ((have + WARPS - 1) / WARPS);
+            atomicAdd(&s.seg_mass[g], u64(weight_of(sh)));
+            atomicAdd(&s.seg_kept[g], 1u);
+        }
+        __syncthreads();
+        finish(cut, least, u);
     }
 
     // Leader, whole block: the target's segment from the segments' masses, and the token by going
@@ -1315,44 +1345,21 @@ __global__ void __launch_bounds__(THREADS, 4) sample_kernel(const __grid_constan
         const u64 model = !want           ? r.template histogram<R::NO_MODEL>()
                           : r.c == a.K ? r.template histogram<R::SAME>()
                                        : r.template histogram<R::APART>();
-        cluster_barrier();
-        u64 n[4];
-        uint32_t most[4];
-        r.join_masses(n, most);
-        double target;
-        r.pick(n, most, true, double(p), &target, true, 0);
+        r.template locate<true, false>(double(p), true, 0);
         const uint32_t bin = s.pick_bin;
-        // how many tokens a CTA may have in it, by the least weight of the bin
-        const float light = fmaxf(1.f, UNIT * ex2f(-(float(bin) + 0.5f) / PER_OCTAVE) * 0.999f - 1.f);
-        const bool fits = bin < BINS - 1 &&
-                          float(s.pick_most) * float(1 << SPLIT) <= float(CAP / r.C) * light;
-        if (fits) {
-            const u64 before = s.pick_before;
+        const u64 before = s.pick_before;
+        if (bin < BINS - 1) {
             r.sum_above(bin, least, model);
             __syncthreads();
-            if (warp == 0) r.send_segments();
-            r.send_count();
-            cluster_barrier();  // (a wait for all: the histograms were read until here)
-            if (r.rank) return;
-            int count;
-            const u64* sorted = r.rank_list(&count);
-            const Cut cut = r.cut_of(sorted, count, true, before, target);
-            const float kv = of_key(cut.key);
-            for (int i = threadIdx.x; i < count; i += THREADS) {
-                const float v = of_key(uint32_t(sorted[i] >> 32));
-                const int idx = int(~uint32_t(sorted[i]));
-                const float sh = r.share(v);
-                if (!r.inside(v, idx, cut, kv) || !(sh >= least)) continue;
-                // its segment
-                const int w = (idx + r.head) / EPW, cta = w / a.per;
-                const int have = min(r.nw, (cta + 1) * a.per) - cta * a.per;
-                const int g = cta * WARPS + (w - cta * a.per) / ((have + WARPS - 1) / WARPS);
-                atomicAdd(&s.seg_mass[g], u64(weight_of(sh)));
-                atomicAdd(&s.seg_kept[g], 1u);
+            if (warp == 0) {
+                r.send_segments();
+                if (lane == 0) st_peer32(map_peer(smem_addr(&s.list_n[r.rank]), 0), s.n_local);
             }
-            __syncthreads();
-            r.finish(cut, least, u);
-            return;
+            const u64* all = r.template exchange<false>(s.n_local);
+            if (!__any_sync(FULL, lane < r.C && all[lane] > u64(CAP / r.C))) {
+                if (r.rank == 0) r.finish_bin(before, least, u);
+                return;
+            }
         }
         const Cut cut = r.resolve(true, 0, p, none);
         r.sum_kept(cut, least, false, model);

@@ -53,6 +53,7 @@ constexpr int CAP = 832;      // tokens the leader can rank
 constexpr int RANKED = 256;   // ranked by comparison with all; more are sorted
 constexpr int MAX_TOPK = 128; // longest top-k that takes the thread-maxima bound
 constexpr int SEGS = MAXC * WARPS;
+constexpr int QUEUE = MAXC * 64;
 constexpr float PER_OCTAVE = 32.f;  // bins an octave of mass
 constexpr int TOPS = 128;           // bins of the thread maxima,
 constexpr float TOPS_PER_OCTAVE = 4.f;
@@ -90,7 +91,10 @@ struct Shared {
         u64 list[CAP];     // (key << 32 | ~index) of the tokens to rank, a run a CTA (leader)
         uint32_t cnt[BINS];  // histogram of counts
     };
-    u64 groups[MAXC][32];  // the CTAs' histograms by groups of 32 bins
+    union {
+        u64 groups[MAXC][32];  // the CTAs' histograms by groups of 32 bins
+        int queue[MAXC * 64];  // words that hold tokens of the cut's bin
+    };
     union {
         struct {
             uint32_t hi[BINS];  // histogram of masses, above and below bit SPLIT
@@ -111,7 +115,7 @@ struct Shared {
     uint32_t list_n[MAXC];
     u64 red[WARPS];
     uint32_t ired[WARPS];
-    uint32_t n_local;
+    uint32_t n_local, queued;
     uint32_t pick_bin, pick_most;
     u64 pick_before;
     uint32_t cut_key;
@@ -752,16 +756,15 @@ struct Row {
         reinterpret_cast<uint4*>(s.hi)[threadIdx.x] = zero;
         reinterpret_cast<uint4*>(s.lo)[threadIdx.x] = zero;
     }
-    // Adds a mass (none where it is 0) to a bin.
+    // Adds a mass to a bin; `at` is the bin's place, a shared-memory address of its upper sum.
+    __device__ __forceinline__ void add_at(uint32_t at, uint32_t w) {
+        asm volatile("red.shared.add.u32 [%0 + %3], %1;\n\tred.shared.add.u32 [%0], %2;" ::"r"(at),
+                     "r"(w & ((1u << SPLIT) - 1)), "r"(w >> SPLIT), "n"(4 * BINS)
+                     : "memory");
+    }
     __device__ __forceinline__ void add_bin(uint32_t b, uint32_t w) {
         if constexpr (RES) {
-            asm volatile(
-                "{\n\t.reg .pred p, q;\n\t"
-                "setp.ne.u32 p, %1, 0;\n\tsetp.ne.u32 q, %2, 0;\n\t"
-                "@p red.shared.add.u32 [%0], %1;\n\t"
-                "@q red.shared.add.u32 [%3], %2;\n\t}" ::"r"(smem_addr(s.lo) + 4 * b),
-                "r"(w & ((1u << SPLIT) - 1)), "r"(w >> SPLIT), "r"(smem_addr(s.hi) + 4 * b)
-                : "memory");
+            if (w) add_at(smem_addr(s.hi) + 4 * b, w);
         } else if (w) {  // any number of tokens a CTA: 64 bits, the carry by hand
             const uint32_t old = atomicAdd(&s.lo[b], w);
             if (old + w < old) atomicAdd(&s.hi[b], 1u);
@@ -782,6 +785,10 @@ struct Row {
     template <int MODEL>
     __device__ u64 histogram() {
         const hl::f2 slope = hl::pk1(-PER_OCTAVE), magic = hl::pk1(8388608.f);
+        const uint32_t origin = smem_addr(s.hi) - 4 * 0x4b000000u;
+        // tokens without a mass (31 octaves down, -inf, NaN) add their 0 to a bin past all others, one a
+        // lane: predicated adds compiled to branches, three more instructions an add
+        const float none = 8388608.f + float(BINS - 32 + lane);
         Model m;
         for (int i = s0 + lane; i < s1; i += 32) {
             float v[EPW], sh[EPW];
@@ -793,16 +800,15 @@ struct Row {
             weights(sh, w);
 #pragma unroll
             for (int j = 0; j < PAIRS; ++j) {
-                uint32_t b[2];
-                if constexpr (CAPPED) {
-                    b[0] = bin_of(v[2 * j]), b[1] = bin_of(v[2 * j + 1]);
+                if constexpr (CAPPED || !RES) {
+                    add_bin(bin_of(v[2 * j]), w[2 * j]);
+                    add_bin(bin_of(v[2 * j + 1]), w[2 * j + 1]);
                 } else {
                     float x, y;
                     hl::upk(hl::fma2(d[j], slope, magic), x, y);
-                    b[0] = __float_as_uint(x) - 0x4b000000u, b[1] = __float_as_uint(y) - 0x4b000000u;
+                    add_at(__float_as_uint(fminf(x, none)) * 4 + origin, w[2 * j]);
+                    add_at(__float_as_uint(fminf(y, none)) * 4 + origin, w[2 * j + 1]);
                 }
-                add_bin(b[0], w[2 * j]);
-                add_bin(b[1], w[2 * j + 1]);
             }
         }
         return MODEL == NO_MODEL ? 0 : model_sum(m);
@@ -1096,6 +1102,7 @@ struct Row {
 
     // The masses of the bins above `bin` (and of min-p), the bin's tokens to the leader.  Words
     // with nothing at or above the bin's lower edge are passed over.
+    template <bool LEAST>
     __device__ void sum_above(uint32_t bin, float least, u64 model) {
         const hl::f2 slope = hl::pk1(-PER_OCTAVE), magic = hl::pk1(8388608.f);
         const float edge = 8388608.f + float(bin);
@@ -1106,34 +1113,52 @@ struct Row {
             const int i = i0 + lane;
             const uint4 q4 = i < s1 ? word(i) : make_uint4(E::LOWEST, E::LOWEST, E::LOWEST, E::LOWEST);
             if (!__any_sync(FULL, E::top(E::word_max(q4)) >= from)) continue;
-            float v[EPW], sh[EPW];
+            float v[EPW], sh[EPW], at[EPW];
             hl::f2 d[PAIRS];
             uint32_t w[EPW];
             unpack(q4, v, !RES);
             shares(v, d, sh);
             weights(sh, w);
+            bool on_edge = false;
 #pragma unroll
             for (int j = 0; j < PAIRS; ++j) {
-                float at[2];
                 if constexpr (CAPPED) {
-                    at[0] = 8388608.f + float(bin_of(v[2 * j]));
-                    at[1] = 8388608.f + float(bin_of(v[2 * j + 1]));
+                    at[2 * j] = 8388608.f + float(bin_of(v[2 * j]));
+                    at[2 * j + 1] = 8388608.f + float(bin_of(v[2 * j + 1]));
                 } else {
-                    hl::upk(hl::fma2(d[j], slope, magic), at[0], at[1]);
+                    hl::upk(hl::fma2(d[j], slope, magic), at[2 * j], at[2 * j + 1]);
                 }
                 uint32_t both = 0;
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int e = 2 * j + q;
-                    const bool in = at[q] < edge && sh[e] >= least;
-                    both += in ? w[e] : 0u;
-                    kept += in && (!CAPPED || w[e]);
-                    if (at[q] == edge && w[e]) append(v[e], index(i, e));
+                for (int e = 2 * j; e < 2 * j + 2; ++e) {
+                    bool in = at[e] < edge;
+                    if constexpr (LEAST) in = in && sh[e] >= least;
+                    if constexpr (CAPPED) in = in && w[e];
+                    if (in) both += w[e], ++kept;
+                    on_edge |= at[e] == edge;
                 }
                 mass += both;
             }
+            if (on_edge) {
+                const uint32_t n = atomicAdd(&s.queued, 1u);
+                if (n < QUEUE) s.queue[n] = i;
+            }
         }
         keep_segment(mass, kept, model);
+        __syncthreads();
+        // the words that hold tokens of the bin (few), a thread a word
+        const uint32_t n = s.queued;
+        if (n > QUEUE && threadIdx.x == 0) s.n_local = CAP + 1;  // too many: the call's caller sees it
+        for (uint32_t j = threadIdx.x; j < min(n, uint32_t(QUEUE)); j += THREADS) {
+            const int i = s.queue[j];
+            float v[EPW];
+            values(i, v);
+            for (int e = 0; e < EPW; ++e) {
+                const float x = CAPPED ? 8388608.f + float(bin_of(v[e]))
+                                       : __fmaf_rn(__fmul_rn(__fsub_rn(v[e], zm), c), -PER_OCTAVE, 8388608.f);
+                if (x == edge && weight_of(share(v[e]))) append(v[e], index(i, e));
+            }
+        }
     }
 
     // Leader, whole block: the same once the bin of the cut is listed, with `before` the mass
@@ -1266,7 +1291,7 @@ __global__ void __launch_bounds__(THREADS, 4) sample_kernel(const __grid_constan
     const int want_k = a.top_k ? a.top_k[r.row] : 0;
     const float p = a.top_p ? a.top_p[r.row] : 1.f;
     const float least = a.min_p ? a.min_p[r.row] : 0.f;
-    if (threadIdx.x == 0) s.n_local = 0;
+    if (threadIdx.x == 0) s.n_local = s.queued = 0;
     const u64 ubits = u64(__double_as_longlong(u));  // in [0, 1): below 1.0's bits (or -0)
     const bool bad = !(temp >= 0.f && temp < CUDART_INF_F) ||
                      !(ubits < 0x3ff0000000000000ull || ubits == 0x8000000000000000ull) ||
@@ -1349,7 +1374,8 @@ __global__ void __launch_bounds__(THREADS, 4) sample_kernel(const __grid_constan
         const uint32_t bin = s.pick_bin;
         const u64 before = s.pick_before;
         if (bin < BINS - 1) {
-            r.sum_above(bin, least, model);
+            if (least == 0.f) r.template sum_above<false>(bin, least, model);
+            else r.template sum_above<true>(bin, least, model);
             __syncthreads();
             if (warp == 0) {
                 r.send_segments();

@@ -59,15 +59,14 @@ struct Batch {
 
 struct Sync {
     unsigned arrived, generation;
-    float norm, factor;
+    float factor;
     double parts[MAX_GRID];
 };
 
 struct Call {
     int n;            // entries
     uint32_t tiles;
-    double max_norm;
-    float inv_scale;
+    float max_norm, inv_scale;
     float* stats;
     Sync* sync;
 };
@@ -146,43 +145,83 @@ struct Type<HEADLOSS_FP16> {
 
 // -------------------------------------------------------------------- tiles ----
 
-// Where a tile's words lie: word w of the tensor starts at base + 16 w, base the tensor's
-// address rounded down, head elements of word 0 before it.
-struct Place {
-    const char* base;
-    int64_t w0;      // the tile's first word
-    int words;       // of the tile, 1 .. TILE
-    int head;
-    bool whole;      // every word of the tile lies inside the tensor
+// A lane's part of a tile.  Word w of the tensor starts at its address rounded down to 16
+// bytes + 16 w; the words inside the tensor are the tile's [k0, k1), and of the two that may reach
+// outside it (the tensor's first and last) a lane has one element at most.
+struct Part {
+    const uint4* words;  // the tile's first word
+    int k0, k1;
+    int64_t at;          // element of the tensor at the tile's first word
+    int64_t edge;        // the lane's element of a word at an end, or -1
 };
 
 template <int D>
-__device__ __forceinline__ Place place_of(const Entry& t, uint32_t tile) {
+__device__ __forceinline__ Part part_of(const Entry& t, uint32_t tile, int lane) {
     constexpr int EPW = Type<D>::EPW, ES = 16 / EPW;
     const uintptr_t at = reinterpret_cast<uintptr_t>(t.grad);
-    Place p;
-    p.base = reinterpret_cast<const char*>(at & ~uintptr_t(15));
-    p.head = int(at & 15) / ES;
-    const int64_t all = (p.head + t.n + EPW - 1) / EPW;
-    p.w0 = int64_t(tile - t.first) * TILE;
-    p.words = all - p.w0 < TILE ? int(all - p.w0) : TILE;
-    p.whole = p.words == TILE && (p.w0 > 0 || p.head == 0) &&
-              ((p.w0 + TILE) * EPW <= p.head + t.n);
+    const int head = int(at & 15) / ES;
+    const int64_t w0 = int64_t(tile - t.first) * TILE;
+    Part p;
+    p.words = reinterpret_cast<const uint4*>(at & ~uintptr_t(15)) + w0;
+    p.at = w0 * EPW - head;
+    const int64_t left = t.n - p.at;  // elements from the tile's first word on
+    p.k0 = p.at < 0 ? 1 : 0;
+    p.k1 = left < int64_t(TILE) * EPW ? int(left) / EPW : TILE;
+    p.edge = -1;
+    if (p.k0) {  // the word before [k0, k1)
+        if (lane < EPW && lane >= head && lane - head < t.n) p.edge = lane - head;
+    }
+    if (left < int64_t(TILE) * EPW && left % EPW && p.k1 >= p.k0) {  // the word after it
+        const int e = lane - 16;
+        if (e >= 0 && e < int(left % EPW)) p.edge = p.at + int64_t(p.k1) * EPW + e;
+    }
     return p;
 }
 
-// A lane's eight words of a whole tile.
-__device__ __forceinline__ void load_tile(const Place& p, int lane, uint4* d) {
-    const uint4* w = reinterpret_cast<const uint4*>(p.base) + p.w0;
+// Any tile word by word: a lane's sum of squares of values times `by`, or the values times `by` to
+// out.  For sums that left fp32's range and outputs off the gradient's 16-byte grid.
+template <int D>
+__device__ __noinline__ float any_tile(const Entry& t, uint32_t tile, int lane, float by, bool store) {
+    constexpr int EPW = Type<D>::EPW;
+    using T = typename Type<D>::T;
+    const Part p = part_of<D>(t, tile, lane);
+    T* y = static_cast<T*>(t.out);
+    float s = 0.f;
+    if (p.edge >= 0) {
+        const float v = Type<D>::up(static_cast<const T*>(t.grad)[p.edge]) * by;
+        s = v * v;
+        if (store) y[p.edge] = Type<D>::down(v);
+    }
+    for (int k = lane; k < p.k1; k += 32) {  // (the lane's words, as in sum_tile)
+        if (k < p.k0) continue;
+        float v[EPW];
+        Type<D>::unpack(p.words[k], v);
 #pragma unroll
-    for (int i = 0; i < LANE_WORDS; ++i) d[i] = w[i * 32 + lane];
+        for (int e = 0; e < EPW; ++e) {
+            v[e] *= by;
+            s = fmaf(v[e], v[e], s);
+            if (store) y[p.at + int64_t(k) * EPW + e] = Type<D>::down(v[e]);
+        }
+    }
+    return s;
 }
 
-// Sum of a lane's squares of a whole tile.
+// A lane's words and element of a tile (0 where it has none) to d and `edge`, and its sum of
+// squares in fp64: fp32 over the tile's share, from scaled values where that left fp32's range
+// or came near its lower end.
 template <int D>
-__device__ __forceinline__ float squares(const uint4* d) {
+__device__ __forceinline__ double sum_tile(const Entry& t, uint32_t tile, int lane, uint4* d,
+                                           float* edge) {
     constexpr int EPW = Type<D>::EPW;
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    const Part p = part_of<D>(t, tile, lane);
+#pragma unroll
+    for (int i = 0; i < LANE_WORDS; ++i) {
+        const int k = i * 32 + lane;
+        d[i] = make_uint4(0, 0, 0, 0);
+        if (k >= p.k0 && k < p.k1) d[i] = p.words[k];
+    }
+    *edge = p.edge >= 0 ? Type<D>::up(static_cast<const typename Type<D>::T*>(t.grad)[p.edge]) : 0.f;
+    float s[4] = {*edge * *edge, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < LANE_WORDS; ++i) {
         float v[EPW];
@@ -190,95 +229,44 @@ __device__ __forceinline__ float squares(const uint4* d) {
 #pragma unroll
         for (int e = 0; e < EPW; ++e) s[e & 3] = fmaf(v[e], v[e], s[e & 3]);
     }
-    return (s[0] + s[1]) + (s[2] + s[3]);
-}
-
-// out's words of a whole tile, where out lies on the 16-byte grid as grad does.
-template <int D>
-__device__ __forceinline__ void store_tile(uint4* out, int lane, const uint4* d, float factor) {
-    constexpr int EPW = Type<D>::EPW;
-#pragma unroll
-    for (int i = 0; i < LANE_WORDS; ++i) {
-        float v[EPW];
-        Type<D>::unpack(d[i], v);
-#pragma unroll
-        for (int e = 0; e < EPW; ++e) v[e] *= factor;
-        __stcs(out + i * 32 + lane, Type<D>::pack(v));
-    }
-}
-
-// Any tile word by word: a lane's sum of squares of values times `by` (out = nullptr), or the
-// values times `by` to out.  The ends of a tensor, tensors whose output lies off the
-// gradient's 16-byte grid, and sums that left fp32's range.
-template <int D>
-__device__ __noinline__ float any_tile(const Entry& t, uint32_t tile, int lane, float by, bool store) {
-    constexpr int EPW = Type<D>::EPW;
-    using T = typename Type<D>::T;
-    const Place p = place_of<D>(t, tile);
-    const T* x = static_cast<const T*>(t.grad);
-    T* y = static_cast<T*>(t.out);
-    float s = 0.f;
-    for (int k = lane; k < p.words; k += 32) {
-        const int64_t first = (p.w0 + k) * EPW - p.head;  // element of the tensor
-        float v[EPW];
-        if (first >= 0 && first + EPW <= t.n) {
-            Type<D>::unpack(reinterpret_cast<const uint4*>(p.base)[p.w0 + k], v);
-        } else {
-#pragma unroll
-            for (int e = 0; e < EPW; ++e)
-                v[e] = first + e >= 0 && first + e < t.n ? Type<D>::up(x[first + e]) : 0.f;
-        }
-#pragma unroll
-        for (int e = 0; e < EPW; ++e) {
-            v[e] *= by;
-            s = fmaf(v[e], v[e], s);
-        }
-        if (!store) continue;
-        if (first >= 0 && first + EPW <= t.n &&
-            (reinterpret_cast<uintptr_t>(y + first) & 15) == 0) {
-            __stcs(reinterpret_cast<uint4*>(y + first), Type<D>::pack(v));
-        } else {
-#pragma unroll
-            for (int e = 0; e < EPW; ++e)
-                if (first + e >= 0 && first + e < t.n) y[first + e] = Type<D>::down(v[e]);
-        }
-    }
-    return s;
-}
-
-// A lane's sum of a tile's squares in fp64, from scaled values where the plain sum left fp32's
-// range or came near its lower end.  Whole tiles stay in d.
-template <int D>
-__device__ __forceinline__ double sum_tile(const Entry& t, uint32_t tile, int lane, uint4* d,
-                                           bool* whole) {
-    const Place p = place_of<D>(t, tile);
-    float s;
-    *whole = p.whole;
-    if (p.whole) {
-        load_tile(p, lane, d);
-        s = squares<D>(d);
-    } else {
-        s = any_tile<D>(t, tile, lane, 1.f, false);
-    }
-    if (s >= 1e-24f && s <= 1e36f) return double(s);
-    const bool low = s < 1e-24f;
+    const float sum = (s[0] + s[1]) + (s[2] + s[3]);
+    if (sum >= 1e-24f && sum <= 1e36f) return double(sum);
+    const bool low = sum < 1e-24f;
     return double(any_tile<D>(t, tile, lane, low ? 0x1p+60f : 0x1p-70f, false)) *
            (low ? 0x1p-120 : 0x1p+140);
 }
 
-// The clipped tile; `here`: it is in d.
+// The clipped tile; `here`: the lane's part is in d and `edge`.
 template <int D>
 __device__ __forceinline__ void clip_tile(const Entry& t, uint32_t tile, int lane, uint4* d,
-                                          bool here, float factor) {
-    constexpr int EPW = Type<D>::EPW, ES = 16 / EPW;
-    const Place p = place_of<D>(t, tile);
-    char* at = static_cast<char*>(t.out) + (p.w0 * EPW - p.head) * ES;
-    if (!p.whole || (reinterpret_cast<uintptr_t>(at) & 15)) {
+                                          float edge, bool here, float factor) {
+    constexpr int EPW = Type<D>::EPW;
+    using T = typename Type<D>::T;
+    const Part p = part_of<D>(t, tile, lane);
+    T* y = static_cast<T*>(t.out);
+    if (reinterpret_cast<uintptr_t>(y + p.at) & 15) {
         any_tile<D>(t, tile, lane, factor, true);
         return;
     }
-    if (!here) load_tile(p, lane, d);
-    store_tile<D>(reinterpret_cast<uint4*>(at), lane, d, factor);
+    if (!here) {
+#pragma unroll
+        for (int i = 0; i < LANE_WORDS; ++i) {
+            const int k = i * 32 + lane;
+            if (k >= p.k0 && k < p.k1) d[i] = p.words[k];
+        }
+        if (p.edge >= 0) edge = Type<D>::up(static_cast<const T*>(t.grad)[p.edge]);
+    }
+    uint4* out = reinterpret_cast<uint4*>(y + p.at);
+#pragma unroll
+    for (int i = 0; i < LANE_WORDS; ++i) {
+        const int k = i * 32 + lane;
+        float v[EPW];
+        Type<D>::unpack(d[i], v);
+#pragma unroll
+        for (int e = 0; e < EPW; ++e) v[e] *= factor;
+        if (k >= p.k0 && k < p.k1) __stcs(out + k, Type<D>::pack(v));
+    }
+    if (p.edge >= 0) y[p.edge] = Type<D>::down(edge * factor);
 }
 
 // ------------------------------------------------------------------- kernel ----
@@ -334,67 +322,82 @@ __global__ void __launch_bounds__(THREADS, 2) clip_kernel(const __grid_constant_
 
     uint4 d[LANE_WORDS];
     double mine = 0.0;
-    uint32_t last = 0xffffffffu;  // the warp's last tile, in d where it is whole
-    bool here = false;
+    uint32_t last = 0xffffffffu;  // the warp's last tile, in d and edge
+    float edge = 0.f;
     for (uint32_t t = t0 + warp; t < t1; t += WARPS) {
         while (at + 1 < c.n && list.e[at + 1].first <= t) ++at;
         const Entry& e = list.e[at];
-        if (e.dtype == HEADLOSS_BF16) mine += sum_tile<HEADLOSS_BF16>(e, t, lane, d, &here);
-        else if (e.dtype == HEADLOSS_FP32) mine += sum_tile<HEADLOSS_FP32>(e, t, lane, d, &here);
-        else mine += sum_tile<HEADLOSS_FP16>(e, t, lane, d, &here);
+        if (e.dtype == HEADLOSS_BF16) mine += sum_tile<HEADLOSS_BF16>(e, t, lane, d, &edge);
+        else if (e.dtype == HEADLOSS_FP32) mine += sum_tile<HEADLOSS_FP32>(e, t, lane, d, &edge);
+        else mine += sum_tile<HEADLOSS_FP16>(e, t, lane, d, &edge);
         last = t;
     }
     mine = block_sum(mine);
 
     Sync* s = c.sync;
     if (threadIdx.x == 0) {
-        s->parts[blockIdx.x] = mine;
-        const unsigned before = load_acquire(&s->generation);
-        __threadfence();
-        s_last = atomicAdd(&s->arrived, 1u) == gridDim.x - 1;
-        __threadfence();
-        if (!s_last) {
-            const unsigned long long began = now_ns();
-            bool given_up = false;
-            while (load_acquire(&s->generation) == before)
-                if (now_ns() - began > WAIT_NS) {
-                    given_up = true;
-                    break;
-                }
-            s_factor = given_up ? 1.f : *reinterpret_cast<volatile float*>(&s->factor);
-            if (given_up) c.stats[0] = c.stats[1] = CUDART_NAN_F;
+        s_last = true;
+        if (gridDim.x > 1) {
+            s->parts[blockIdx.x] = mine;
+            const unsigned before = load_acquire(&s->generation);
+            __threadfence();
+            s_last = atomicAdd(&s->arrived, 1u) == gridDim.x - 1;
+            __threadfence();
+            if (!s_last) {
+                const unsigned long long began = now_ns();
+                bool given_up = false;
+                while (load_acquire(&s->generation) == before)
+                    if (now_ns() - began > WAIT_NS) {
+                        given_up = true;
+                        break;
+                    }
+                s_factor = given_up ? 1.f : *reinterpret_cast<volatile float*>(&s->factor);
+                if (given_up) c.stats[0] = c.stats[1] = CUDART_NAN_F;
+            }
         }
     }
     __syncthreads();
     if (s_last) {
-        double v = 0.0;
-        for (int i = threadIdx.x; i < int(gridDim.x); i += THREADS)
-            v += reinterpret_cast<volatile double*>(s->parts)[i];
-        v = block_sum(v);
+        double v = mine;
+        if (gridDim.x > 1) {
+            v = 0.0;
+            for (int i = threadIdx.x; i < int(gridDim.x); i += THREADS)
+                v += reinterpret_cast<volatile double*>(s->parts)[i];
+            v = block_sum(v);
+        }
         if (threadIdx.x == 0) {
-            const double norm = double(c.inv_scale) * sqrt(v);
-            const float factor = norm > c.max_norm && isfinite(float(norm))
-                                     ? float(double(c.inv_scale) * (c.max_norm / norm))
-                                     : c.inv_scale;
-            c.stats[0] = float(norm), c.stats[1] = factor;
-            s->factor = factor;
-            s->arrived = 0;
+            float norm, factor = c.inv_scale;
+            if (v >= 1e-30 && v <= 1e36) {  // (fp64's root and division take long here)
+                norm = c.inv_scale * sqrtf(float(v));
+                if (norm > c.max_norm && isfinite(norm)) factor *= c.max_norm / norm;
+            } else {
+                const double wide = double(c.inv_scale) * sqrt(v);
+                norm = float(wide);
+                if (wide > double(c.max_norm) && isfinite(norm))
+                    factor = float(double(c.inv_scale) * (double(c.max_norm) / wide));
+            }
+            c.stats[0] = norm, c.stats[1] = factor;
             s_factor = factor;
-            __threadfence();
-            store_release(&s->generation, s->generation + 1);
+            if (gridDim.x > 1) {
+                s->factor = factor;
+                s->arrived = 0;
+                __threadfence();
+                store_release(&s->generation, s->generation + 1);
+            }
         }
     }
     __syncthreads();
     const float factor = s_factor;
 
     if (last == 0xffffffffu) return;
+    bool here = true;
     for (uint32_t t = last;; t -= WARPS) {
         while (list.e[at].first > t) --at;
         const Entry& e = list.e[at];
         if (factor != 1.f || e.grad != e.out) {
-            if (e.dtype == HEADLOSS_BF16) clip_tile<HEADLOSS_BF16>(e, t, lane, d, here, factor);
-            else if (e.dtype == HEADLOSS_FP32) clip_tile<HEADLOSS_FP32>(e, t, lane, d, here, factor);
-            else clip_tile<HEADLOSS_FP16>(e, t, lane, d, here, factor);
+            if (e.dtype == HEADLOSS_BF16) clip_tile<HEADLOSS_BF16>(e, t, lane, d, edge, here, factor);
+            else if (e.dtype == HEADLOSS_FP32) clip_tile<HEADLOSS_FP32>(e, t, lane, d, edge, here, factor);
+            else clip_tile<HEADLOSS_FP16>(e, t, lane, d, edge, here, factor);
         }
         here = false;
         if (t < t0 + WARPS) break;
@@ -411,7 +414,7 @@ int launch(const List<N>& list, const Call& call, int grid, cudaStream_t s) {
     attr[0].id = cudaLaunchAttributeCooperative;
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = grid > 1;
     void* args[] = {const_cast<List<N>*>(&list), const_cast<Call*>(&call)};
     if (cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&clip_kernel<N>), args) !=
         cudaSuccess) {
@@ -532,13 +535,17 @@ int headloss_clip_grads(headloss_clip_t h, const headloss_gradient* grads, int n
     Builder b{grads, n_grads};
     b.count();
     if (b.tiles >= (uint64_t(1) << 32) - MAX_GRID * WARPS) return HEADLOSS_ERR_ARG;
-    Call call{b.used, uint32_t(b.tiles), double(max_norm), inv_scale, stats_out, h->sync};
-    // a warp a tile as far as the grid goes
-    const int64_t want = (int64_t(b.tiles) + WARPS - 1) / WARPS;
+    Call call{b.used, uint32_t(b.tiles), max_norm, inv_scale, stats_out, h->sync};
+    // a warp a tile as far as the grid goes; a CTA alone takes two, which costs less than the
+    // grid's barrier
+    const int64_t want = b.tiles <= 2 * WARPS ? 1 : (int64_t(b.tiles) + WARPS - 1) / WARPS;
     const int grid = int(want < 1 ? 1 : want < h->grid ? want : h->grid);
     if (b.used <= 1) return launch_list<1>(b, call, grid, s);
+    if (b.used <= 16) return launch_list<16>(b, call, grid, s);
     if (b.used <= 64) return launch_list<64>(b, call, grid, s);
+    if (b.used <= 160) return launch_list<160>(b, call, grid, s);
     if (b.used <= 320) return launch_list<320>(b, call, grid, s);
+    if (b.used <= 512) return launch_list<512>(b, call, grid, s);
     if (b.used <= 960) return launch_list<960>(b, call, grid, s);
     Batch batch;
     int in_batch = 0, at = 0;

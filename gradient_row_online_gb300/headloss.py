@@ -7,6 +7,7 @@ is not built, every call raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -429,6 +430,13 @@ class HeadLoss:
             pass
 
 
+def _raw_stream(device: int) -> int:
+    """The current stream's handle, without the Stream object torch would make."""
+    import torch
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(device) if get else torch.cuda.current_stream(device).cuda_stream
+
+
 class HeadSampler:
     """headloss_sample on torch tensors: one token a row of `logits` (N x V, unit
     column stride, any row stride), from one uniform a row.
@@ -442,46 +450,60 @@ class HeadSampler:
         import torch
         self.softcap, self.logits_scale = float(softcap), float(logits_scale)
         self.err = torch.zeros(1, dtype=torch.int32, device=device)
-        self._settings = (("temperature", torch.float32), ("top_k", torch.int32),
-                          ("top_p", torch.float32), ("min_p", torch.float32))
+        self.device, self.index = self.err.device, self.err.get_device()
+        self._call = load_library().headloss_sample
+        self._empty = torch.empty
+        self._f32, self._i32 = torch.float32, torch.int32
+        self._f64, self._i64 = torch.float64, torch.int64
+        self._codes = {torch.float32: HEADLOSS_FP32, torch.bfloat16: HEADLOSS_BF16,
+                       torch.float16: HEADLOSS_FP16}
 
-    @staticmethod
-    def _given(name, a, dtype, shape, device):
-        import torch
+    def _given(self, name, a, dtype, N):
+        """The address of a setting (None: 0), and what keeps it alive."""
         if a is None:
-            return None
+            return None, None
         if isinstance(a, (int, float)):
-            return torch.full(shape, a, dtype=dtype, device=device)
-        if a.dtype != dtype or a.shape != shape or a.device != device or not a.is_contiguous():
-            raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} on "
-                             f"{device} is wanted")
-        return a
+            import torch
+            a = torch.full((N,), a, dtype=dtype, device=self.device)
+        elif (a.dtype is not dtype or a.dim() != 1 or a.numel() != N or
+              a.get_device() != self.index or not a.is_contiguous()):
+            raise ValueError(f"{name}: a contiguous {dtype} tensor of {N} on {self.device} is "
+                             "wanted")
+        return a.data_ptr(), a
 
     def __call__(self, logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=None,
                  out=None, stream=None):
-        import torch
-        if logits.dim() != 2 or logits.shape[1] < 1 or logits.device != self.err.device or (
-                logits.shape[1] > 1 and logits.stride(1) != 1):
+        if (logits.dim() != 2 or logits.get_device() != self.index or logits.shape[1] < 1 or
+                (logits.shape[1] > 1 and logits.stride(1) != 1)):
             raise ValueError("logits: an N x V tensor with unit column stride on "
-                             f"{self.err.device} is wanted")
+                             f"{self.device} is wanted")
         N, V = logits.shape
-        ld = logits.stride(0) if N > 1 else V
-        if logits.dtype not in (torch.float32, torch.bfloat16, torch.float16):
+        code = self._codes.get(logits.dtype)
+        if code is None:
             raise HeadlossError(HEADLOSS_ERR_DTYPE, "headloss_sample")
-        device, rows = logits.device, logits.shape[:1]
-        uniforms = self._given("uniforms", uniforms, torch.float64, rows, device)
         if uniforms is None:
             raise HeadlossError(HEADLOSS_ERR_MISSING_INPUT, "headloss_sample")
-        given = [self._given(name, a, dtype, rows, device) for (name, dtype), a in
-                 zip(self._settings, (temperature, top_k, top_p, min_p))]
-        wanted = (torch.int64, torch.float32, torch.float32, torch.int32)
+        given, f32 = self._given, self._f32
+        u, _u = given("uniforms", uniforms, self._f64, N)
+        t, _t = given("temperature", temperature, f32, N)
+        k, _k = given("top_k", top_k, self._i32, N)
+        p, _p = given("top_p", top_p, f32, N)
+        m, _m = given("min_p", min_p, f32, N)
         if out is None:
-            out = tuple(torch.empty(rows, dtype=t, device=device) for t in wanted)
+            empty, device = self._empty, self.device
+            out = (empty(N, dtype=self._i64, device=device), empty(N, dtype=f32, device=device),
+                   empty(N, dtype=f32, device=device), empty(N, dtype=self._i32, device=device))
         else:
-            for name, a, t in zip(("tokens", "logprobs", "draw_logprobs", "n_kept"), out, wanted):
-                self._given(name, a, t, rows, device)
-        headloss_sample(logits, N, V, ld, dtype_code(logits.dtype), uniforms, *given,
-                        self.softcap, self.logits_scale, *out, self.err, stream)
+            for name, a, d in zip(("tokens", "logprobs", "draw_logprobs", "n_kept"), out,
+                                  (self._i64, f32, f32, self._i32)):
+                given(name, a, d, N)
+        status = self._call(logits.data_ptr(), N, V, logits.stride(0) if N > 1 else V, code, u, t,
+                            k, p, m, self.softcap, self.logits_scale, out[0].data_ptr(),
+                            out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(),
+                            self.err.data_ptr(),
+                            _raw_stream(self.index) if stream is None else _stream(stream))
+        if status:
+            _check(status, "headloss_sample")
         return out
 
     def device_error(self, stream=None) -> int:
@@ -507,29 +529,46 @@ class GradClipper:
         self.h = None
         self.max_grads = max(int(max_grads), len(grads), 1)
         self.bind(grads, outs)
+        self._call = load_library().headloss_clip_grads
         self.h = headloss_clip_create(self.max_grads)
 
     def bind(self, grads, outs=None) -> None:
+        import torch
         grads = list(grads)
         outs = grads if outs is None else list(outs)
         if len(outs) != len(grads) or len(grads) > self.max_grads:
             raise ValueError(f"{len(grads)} gradients and {len(outs)} outputs (up to "
                              f"{self.max_grads})")
-        table = (headloss_gradient * max(1, len(grads)))()
-        for e, g, o in zip(table, grads, outs):
-            if not g.is_cuda or not g.is_contiguous() or not o.is_contiguous() or (
-                    o.dtype != g.dtype or o.shape != g.shape or o.device != g.device):
+        codes = {torch.float32: HEADLOSS_FP32, torch.bfloat16: HEADLOSS_BF16,
+                 torch.float16: HEADLOSS_FP16}
+        for g, o in zip(grads, outs):
+            if not g.is_cuda or not g.is_contiguous() or o is not g and (
+                    not o.is_contiguous() or o.dtype is not g.dtype or o.shape != g.shape or
+                    o.get_device() != g.get_device()):
                 raise ValueError("gradients are contiguous CUDA tensors, their outputs of the "
                                  "same type, shape and device")
-            e.grad, e.out, e.n, e.dtype = g.data_ptr(), o.data_ptr(), g.numel(), dtype_code(g.dtype)
-        self.grads, self.outs, self.table = grads, outs, table
+            if g.dtype not in codes:
+                raise HeadlossError(HEADLOSS_ERR_DTYPE, "headloss_clip_grads")
+        # the entries of headloss_gradient as four 64-bit words each (dtype in the low half)
+        words = array.array("q", bytes(32 * max(1, len(grads))))
+        for j, (g, o) in enumerate(zip(grads, outs)):
+            words[4 * j] = g.data_ptr()
+            words[4 * j + 1] = o.data_ptr()
+            words[4 * j + 2] = g.numel()
+            words[4 * j + 3] = codes[g.dtype]
+        self.grads, self.outs, self.words = grads, outs, words
+        self.table = ctypes.cast(words.buffer_info()[0], ctypes.POINTER(headloss_gradient))
+        self.index = grads[0].get_device() if grads else torch.cuda.current_device()
 
     def __call__(self, max_norm: float, inv_scale: float = 1.0, stats=None, stream=None):
-        import torch
         if stats is None:
-            device = self.grads[0].device if self.grads else "cuda"
-            stats = torch.empty(2, dtype=torch.float32, device=device)
-        headloss_clip_grads(self.h, self.table, len(self.grads), max_norm, inv_scale, stats, stream)
+            import torch
+            stats = torch.empty(2, dtype=torch.float32, device=self.index)
+        status = self._call(self.h, self.table, len(self.grads), max_norm, inv_scale,
+                            stats.data_ptr(),
+                            _raw_stream(self.index) if stream is None else _stream(stream))
+        if status:
+            _check(status, "headloss_clip_grads")
         return stats
 
     def close(self):

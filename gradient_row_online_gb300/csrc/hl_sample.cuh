@@ -14,9 +14,10 @@
 // these ways, each ending in the leader CTA while the others have left:
 //
 //   no top-k, no top-p   every warp sums its segment's masses.
-//   a small top-k        a histogram of the thread maxima bounds the cut from below (as many
-//                        tokens as maxima lie above it); the few tokens above the bound are
-//                        ranked by the leader, which finishes the row alone.
+//   a small top-k        histograms of the CTAs' thread maxima bound the cut from below (as many
+//                        tokens as maxima lie above it; the bounds go along with the largest
+//                        logit); the few tokens above the bound are ranked by the leader,
+//                        which finishes the row alone.
 //   top-p                a histogram of the order (1/32 octave of mass a bin) with exact masses
 //                        finds the bin of the cut; the next pass sums the segments' masses in the
 //                        bins above it and sends the bin's few tokens to be ranked.
@@ -53,7 +54,7 @@ constexpr int CAP = 832;      // tokens the leader can rank
 constexpr int RANKED = 256;   // ranked by comparison with all; more are sorted
 constexpr int MAX_TOPK = 128; // longest top-k that takes the thread-maxima bound
 constexpr int SEGS = MAXC * WARPS;
-constexpr int QUEUE = MAXC * 64;
+constexpr int QUEUE = 512;
 constexpr float PER_OCTAVE = 32.f;  // bins an octave of mass
 constexpr int TOPS = 128;           // bins of the thread maxima,
 constexpr float TOPS_PER_OCTAVE = 4.f;
@@ -93,7 +94,7 @@ struct Shared {
     };
     union {
         u64 groups[MAXC][32];  // the CTAs' histograms by groups of 32 bins
-        int queue[MAXC * 64];  // words that hold tokens of the cut's bin
+        int queue[QUEUE];      // words with tokens to list
     };
     union {
         struct {
@@ -103,14 +104,13 @@ struct Shared {
         uint32_t tops[TOPS];  // histogram of the thread maxima
         u64 rank[BINS];       // where lists are ranked
     };
-    u64 xch[2][MAXC];      // exchanges of one value a CTA
+    u64 xch[2][MAXC][2];   // exchanges of two values a CTA
     u64 seg_mass[SEGS];    // the segments' kept masses, the model's, and counts (leader)
     u64 seg_model[SEGS];
     uint32_t seg_kept[SEGS];
     u64 my_mass[WARPS];    // the CTA's own segments
     u64 my_model[WARPS];
     uint32_t my_kept[WARPS];
-    float from;
     double target;
     uint32_t list_n[MAXC];
     u64 red[WARPS];
@@ -273,14 +273,6 @@ __device__ __forceinline__ void st_peer32(uint32_t addr, uint32_t v) {
 __device__ __forceinline__ uint32_t ld_peer32(uint32_t addr) {
     uint32_t v;
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint4 ld_peer_quad(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(addr)
-                 : "memory");
     return v;
 }
 __device__ __forceinline__ void cluster_arrive() {
@@ -457,7 +449,7 @@ struct Row {
     }
     // Below every logit of a bin (of `per` an octave): distances lie below (bin + 1/2) / (per c),
     // and a little more for the roundings.
-    __device__ float lower_edge(float bin, float per) const {
+    __device__ float lower_edge(float top, float bin, float per) const {
         const float far = __fmul_ru(__fdiv_ru(bin + 0.5f, __fmul_rd(c, per)), 1.00001f);
         return __fsub_rd(top, far);
     }
@@ -465,13 +457,17 @@ struct Row {
         return v > kv || (v == kv && idx <= k.idx);
     }
 
-    // Every CTA's value (of warp 0's lanes, all alike) at every CTA.  ALONE: the other warps
-    // wrote nothing that another CTA reads after it.
+    // Every CTA's two values (of warp 0's lanes, all alike) at every CTA.  ALONE: the other
+    // warps wrote nothing that another CTA reads after it.
     template <bool ALONE>
-    __device__ const u64* exchange(u64 v) {
+    __device__ const u64 (*exchange(u64 v0, u64 v1 = 0))[2] {
         __syncwarp();
         if (warp == 0) {
-            if (lane < C) st_peer64(map_peer(smem_addr(&s.xch[par][rank]), lane), v);
+            if (lane < C) {
+                const uint32_t at = map_peer(smem_addr(&s.xch[par][rank][0]), lane);
+                st_peer64(at, v0);
+                st_peer64(at + 8, v1);
+            }
             __syncwarp();
             cluster_arrive();
         } else if constexpr (ALONE) {
@@ -480,7 +476,7 @@ struct Row {
             cluster_arrive();
         }
         cluster_wait();
-        const u64* got = s.xch[par];
+        const u64(*got)[2] = s.xch[par];
         par ^= 1;
         return got;
     }
@@ -508,6 +504,18 @@ struct Row {
 
     // ------------------------------------------------------ lists to rank ----
 
+    // Words with tokens to list are queued as a pass finds them (their lanes would hold up the
+    // others), and gone through a thread a word after a block barrier.
+    __device__ __forceinline__ void enqueue(int i) {
+        const uint32_t n = atomicAdd(&s.queued, 1u);
+        if (n < QUEUE) s.queue[n] = i;
+    }
+    // How many are queued; with too many the CTA's count shows an overflow.
+    __device__ uint32_t queued() {
+        const uint32_t n = s.queued;
+        if (n > QUEUE && threadIdx.x == 0) s.n_local = CAP + 1;
+        return n > QUEUE ? 0u : n;
+    }
     // Appends a token to this CTA's run of the leader's list.
     __device__ __forceinline__ void append(float v, int idx) {
         const uint32_t at = atomicAdd(&s.n_local, 1u);
@@ -537,8 +545,13 @@ struct Row {
             __syncthreads();
             if (int(threadIdx.x) < n) {
                 int better = 0;
+                const ulonglong2* two = reinterpret_cast<const ulonglong2*>(s.rank);
 #pragma unroll 4
-                for (int j = 0; j < n; ++j) better += s.rank[j] > mine;
+                for (int j = 0; j < n / 2; ++j) {
+                    const ulonglong2 o = two[j];
+                    better += (o.x > mine) + (o.y > mine);
+                }
+                if (n & 1) better += s.rank[n - 1] > mine;
                 sorted[better] = mine;
             }
             __syncthreads();
@@ -624,42 +637,41 @@ struct Row {
 
     // -------------------------------------------------------- small top-k ----
 
-    // A bound from below of the k-th largest logit: the lower edge of the bin where the
-    // histogram of the cluster's thread maxima reaches k.
-    __device__ float bound_of(float mine, int k) {
+    // Bounds from below of the k-th and of the ceil(k / C)-th largest logit of the CTA, as keys: the
+    // lower edges of the bins where the histogram of its thread maxima (from its own
+    // largest) reaches so many.  At least k tokens lie at or above the largest of the first over the CTAs,
+    // and at or above the least of the second.  In warp 0.
+    __device__ u64 bounds_of(float mine, float cta_top, int k) {
         if (mine > -CUDART_INF_F)
             atomicAdd(&s.tops[min(uint32_t(TOPS - 1), __float2uint_rn(__fmul_rn(
-                                                          __fmul_rn(__fsub_rn(top, mine), c),
+                                                          __fmul_rn(__fsub_rn(cta_top, mine), c),
                                                           TOPS_PER_OCTAVE)))],
                       1u);
-        cluster_barrier();
-        if (warp == 0) {
-            static_assert(TOPS == 128, "four bins a lane");
-            uint4 n = make_uint4(0, 0, 0, 0);
-            for (int r = 0; r < C; ++r) {
-                const uint4 x = ld_peer_quad(map_peer(smem_addr(&s.tops[4 * lane]), r));
-                n.x += x.x, n.y += x.y, n.z += x.z, n.w += x.w;
-            }
-            const uint32_t sum = n.x + n.y + n.z + n.w;
-            uint32_t inc = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t m = __shfl_up_sync(FULL, inc, o);
-                if (lane >= o) inc += m;
-            }
-            const unsigned past = __ballot_sync(FULL, inc >= uint32_t(k));
-            if (lane == (past ? __ffs(past) - 1 : 0)) {
-                uint32_t at = inc - sum + n.x;
-                int bin = 4 * lane;
-                if (at < uint32_t(k)) ++bin, at += n.y;
-                if (at < uint32_t(k)) ++bin, at += n.z;
-                if (at < uint32_t(k)) ++bin;
-                s.from = !past || bin == TOPS - 1 ? -CUDART_INF_F
-                                                  : lower_edge(float(bin), TOPS_PER_OCTAVE);
-            }
-        }
         __syncthreads();
-        return s.from;
+        if (warp) return 0;
+        static_assert(TOPS == 128, "four bins a lane");
+        const uint4 n = reinterpret_cast<const uint4*>(s.tops)[lane];
+        const uint32_t sum = n.x + n.y + n.z + n.w;
+        uint32_t inc = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t m = __shfl_up_sync(FULL, inc, o);
+            if (lane >= o) inc += m;
+        }
+        auto bound = [&](uint32_t want) -> uint32_t {
+            const unsigned past = __ballot_sync(FULL, inc >= want);
+            if (!past) return KEY_NONE;
+            const int at = __ffs(past) - 1;
+            uint32_t have = inc - sum + n.x;  // (only lane `at`'s is used)
+            int bin = 4 * lane;
+            if (have < want) ++bin, have += n.y;
+            if (have < want) ++bin, have += n.z;
+            if (have < want) ++bin;
+            bin = __shfl_sync(FULL, bin, at);
+            const float edge = lower_edge(cta_top, float(bin), TOPS_PER_OCTAVE);
+            return bin < TOPS - 1 && edge == edge ? key_of(edge) : KEY_NONE;
+        };
+        return (u64(bound(uint32_t(k))) << 32) | bound(uint32_t((k + C - 1) / C));
     }
 
     // The tokens at or above `from` to the leader, and the row finished there.  False (in
@@ -669,19 +681,26 @@ struct Row {
         Model model;
         for (int i = s0 + lane; i < s1; i += 32) {
             const uint4 w = word(i);
-            const bool any = E::top(E::word_max(w)) >= from;
-            if (want || any) {
+            if (want) {
                 float v[EPW];
                 E::unpack(w, v);
-                if (want) add_model(model, v);
-                if (any)
-                    for (int e = 0; e < EPW; ++e)
-                        if (v[e] >= from && v[e] > -CUDART_INF_F) append(v[e], index(i, e));
+                add_model(model, v);
             }
+            if (E::top(E::word_max(w)) >= from) enqueue(i);
         }
         if (want) {
             const u64 m = model_sum(model);
             if (lane == 0) s.my_model[warp] = m;
+        }
+        __syncthreads();
+        for (uint32_t j = threadIdx.x; j < queued(); j += THREADS) {
+            const int i = s.queue[j];
+            float v[EPW];
+            E::unpack(word(i), v);
+#pragma unroll
+            for (int e = 0; e < EPW; ++e) {
+                if (v[e] >= from && v[e] > -CUDART_INF_F) append(v[e], index(i, e));
+            }
         }
         __syncthreads();
         if (warp == 0) {
@@ -689,8 +708,8 @@ struct Row {
                 st_peer64(map_peer(smem_addr(&s.seg_model[rank * WARPS + lane]), 0), s.my_model[lane]);
             if (lane == 0) st_peer32(map_peer(smem_addr(&s.list_n[rank]), 0), s.n_local);
         }
-        const u64* all = exchange<false>(s.n_local);
-        if (__any_sync(FULL, lane < C && all[lane] > u64(CAP / C))) return false;
+        const u64(*all)[2] = exchange<false>(s.n_local);
+        if (__any_sync(FULL, lane < C && all[lane][0] > u64(CAP / C))) return false;
         if (rank) return true;
 
         int n;
@@ -878,10 +897,10 @@ struct Row {
                 for (int i = 0; i < WARPS; ++i)
                     least = min(least, ~uint32_t(s.red[i] >> 32)),
                     largest = max(largest, uint32_t(s.red[i]));
-                const u64* got = exchange<true>((u64(~least) << 32) | largest);
+                const u64(*got)[2] = exchange<true>((u64(~least) << 32) | largest);
                 for (int r = 0; r < C; ++r)
-                    least = min(least, ~uint32_t(got[r] >> 32)),
-                    largest = max(largest, uint32_t(got[r]));
+                    least = min(least, ~uint32_t(got[r][0] >> 32)),
+                    largest = max(largest, uint32_t(got[r][0]));
                 k0 = least, k1 = largest;
             } else {
                 k1 = k1 - (bin << shift);
@@ -961,8 +980,8 @@ struct Row {
             if (i < warp) lower += s.red[i];
             count += s.red[i];
         }
-        const u64* got = exchange<true>(count);
-        for (int r = 0; r < rank; ++r) lower += got[r];
+        const u64(*got)[2] = exchange<true>(count);
+        for (int r = 0; r < rank; ++r) lower += got[r][0];
         if (stay > lower && stay <= lower + mine) {
             for (int i = s0; i < s1; i += 32) {
                 float v[EPW];
@@ -1106,7 +1125,7 @@ struct Row {
     __device__ void sum_above(uint32_t bin, float least, u64 model) {
         const hl::f2 slope = hl::pk1(-PER_OCTAVE), magic = hl::pk1(8388608.f);
         const float edge = 8388608.f + float(bin);
-        const float from = lower_edge(float(bin), PER_OCTAVE);
+        const float from = lower_edge(top, float(bin), PER_OCTAVE);
         u64 mass = 0;
         uint32_t kept = 0;
         for (int i0 = s0; i0 < s1; i0 += 32) {
@@ -1139,17 +1158,11 @@ struct Row {
                 }
                 mass += both;
             }
-            if (on_edge) {
-                const uint32_t n = atomicAdd(&s.queued, 1u);
-                if (n < QUEUE) s.queue[n] = i;
-            }
+            if (on_edge) enqueue(i);
         }
         keep_segment(mass, kept, model);
         __syncthreads();
-        // the words that hold tokens of the bin (few), a thread a word
-        const uint32_t n = s.queued;
-        if (n > QUEUE && threadIdx.x == 0) s.n_local = CAP + 1;  // too many: the call's caller sees it
-        for (uint32_t j = threadIdx.x; j < min(n, uint32_t(QUEUE)); j += THREADS) {
+        for (uint32_t j = threadIdx.x; j < queued(); j += THREADS) {
             const int i = s.queue[j];
             float v[EPW];
             values(i, v);
@@ -1324,8 +1337,9 @@ __global__ void __launch_bounds__(THREADS, 4) sample_kernel(const __grid_constan
     const bool any_lost = __syncthreads_or(lost);
     const uint32_t cta_top = __reduce_max_sync(FULL, s.ired[lane % WARPS]);
     cluster_wait();
-    const u64* got = r.template exchange<true>((u64(any_lost) << 32) | cta_top);
-    const u64 other = got[lane < r.C ? lane : 0];
+    const u64 bounds = small_k && k > 1 ? r.bounds_of(mine_top, of_key(cta_top), k) : 0;
+    const u64(*got)[2] = r.template exchange<true>((u64(any_lost) << 32) | cta_top, bounds);
+    const u64 other = got[lane < r.C ? lane : 0][0], edges = got[lane < r.C ? lane : 0][1];
     const uint32_t topkey = __reduce_max_sync(FULL, uint32_t(other));
     const bool given_up = __any_sync(FULL, (other >> 32) != 0);
     r.top = of_key(topkey);
@@ -1339,7 +1353,9 @@ __global__ void __launch_bounds__(THREADS, 4) sample_kernel(const __grid_constan
     r.zm = r.z(r.top);
 
     if (small_k) {
-        const float from = k == 1 ? r.top : r.bound_of(mine_top, k);
+        const uint32_t edge = max(__reduce_max_sync(FULL, uint32_t(edges >> 32)),
+                                  __reduce_min_sync(FULL, uint32_t(edges)));
+        const float from = k == 1 ? r.top : edge > KEY_NONE ? of_key(edge) : -CUDART_INF_F;
         if (r.few(from, k, p, least, u)) return;
     }
 
@@ -1381,8 +1397,8 @@ __global__ void __launch_bounds__(THREADS, 4) sample_kernel(const __grid_constan
                 r.send_segments();
                 if (lane == 0) st_peer32(map_peer(smem_addr(&s.list_n[r.rank]), 0), s.n_local);
             }
-            const u64* all = r.template exchange<false>(s.n_local);
-            if (!__any_sync(FULL, lane < r.C && all[lane] > u64(CAP / r.C))) {
+            const u64(*all)[2] = r.template exchange<false>(s.n_local);
+            if (!__any_sync(FULL, lane < r.C && all[lane][0] > u64(CAP / r.C))) {
                 if (r.rank == 0) r.finish_bin(before, least, u);
                 return;
             }

@@ -516,44 +516,62 @@ struct Row {
         if (n > QUEUE && threadIdx.x == 0) s.n_local = CAP + 1;
         return n > QUEUE ? 0u : n;
     }
-    // Appends a token to this CTA's run of the leader's list.
-    __device__ __forceinline__ void append(float v, int idx) {
-        const uint32_t at = atomicAdd(&s.n_local, 1u);
-        if (at < uint32_t(CAP / C))
-            st_peer64(map_peer(smem_addr(&s.list[rank * (CAP / C) + at]), 0),
-                      (u64(key_of(v)) << 32) | uint32_t(~idx));
+    // Appends tokens of a word (the bits of `which`) to this CTA's run of the leader's list.
+    __device__ __forceinline__ void append(const float* v, uint32_t which, int i) {
+        if (!which) return;
+        uint32_t at = atomicAdd(&s.n_local, uint32_t(__popc(which)));
+        const uint32_t run = uint32_t(CAP / C), to = map_peer(smem_addr(&s.list[rank * run]), 0);
+#pragma unroll
+        for (int e = 0; e < EPW; ++e) {
+            if (!(which >> e & 1)) continue;
+            if (at < run) st_peer64(to + 8 * at, (u64(key_of(v[e])) << 32) | uint32_t(~index(i, e)));
+            ++at;
+        }
     }
     // After the appends and a block barrier: the CTA's count to the leader.
     __device__ void send_count() {
         if (threadIdx.x == 0) st_peer32(map_peer(smem_addr(&s.list_n[rank]), 0), s.n_local);
     }
-    // Leader: the runs put together, descending.
-    __device__ const u64* rank_list(int* n_out) {
-        const int run = CAP / C;
+    // Leader: how many tokens are listed, and the i-th over the runs.
+    __device__ int count_listed() const {
         int n = 0;
         for (int r = 0; r < C; ++r) n += int(s.list_n[r]);
+        return n;
+    }
+    __device__ u64 listed(int i) const {
+        int r = 0;
+        while (i >= int(s.list_n[r])) i -= int(s.list_n[r++]);
+        return s.list[r * (CAP / C) + i];
+    }
+    // Leader: the runs put together, descending.
+    __device__ const u64* rank_list(int* n_out) {
+        const int n = count_listed();
         *n_out = n;
-        auto at = [&](int i) -> u64 {
-            int r = 0;
-            while (i >= int(s.list_n[r])) i -= int(s.list_n[r++]);
-            return s.list[r * run + i];
-        };
+        auto at = [&](int i) -> u64 { return listed(i); };
         if (n <= RANKED) {
+            // by comparison with all; up to half as many, two threads a token, each with half of the others
             u64* sorted = s.rank + RANKED;
-            const u64 mine = int(threadIdx.x) < n ? at(threadIdx.x) : 0;
-            if (int(threadIdx.x) < n) s.rank[threadIdx.x] = mine;
+            uint32_t* part = reinterpret_cast<uint32_t*>(sorted + RANKED);
+            const bool halves = n <= RANKED / 2;
+            const int i = halves ? threadIdx.x & (RANKED / 2 - 1) : threadIdx.x;
+            const u64 mine = i < n ? at(i) : 0;
+            if (i < n) s.rank[i] = mine;
+            if (threadIdx.x == 0 && (n & 1)) s.rank[n] = 0;
             __syncthreads();
-            if (int(threadIdx.x) < n) {
-                int better = 0;
+            const int pairs = (n + 1) / 2, mid = halves ? (pairs + 1) / 2 : pairs;
+            const bool second = halves && threadIdx.x >= RANKED / 2;
+            int better = 0;
+            if (i < n) {
                 const ulonglong2* two = reinterpret_cast<const ulonglong2*>(s.rank);
 #pragma unroll 4
-                for (int j = 0; j < n / 2; ++j) {
+                for (int j = second ? mid : 0; j < (second ? pairs : mid); ++j) {
                     const ulonglong2 o = two[j];
                     better += (o.x > mine) + (o.y > mine);
                 }
-                if (n & 1) better += s.rank[n - 1] > mine;
-                sorted[better] = mine;
+                if (second) part[i] = uint32_t(better);
             }
+            if (halves) __syncthreads();
+            if (i < n && !second) sorted[better + (halves ? int(part[i]) : 0)] = mine;
             __syncthreads();
             return sorted;
         }
@@ -616,16 +634,24 @@ struct Row {
             if (hit) {
                 const int group = __ffs(hit) - 1, bin = group * 32 + lane;
                 at = __shfl_sync(FULL, at, group);
+                uint32_t n[MAXC], hi[MAXC], lo[MAXC];  // all peers' at once
+#pragma unroll
+                for (int r = 0; r < MAXC; ++r) {
+                    n[r] = hi[r] = lo[r] = 0;
+                    if (r < C) {
+                        if constexpr (!MASS || COUNTS) n[r] = ld_peer32(map_peer(smem_addr(&s.cnt[bin]), r));
+                        if constexpr (MASS) {
+                            hi[r] = ld_peer32(map_peer(smem_addr(&s.hi[bin]), r));
+                            lo[r] = ld_peer32(map_peer(smem_addr(&s.lo[bin]), r));
+                        }
+                    }
+                }
                 u64 m = 0;
                 uint32_t most = 0;
-                for (int r = 0; r < C; ++r) {
-                    uint32_t n = 0;
-                    if constexpr (!MASS || COUNTS) n = ld_peer32(map_peer(smem_addr(&s.cnt[bin]), r));
-                    most = max(most, n);
-                    if constexpr (MASS)
-                        m += joined(ld_peer32(map_peer(smem_addr(&s.hi[bin]), r)),
-                                    ld_peer32(map_peer(smem_addr(&s.lo[bin]), r)));
-                    else m += n;
+#pragma unroll
+                for (int r = 0; r < MAXC; ++r) {
+                    most = max(most, n[r]);
+                    m += MASS ? joined(hi[r], lo[r]) : u64(n[r]);
                 }
                 inc = warp_scan(m, lane);
                 at += inc - m;
@@ -697,10 +723,10 @@ struct Row {
             const int i = s.queue[j];
             float v[EPW];
             E::unpack(word(i), v);
+            uint32_t which = 0;
 #pragma unroll
-            for (int e = 0; e < EPW; ++e) {
-                if (v[e] >= from && v[e] > -CUDART_INF_F) append(v[e], index(i, e));
-            }
+            for (int e = 0; e < EPW; ++e) which |= v[e] >= from && v[e] > -CUDART_INF_F ? 1u << e : 0u;
+            append(v, which, i);
         }
         __syncthreads();
         if (warp == 0) {
@@ -924,14 +950,17 @@ struct Row {
             for (int i = s0 + lane; i < s1; i += 32) {
                 float v[EPW];
                 values(i, v);
+                uint32_t which = 0;
+#pragma unroll
                 for (int e = 0; e < EPW; ++e) {
                     bool in;
                     if (by_bin) in = bin_of(v[e]) == bin;
                     else in = key_of(v[e]) >= k0 && key_of(v[e]) <= k1;
                     if (in && weight_of(share(v[e])) &&
                         (all || inside(v[e], index(i, e), within, wv)))
-                        append(v[e], index(i, e));
+                        which |= 1u << e;
                 }
+                append(v, which, i);
             }
             __syncthreads();
             send_count();
@@ -1166,34 +1195,77 @@ struct Row {
             const int i = s.queue[j];
             float v[EPW];
             values(i, v);
+            uint32_t which = 0;
+#pragma unroll
             for (int e = 0; e < EPW; ++e) {
                 const float x = CAPPED ? 8388608.f + float(bin_of(v[e]))
                                        : __fmaf_rn(__fmul_rn(__fsub_rn(v[e], zm), c), -PER_OCTAVE, 8388608.f);
-                if (x == edge && weight_of(share(v[e]))) append(v[e], index(i, e));
+                which |= x == edge && weight_of(share(v[e])) ? 1u << e : 0u;
             }
+            append(v, which, i);
         }
     }
 
     // Leader, whole block: the same once the bin of the cut is listed, with `before` the mass
     // above it: the listed tokens inside the cut join their segments.
     __device__ void finish_bin(u64 before, float least, double u) {
-        int count;
-        const u64* sorted = rank_list(&count);
-        const Cut cut = cut_of(sorted, count, true, before, s.target);
-        const float kv = of_key(cut.key);
-        for (int i = threadIdx.x; i < count; i += THREADS) {
-            const float v = of_key(uint32_t(sorted[i] >> 32));
-            const int idx = int(~uint32_t(sorted[i]));
-            const float sh = share(v);
-            if (!inside(v, idx, cut, kv) || !(sh >= least)) continue;
-            const int w = (idx + head) / EPW, cta = w / a.per;
-            const int have = min(nw, (cta + 1) * a.per) - cta * a.per;
-            const int g = cta * WARPS + (w - cta * a.per) / ((have + WARPS - 1) / WARPS);
-            atomicAdd(&s.seg_mass[g], u64(weight_of(sh)));
-            atomicAdd(&s.seg_kept[g], 1u);
+        const int n = count_listed();
+        // before a mass of p W: as integers, before its ceiling
+        const u64 limit = u64(__double2ull_ru(s.target));
+        if (n > RANKED) {
+            int count;
+            const u64* sorted = rank_list(&count);
+            const Cut cut = cut_of(sorted, count, true, before, s.target);
+            const float kv = of_key(cut.key);
+            for (int i = threadIdx.x; i < count; i += THREADS) {
+                const float v = of_key(uint32_t(sorted[i] >> 32));
+                const int idx = int(~uint32_t(sorted[i]));
+                if (inside(v, idx, cut, kv)) join_segment(v, idx, least);
+            }
+            __syncthreads();
+            finish(cut, least, u);
+            return;
         }
+        // a token's mass before it by comparison with all; the last that stays is the cut
+        const int t = threadIdx.x;
+        const u64 mine = t < n ? listed(t) : 0;
+        const float v = of_key(uint32_t(mine >> 32));
+        ulonglong2* all = reinterpret_cast<ulonglong2*>(s.rank);
+        if (t < n) all[t] = make_ulonglong2(mine, weight_of(share(v)));
         __syncthreads();
-        finish(cut, least, u);
+        u64 last = ~u64(0);
+        if (t < n) {
+            u64 at = before;
+#pragma unroll 4
+            for (int j = 0; j < n; ++j) {
+                const ulonglong2 o = all[j];
+                at += o.x > mine ? o.y : 0;
+            }
+            if (at < limit || at == 0) {
+                last = mine;
+                join_segment(v, int(~uint32_t(mine)), least);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            const u64 other = __shfl_xor_sync(FULL, last, o);
+            last = other < last ? other : last;
+        }
+        if (lane == 0) s.red[warp] = last;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < WARPS; ++i) last = s.red[i] < last ? s.red[i] : last;
+        finish(Cut{uint32_t(last >> 32), int(~uint32_t(last))}, least, u);
+    }
+    // A listed token that stays joins its segment.
+    __device__ void join_segment(float v, int idx, float least) {
+        const float sh = share(v);
+        if (!(sh >= least)) return;
+        const int w = (idx + head) / EPW, cta = w / a.per;
+        const int have = min(nw, (cta + 1) * a.per) - cta * a.per;
+        const int g = cta * WARPS + (w - cta * a.per) / ((have + WARPS - 1) / WARPS);
+        atomicAdd(&s.seg_mass[g], u64(weight_of(sh)));
+        atomicAdd(&s.seg_kept[g], 1u);
     }
 
     // Leader, whole block: the target's segment from the segments' masses, and the token by going

@@ -57,10 +57,11 @@ struct Batch {
     Entry e[BATCH];
 };
 
+// The barrier's words on lines of their own: the waiting CTAs' polls would hold up the arrivals.
 struct Sync {
-    unsigned arrived, generation;
-    float factor;
-    double parts[MAX_GRID];
+    alignas(128) unsigned arrived;
+    alignas(128) unsigned long long answer;  // generation << 32 | the factor's bits
+    alignas(128) double parts[MAX_GRID];
 };
 
 struct Call {
@@ -271,13 +272,20 @@ __device__ __forceinline__ void clip_tile(const Entry& t, uint32_t tile, int lan
 
 // ------------------------------------------------------------------- kernel ----
 
-__device__ __forceinline__ unsigned load_acquire(const unsigned* p) {
+// The barrier's words.  An arrival releases the CTA's sum and acquires the others'; the answer
+// carries all that the waiting CTAs need in one word, so it needs no fence.
+__device__ __forceinline__ unsigned arrive(unsigned* p) {
     unsigned v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(v) : "l"(p) : "memory");
     return v;
 }
-__device__ __forceinline__ void store_release(unsigned* p, unsigned v) {
-    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+__device__ __forceinline__ unsigned long long load_answer(const unsigned long long* p) {
+    unsigned long long v;
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void store_answer(unsigned long long* p, unsigned long long v) {
+    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
 }
 __device__ __forceinline__ unsigned long long now_ns() {
     unsigned long long t;
@@ -335,24 +343,25 @@ __global__ void __launch_bounds__(THREADS, 2) clip_kernel(const __grid_constant_
     mine = block_sum(mine);
 
     Sync* s = c.sync;
+    unsigned long long before = 0;
     if (threadIdx.x == 0) {
         s_last = true;
         if (gridDim.x > 1) {
             s->parts[blockIdx.x] = mine;
-            const unsigned before = load_acquire(&s->generation);
-            __threadfence();
-            s_last = atomicAdd(&s->arrived, 1u) == gridDim.x - 1;
-            __threadfence();
+            before = load_answer(&s->answer);
+            s_last = arrive(&s->arrived) == gridDim.x - 1;
             if (!s_last) {
                 const unsigned long long began = now_ns();
-                bool given_up = false;
-                while (load_acquire(&s->generation) == before)
+                unsigned long long got;
+                while ((got = load_answer(&s->answer)) >> 32 == before >> 32) {
+                    __nanosleep(64);
                     if (now_ns() - began > WAIT_NS) {
-                        given_up = true;
+                        got = __float_as_uint(1.f);
+                        c.stats[0] = c.stats[1] = CUDART_NAN_F;
                         break;
                     }
-                s_factor = given_up ? 1.f : *reinterpret_cast<volatile float*>(&s->factor);
-                if (given_up) c.stats[0] = c.stats[1] = CUDART_NAN_F;
+                }
+                s_factor = __uint_as_float(unsigned(got));
             }
         }
     }
@@ -379,10 +388,8 @@ __global__ void __launch_bounds__(THREADS, 2) clip_kernel(const __grid_constant_
             c.stats[0] = norm, c.stats[1] = factor;
             s_factor = factor;
             if (gridDim.x > 1) {
-                s->factor = factor;
-                s->arrived = 0;
-                __threadfence();
-                store_release(&s->generation, s->generation + 1);
+                s->arrived = 0;  // (no one arrives any more in this launch)
+                store_answer(&s->answer, ((before >> 32) + 1) << 32 | __float_as_uint(factor));
             }
         }
     }
@@ -536,9 +543,9 @@ int headloss_clip_grads(headloss_clip_t h, const headloss_gradient* grads, int n
     b.count();
     if (b.tiles >= (uint64_t(1) << 32) - MAX_GRID * WARPS) return HEADLOSS_ERR_ARG;
     Call call{b.used, uint32_t(b.tiles), max_norm, inv_scale, stats_out, h->sync};
-    // a warp a tile as far as the grid goes; a CTA alone takes two, which costs less than the
+    // a warp a tile as far as the grid goes; a CTA alone takes four, which costs less than the
     // grid's barrier
-    const int64_t want = b.tiles <= 2 * WARPS ? 1 : (int64_t(b.tiles) + WARPS - 1) / WARPS;
+    const int64_t want = b.tiles <= 4 * WARPS ? 1 : (int64_t(b.tiles) + WARPS - 1) / WARPS;
     const int grid = int(want < 1 ? 1 : want < h->grid ? want : h->grid);
     if (b.used <= 1) return launch_list<1>(b, call, grid, s);
     if (b.used <= 16) return launch_list<16>(b, call, grid, s);

@@ -372,3 +372,63 @@ def test_refusals():
         pkg.HeadSampler(softcap=-1.0)(x, u)
     with pytest.raises(hlb.HeadlossError):
         pkg.HeadSampler(logits_scale=0.0)(x, u)
+
+
+# -------------------------------------------- rows that leave the ordinary way ----
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("sigma", [0.02, 0.5, 1.0])
+def test_flat_rows(dtype, sigma):
+    """Nearly uniform long rows: the cut's bin holds more tokens than can be ranked, in keys that
+    differ and in keys that do not."""
+    x, u = noise(3, 128_256, dtype, seed=11, sigma=sigma)
+    for f in (dict(p=0.9), dict(t=0.7, p=0.5), dict(k=50_000, p=0.9), dict(k=70_000), dict(p=0.9, m=0.3),
+              dict(k=100, p=0.95), {}):
+        check(x, u, **f)
+
+
+def test_long_rows_of_few_values():
+    g = torch.Generator().manual_seed(17)
+    x = torch.randint(-2, 3, (3, 151_936), generator=g).float() * 1.5
+    u = torch.rand(3, generator=g, dtype=torch.float64)
+    for dtype in (torch.bfloat16, torch.float32):
+        for f in (dict(k=40), dict(k=60_000), dict(p=0.3), dict(p=0.9), dict(k=50_000, p=0.7),
+                  dict(t=0.0), {}):
+            check(x.to(dtype).cuda(), u.cuda(), **f)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("descending", [True, False])
+def test_sorted_rows(dtype, descending):
+    """A vocabulary in the order of its logits: all candidates lie in one part of the row."""
+    x, u = noise(4, 128_256, dtype, seed=13)
+    x = x.float().sort(dim=1, descending=descending).values.to(DT[dtype])
+    for f in (dict(k=1), dict(k=20, p=0.9), dict(t=0.8, k=100, p=0.95), dict(k=128), dict(k=129), dict(p=0.95),
+              dict(k=3000, p=0.9), {}):
+        check(x, u, **f)
+
+
+@pytest.mark.parametrize("v", [1000, 32_000, 151_936])
+def test_one_token_has_it_all(v):
+    """A peak 40 octaves above a flat body: every mass but its own rounds to nothing."""
+    x = torch.full((3, v), -1.0)
+    x[:, v // 3] = 30.0
+    x[1, v - 1] = 30.0
+    u = torch.tensor([0.0, 0.6, 0.999], dtype=torch.float64).cuda()
+    for f in ({}, dict(p=0.9), dict(k=50, p=0.9), dict(k=5000), dict(m=0.5), dict(t=0.0)):
+        tok = check(x.bfloat16().cuda(), u, **f)
+        assert tok[0] == v // 3 and tok[2] == v // 3
+
+
+def test_log_probs_do_not_depend_on_the_batch():
+    """The model's log-probs are sums in fixed point: the same bits for a row alone and among
+    others, although rows are then split over other numbers of CTAs."""
+    x, u = noise(600, 32_000, "bf16", seed=41)
+    sampler = pkg.HeadSampler()
+    t = torch.full((600,), 0.8, device="cuda")
+    p = torch.full((600,), 0.9, device="cuda")
+    a = sampler(x, u, temperature=t, top_p=p)
+    for i in (0, 311, 599):
+        b = sampler(x[i:i + 1], u[i:i + 1], temperature=t[:1], top_p=p[:1])
+        assert all(torch.equal(q[i:i + 1], r) for q, r in zip(a, b))

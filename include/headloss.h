@@ -122,7 +122,7 @@ enum headloss_slot {
  * out:          receives the handle.
  *
  * Allocates the handle's workspace on the current device (the only
- * allocation this library makes).  Errors: ERR_ARG, ERR_CUDA.
+ * allocation of the loss calls).  Errors: ERR_ARG, ERR_CUDA.
  */
 int headloss_create(uint32_t flags, const headloss_weights* w, float temperature,
                     float clip_eps, float softcap, float logits_scale, headloss_t* out);

@@ -21,6 +21,7 @@
  *   token: the first kept j, by index, with sum of kept w_0 .. w_j > t.
  * T = 0 (or so small that K / T overflows) is greedy: top-k 1 at T = 1.
  *
+ * Rows' settings differ freely: greedy, unfiltered and filtered rows share a call.
  * Status codes are those of headloss.h.
  */
 #ifndef HEADLOSS_SAMPLE_H
@@ -48,7 +49,8 @@ extern "C" {
  *               logit -inf or NaN, or settings outside the ranges above).  The loss calls
  *               take -1 as a masked row.
  * logprobs:     N fp32 or NULL (written): log p(token) of the whole softmax at T = 1 without
- *               filters, the old_logprobs of a GRPO step; 0 for a row without a token.
+ *               filters, the old_logprobs of a GRPO step; 0 for a row without a token.  Summed in
+ *               fixed point: the same bits however the row is split over CTAs.
  * draw_logprobs: N fp32 or NULL (written): log(mass of the token / kept mass) at the
  *               row's temperature, the log-prob under the distribution drawn from; 0 likewise.
  * n_kept:       N int32 or NULL (written): the number of tokens that could be drawn.

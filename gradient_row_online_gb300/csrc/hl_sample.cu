@@ -12,7 +12,7 @@ extern "C" int headloss_sample(const void* logits, int64_t N, int64_t V, int64_t
                                float softcap, float logits_scale, int64_t* tokens, float* logprobs,
                                float* draw_logprobs, int32_t* n_kept, int* err, void* stream) {
     using namespace hl_sample;
-    if (N < 0 || N > (int64_t(1) << 40) || V < 1 || V >= (int64_t(1) << 31) - 4096 || ld < V)
+    if (N < 0 || N > INT32_MAX || V < 1 || V >= (int64_t(1) << 31) - 4096 || ld < V)
         return HEADLOSS_ERR_ARG;
     if (!(softcap >= 0.f) || !isfinite(softcap) || !(logits_scale > 0.f) || !isfinite(logits_scale))
         return HEADLOSS_ERR_ARG;

@@ -430,11 +430,17 @@ class HeadLoss:
             pass
 
 
+_get_raw_stream = None
+
+
 def _raw_stream(device: int) -> int:
     """The current stream's handle, without the Stream object torch would make."""
-    import torch
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return get(device) if get else torch.cuda.current_stream(device).cuda_stream
+    global _get_raw_stream
+    if _get_raw_stream is None:
+        import torch
+        _get_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _get_raw_stream(device)
 
 
 class HeadSampler:
@@ -559,11 +565,12 @@ class GradClipper:
         self.grads, self.outs, self.words = grads, outs, words
         self.table = ctypes.cast(words.buffer_info()[0], ctypes.POINTER(headloss_gradient))
         self.index = grads[0].get_device() if grads else torch.cuda.current_device()
+        self.device = torch.device("cuda", self.index)
+        self._empty, self._f32 = torch.empty, torch.float32
 
     def __call__(self, max_norm: float, inv_scale: float = 1.0, stats=None, stream=None):
         if stats is None:
-            import torch
-            stats = torch.empty(2, dtype=torch.float32, device=self.index)
+            stats = self._empty(2, dtype=self._f32, device=self.device)
         status = self._call(self.h, self.table, len(self.grads), max_norm, inv_scale,
                             stats.data_ptr(),
                             _raw_stream(self.index) if stream is None else _stream(stream))

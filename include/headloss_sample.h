@@ -59,7 +59,7 @@ extern "C" {
  *               up (~2 s; that row's token is -1).
  * stream:       cudaStream_t (NULL = legacy default stream).  Asynchronous, no allocation.
  *
- * N == 0 is valid.  Errors (nothing enqueued): ERR_ARG (N < 0, V < 1, V >= 2^31, ld < V, a
+ * N == 0 is valid.  Errors (nothing enqueued): ERR_ARG (N < 0, N >= 2^31, V < 1, V >= 2^31 - 4096, ld < V, a
  * softcap or logits_scale out of range, a NULL logits / uniforms / tokens / err with N > 0),
  * ERR_DTYPE, ERR_ALIGN (logits not aligned to its element; uniforms or tokens not 8-byte, an
  * fp32 or int32 array not 4-byte aligned), ERR_CUDA (launch failure).

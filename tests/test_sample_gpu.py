@@ -432,3 +432,15 @@ def test_log_probs_do_not_depend_on_the_batch():
     for i in (0, 311, 599):
         b = sampler(x[i:i + 1], u[i:i + 1], temperature=t[:1], top_p=p[:1])
         assert all(torch.equal(q[i:i + 1], r) for q, r in zip(a, b))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("offset", [1, 3, 7])
+def test_views_off_the_grid(dtype, offset):
+    """The base itself off the 16-byte grid: columns from `offset` on, as a view."""
+    x, u = noise(5, 4000, dtype, seed=offset, pitch=4000 + offset)
+    whole = torch.empty(5, 4000 + offset, dtype=DT[dtype], device="cuda")
+    whole[:, :offset] = 100.0  # what lies before the view would win every draw
+    whole[:, offset:] = x
+    for f in ({}, dict(p=0.9), dict(t=0.8, k=40, p=0.9), dict(k=900)):
+        check(whole[:, offset:], u, **f)

@@ -40,7 +40,7 @@ extern "C" {
  *               at element i * ld (ld >= V: columns past V, a padded vocabulary, are not
  *               read).  The base is aligned to the element; rows need no further alignment.
  * uniforms:     N fp64 in [0, 1), device, 8-byte aligned.
- * temperature:  N fp32, >= 0 and finite, or NULL (1 everywhere).  0: greedy.
+ * temperature:  N fp32, >= 0 and finite, or NULL (1 everywhere).  0 (or -0): greedy.
  * top_k:        N int32 or NULL.  <= 0 or >= V: off.
  * top_p:        N fp32, >= 0, or NULL.  >= 1: off.
  * min_p:        N fp32 in [0, 1] or NULL.  0: off.

@@ -16,6 +16,10 @@ extern "C" int headloss_sample(const void* logits, int64_t N, int64_t V, int64_t
         return HEADLOSS_ERR_ARG;
     if (!(softcap >= 0.f) || !isfinite(softcap) || !(logits_scale > 0.f) || !isfinite(logits_scale))
         return HEADLOSS_ERR_ARG;
+    // what the kernel multiplies by: with an infinity the row's largest logit would have no mass
+    const float inv_cap = softcap > 0.f ? float(1.0 / double(softcap)) : 0.f;
+    const float K = float(double(logits_scale) * 1.4426950408889634);
+    if (!isfinite(inv_cap) || !isfinite(K)) return HEADLOSS_ERR_ARG;
     if (dtype != HEADLOSS_FP32 && dtype != HEADLOSS_BF16 && dtype != HEADLOSS_FP16)
         return HEADLOSS_ERR_DTYPE;
     if (N == 0) return HEADLOSS_OK;
@@ -36,8 +40,8 @@ extern "C" int headloss_sample(const void* logits, int64_t N, int64_t V, int64_t
     a.top_p = top_p;
     a.min_p = min_p;
     a.cap = softcap;
-    a.inv_cap = softcap > 0.f ? float(1.0 / double(softcap)) : 0.f;
-    a.K = float(double(logits_scale) * 1.4426950408889634);
+    a.inv_cap = inv_cap;
+    a.K = K;
     a.tokens = tokens;
     a.logprobs = logprobs;
     a.draw_logprobs = draw_logprobs;

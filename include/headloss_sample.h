@@ -44,7 +44,8 @@ extern "C" {
  * top_k:        N int32 or NULL.  <= 0 or >= V: off.
  * top_p:        N fp32, >= 0, or NULL.  >= 1: off.
  * min_p:        N fp32 in [0, 1] or NULL.  0: off.
- * softcap, logits_scale: as in headloss_create (c >= 0, 0 = off; s > 0).
+ * softcap, logits_scale: as in headloss_create (c >= 0, 0 = off; s > 0), with 1 / c and
+ *               s log2(e) inside fp32's range (c = 0 or c > 2.94e-39, s < 2.35e38).
  * tokens:       N int64 (written): the drawn token; -1 for a row without one (every
  *               logit -inf or NaN, or settings outside the ranges above).  The loss calls
  *               take -1 as a masked row.

@@ -1225,7 +1225,7 @@ struct Row {
                 }
                 mass += both;
             }
-            if (on_edge) enqueue(i);
+            if (on_edge && i < s1) enqueue(i);  // (at c = 0 a lane past the segment sees -inf in bin 0)
         }
         keep_segment(mass, kept, model);
         __syncthreads();

@@ -19,3 +19,15 @@ def test_negative_zero_temperature_is_greedy(name, cap, dtype):
     x, u = noise(6, 4099, dtype, seed=3)
     tok = check(x, u, cap, **dict(FILTERS[name], t=-0.0))
     assert np.array_equal(tok, x.float().argmax(1).cpu().numpy())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+@pytest.mark.parametrize("v", [777, 4099, 128_256])
+def test_a_scale_and_temperature_whose_quotient_is_zero(v, cap, dtype):
+    """K / T = 0: every token that is not masked weighs the same."""
+    x, u = noise(3, v, dtype, seed=v)
+    x[1, ::3] = -math.inf
+    x[2, v // 4:] = -math.inf
+    for f in ({}, dict(p=0.9), dict(p=0.0), dict(k=40, p=0.9), dict(k=700, p=0.5), dict(m=0.5, p=0.7)):
+        check(x, u, cap, 1e-30, t=3e38, **f)

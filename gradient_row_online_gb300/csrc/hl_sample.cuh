@@ -486,10 +486,11 @@ struct Row {
                    __float2uint_rn(__fmul_rn(__fmul_rn(__fsub_rn(top, v), c), PER_OCTAVE)));
     }
     // Below every logit of a bin (of `per` an octave): distances lie below (bin + 1/2) / (per c),
-    // and a little more for the roundings.
+    // and a little more for the roundings.  -inf where c is so small that a bin has no end (c = 0:
+    // all logits are in bin 0, whatever the largest is).
     __device__ float lower_edge(float top, float bin, float per) const {
         const float far = __fmul_ru(__fdiv_ru(bin + 0.5f, __fmul_rd(c, per)), 1.00001f);
-        return __fsub_rd(top, far);
+        return far < CUDART_INF_F ? __fsub_rd(top, far) : -CUDART_INF_F;
     }
     __device__ __forceinline__ bool inside(float v, int idx, const Cut& k, float kv) const {
         return v > kv || (v == kv && idx <= k.idx);
@@ -733,7 +734,7 @@ struct Row {
             if (have < want) ++bin;
             bin = __shfl_sync(FULL, bin, at);
             const float edge = lower_edge(cta_top, float(bin), TOPS_PER_OCTAVE);
-            return bin < TOPS - 1 && edge == edge ? key_of(edge) : KEY_NONE;
+            return bin < TOPS - 1 ? key_of(edge) : KEY_NONE;
         };
         return (u64(bound(uint32_t(k))) << 32) | bound(uint32_t((k + C - 1) / C));
     }

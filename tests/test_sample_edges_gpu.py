@@ -31,3 +31,18 @@ def test_a_scale_and_temperature_whose_quotient_is_zero(v, cap, dtype):
     x[2, v // 4:] = -math.inf
     for f in ({}, dict(p=0.9), dict(p=0.0), dict(k=40, p=0.9), dict(k=700, p=0.5), dict(m=0.5, p=0.7)):
         check(x, u, cap, 1e-30, t=3e38, **f)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("s,t", [(1e-30, 3e38), (1e-6, 3e38), (0.5, 1.0)])
+@pytest.mark.parametrize("v", [777, 4099, 128_256])
+def test_capped_rows_with_infinite_logits(v, s, t, dtype):
+    """A softcap keeps +inf at a finite z: the largest among other tokens with a mass, at ordinary
+    temperatures and at K / T = 0 and just above (where an infinite distance has no bin)."""
+    x, u = noise(3, v, dtype, seed=v + 1)
+    x[0, v // 2] = math.inf
+    x[1, v - 1] = math.inf
+    x[1, :v // 2] = -math.inf
+    x[2, ::5] = math.inf
+    for f in ({}, dict(p=0.9), dict(p=0.0), dict(k=40, p=0.9), dict(k=700, p=0.5), dict(m=0.5, p=0.7)):
+        check(x, u, 30.0, s, t=t, **f)

@@ -36,6 +36,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math_constants.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include <atomic>
@@ -95,8 +96,8 @@ typedef unsigned long long u64;
 
 struct Shared {
     u64 bar[WARPS];
-    union {
-        u64 list[CAP];     // (key << 32 | ~index) of the tokens to rank, a run a CTA (leader)
+    union {  // (aligned: cnt, and hi, lo, tops and rank below, are also read 16 bytes at a time)
+        alignas(16) u64 list[CAP];  // (key << 32 | ~index) of the tokens to rank, a run a CTA (leader)
         uint32_t cnt[BINS];  // histogram of counts
     };
     union {
@@ -105,7 +106,7 @@ struct Shared {
     };
     union {
         struct {
-            uint32_t hi[BINS];  // histogram of masses, above and below bit SPLIT
+            alignas(16) uint32_t hi[BINS];  // histogram of masses, above and below bit SPLIT
             uint32_t lo[BINS];
         };
         uint32_t tops[TOPS];  // histogram of the thread maxima
@@ -130,6 +131,8 @@ struct Shared {
     u64 fin[3];
     uint32_t fin_seg;
 };
+static_assert(alignof(Shared) >= 16 && offsetof(Shared, list) % 16 == 0 && offsetof(Shared, hi) % 16 == 0,
+              "words of 16 bytes");
 
 // A cut of the order: tokens above the key stay, and at the key those up to an index.
 struct Cut {

@@ -7,7 +7,9 @@
 //   phase 1   squares, in fp32 over a lane's share of one tile (at most 64), in
 //             fp64 from there on, in an order that the sizes and the grid fix;
 //   barrier   over the grid (bounded); the last CTA to arrive joins the CTAs' sums in
-//             their order and publishes the factor.  Up to eight CTAs are one cluster, whose
+//             their order and publishes the factor.  A CTA that waits too long publishes a
+//             failure instead; whichever comes first holds for all, and after a failure none
+//             goes on to phase 2.  Up to eight CTAs are one cluster, whose
 //             CTAs send one another their sums and join them each;
 //   phase 2   the run again, backwards: the last tile is still in registers, the ones before it
 //             still in L2.  In place with factor 1 it is left out.
@@ -17,7 +19,6 @@
 // at 2 n, the barrier and the short phases' starts being the difference.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <math_constants.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -37,6 +38,7 @@ constexpr int CLUSTER = 8;              // CTAs that are one cluster at most
 constexpr int BATCH = 512;             // list entries a launch of list_kernel carries
 constexpr unsigned FULL = 0xffffffffu;
 constexpr unsigned long long WAIT_NS = 2000000000ull;
+constexpr unsigned FAILED = 0x7fffffffu;  // a factor's bits (NaN): a CTA gave up at the barrier
 
 struct Entry {
     const void* grad;
@@ -62,9 +64,11 @@ struct Batch {
 };
 
 // The barrier's words on lines of their own: the waiting CTAs' polls would hold up the arrivals.
+// The generation counts the handle's launches with a barrier: an arrival tells a CTA its own,
+// whenever it comes, and the answer of generation g carries g + 1.
 struct Sync {
-    alignas(128) unsigned arrived;
-    alignas(128) unsigned long long answer;  // generation << 32 | the factor's bits
+    alignas(128) unsigned long long arrived;  // generation << 32 | arrivals
+    alignas(128) unsigned long long answer;   // generation + 1 << 32 | the factor's bits
     alignas(128) double parts[MAX_GRID];
 };
 
@@ -75,6 +79,10 @@ struct Call {
     float* stats;
     Sync* sync;
     bool cluster;     // the grid is one cluster
+#ifdef HL_FAULT_INJECT
+    int late;         // a CTA that comes late to the barrier (-1: none), by late_ns
+    unsigned long long late_ns, wait_ns;
+#endif
 };
 
 __global__ void list_kernel(const __grid_constant__ Batch b, Entry* list, int at, int n) {
@@ -279,9 +287,9 @@ __device__ __forceinline__ void clip_tile(const Entry& t, uint32_t tile, int lan
 
 // The barrier's words.  An arrival releases the CTA's sum and acquires the others'; the answer
 // carries all that the waiting CTAs need in one word, so it needs no fence.
-__device__ __forceinline__ unsigned arrive(unsigned* p) {
-    unsigned v;
-    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(v) : "l"(p) : "memory");
+__device__ __forceinline__ unsigned long long arrive(unsigned long long* p) {
+    unsigned long long v;
+    asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], 1;" : "=l"(v) : "l"(p) : "memory");
     return v;
 }
 __device__ __forceinline__ unsigned long long load_answer(const unsigned long long* p) {
@@ -289,8 +297,13 @@ __device__ __forceinline__ unsigned long long load_answer(const unsigned long lo
     asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
     return v;
 }
-__device__ __forceinline__ void store_answer(unsigned long long* p, unsigned long long v) {
-    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+// Publishes `v` where the answer still is `seen`, an earlier generation's; the answer that holds.
+__device__ __forceinline__ unsigned long long publish(unsigned long long* p, unsigned long long seen,
+                                                      unsigned long long v) {
+    unsigned long long old;
+    asm volatile("atom.cas.relaxed.gpu.global.b64 %0, [%1], %2, %3;"
+                 : "=l"(old) : "l"(p), "l"(seen), "l"(v) : "memory");
+    return old == seen ? v : old;
 }
 __device__ __forceinline__ unsigned long long now_ns() {
     unsigned long long t;
@@ -352,6 +365,7 @@ __global__ void __launch_bounds__(THREADS, 2) clip_kernel(const __grid_constant_
 
     Sync* s = c.sync;
     unsigned long long before = 0;
+    unsigned tag = 0;  // of this launch's answer
     const bool alone = gridDim.x == 1 || c.cluster;  // the CTA forms the factor by itself
     if (c.cluster) {
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -374,17 +388,25 @@ __global__ void __launch_bounds__(THREADS, 2) clip_kernel(const __grid_constant_
     if (threadIdx.x == 0) {
         s_last = alone;
         if (!alone) {
+#ifdef HL_FAULT_INJECT
+            if (int(blockIdx.x) == c.late)
+                for (const unsigned long long from = now_ns(); now_ns() - from < c.late_ns;) __nanosleep(1000);
+            const unsigned long long limit = c.wait_ns ? c.wait_ns : WAIT_NS;
+#else
+            constexpr unsigned long long limit = WAIT_NS;
+#endif
             s->parts[blockIdx.x] = mine;
             before = load_answer(&s->answer);
-            s_last = arrive(&s->arrived) == gridDim.x - 1;
+            const unsigned long long n = arrive(&s->arrived);
+            tag = unsigned(n >> 32) + 1;
+            s_last = unsigned(n) == gridDim.x - 1;
             if (!s_last) {
                 const unsigned long long began = now_ns();
                 unsigned long long got;
-                while ((got = load_answer(&s->answer)) >> 32 == before >> 32) {
+                while (unsigned((got = load_answer(&s->answer)) >> 32) != tag) {
                     __nanosleep(64);
-                    if (now_ns() - began > WAIT_NS) {
-                        got = __float_as_uint(1.f);
-                        c.stats[0] = c.stats[1] = CUDART_NAN_F;
+                    if (now_ns() - began > limit) {
+                        got = publish(&s->answer, got, uint64_t(tag) << 32 | FAILED);
                         break;
                     }
                 }
@@ -412,18 +434,22 @@ __global__ void __launch_bounds__(THREADS, 2) clip_kernel(const __grid_constant_
                 if (wide > double(c.max_norm) && isfinite(norm))
                     factor = float(double(c.inv_scale) * (double(c.max_norm) / wide));
             }
+            if (!alone) {
+                unsigned long long got = before;
+                if (unsigned(before >> 32) != tag)  // (else one gave up before this CTA came)
+                    got = publish(&s->answer, before, uint64_t(tag) << 32 | __float_as_uint(factor));
+                s->arrived = uint64_t(tag) << 32;  // (no one arrives any more in this launch)
+                factor = __uint_as_float(unsigned(got));
+                if (isnan(factor)) norm = factor;
+            }
             if (!alone || blockIdx.x == 0) c.stats[0] = norm, c.stats[1] = factor;
             s_factor = factor;
-            if (!alone) {
-                s->arrived = 0;  // (no one arrives any more in this launch)
-                store_answer(&s->answer, ((before >> 32) + 1) << 32 | __float_as_uint(factor));
-            }
         }
     }
     __syncthreads();
     const float factor = s_factor;
 
-    if (last == 0xffffffffu) return;
+    if (last == 0xffffffffu || isnan(factor)) return;
     bool here = true;
     for (uint32_t t = last;; t -= WARPS) {
         while (list.e[at].first > t) --at;
@@ -513,6 +539,10 @@ struct headloss_clip {
     void* ws = nullptr;
     hl_clip::Sync* sync = nullptr;
     hl_clip::Entry* list = nullptr;
+#ifdef HL_FAULT_INJECT
+    int late = -1;
+    unsigned long long late_ns = 0, wait_ns = 0;
+#endif
 };
 
 extern "C" {
@@ -554,6 +584,15 @@ void headloss_clip_destroy(headloss_clip_t h) {
     delete h;
 }
 
+#ifdef HL_FAULT_INJECT
+// Test builds alone: CTA `late` (-1: none) comes `late_ns` late to the grid's barrier, where the
+// others give up after `wait_ns` (0: the usual limit).
+void headloss_clip_test_inject(headloss_clip_t h, int late, unsigned long long late_ns,
+                               unsigned long long wait_ns) {
+    h->late = late, h->late_ns = late_ns, h->wait_ns = wait_ns;
+}
+#endif
+
 int headloss_clip_grads(headloss_clip_t h, const headloss_gradient* grads, int n_grads,
                         float max_norm, float inv_scale, float* stats_out, void* stream) {
     using namespace hl_clip;
@@ -574,13 +613,22 @@ int headloss_clip_grads(headloss_clip_t h, const headloss_gradient* grads, int n
     Builder b{grads, n_grads};
     b.count();
     if (b.tiles >= (uint64_t(1) << 32) - MAX_GRID * WARPS) return HEADLOSS_ERR_ARG;
-    Call call{b.used, uint32_t(b.tiles), max_norm, inv_scale, stats_out, h->sync, false};
+    Call call = {};
+    call.n = b.used;
+    call.tiles = uint32_t(b.tiles);
+    call.max_norm = max_norm;
+    call.inv_scale = inv_scale;
+    call.stats = stats_out;
+    call.sync = h->sync;
     // a warp a tile as far as the grid goes; a cluster's warps take up to two, which costs less
     // than the grid's barrier
     int64_t want = (int64_t(b.tiles) + WARPS - 1) / WARPS;
     if (want <= 2 * CLUSTER) want = want < CLUSTER ? want : CLUSTER;
     const int grid = int(want < 1 ? 1 : want < h->grid ? want : h->grid);
     call.cluster = grid > 1 && grid <= CLUSTER;
+#ifdef HL_FAULT_INJECT
+    call.late = h->late, call.late_ns = h->late_ns, call.wait_ns = h->wait_ns;
+#endif
     if (b.used <= 1) return launch_list<1>(b, call, grid, s);
     if (b.used <= 16) return launch_list<16>(b, call, grid, s);
     if (b.used <= 64) return launch_list<64>(b, call, grid, s);

@@ -52,7 +52,9 @@ int headloss_clip_create(int max_grads, headloss_clip_t* out);
  * max_norm:  > 0 (infinity: never clipped).  inv_scale: > 0, finite.
  * stats_out: 2 fp32, device, 4-byte aligned (written): norm, factor.
  * In place with factor 1 nothing is written but stats_out.
- * Asynchronous on `stream`, no allocation.
+ * Asynchronous on `stream`, no allocation.  The kernel's CTAs wait for one another, for two
+ * seconds at most (a GPU that was taken from the process meanwhile): then nothing is written to
+ * any out, and norm and factor are NaN (a factor never is otherwise); the handle stays usable.
  * Errors (nothing enqueued): ERR_ARG (NULL handle, grads (n_grads > 0) or stats_out, n_grads < 0 or
  * above the handle's, max_norm or inv_scale out of range, an entry with n < 0 or a NULL pointer), ERR_DTYPE,
  * ERR_ALIGN, ERR_CUDA (launch failure).

@@ -443,6 +443,16 @@ def _raw_stream(device: int) -> int:
     return _get_raw_stream(device)
 
 
+def _torch_stream(stream, device: int):
+    """The torch stream of a `stream` argument (a torch stream or a handle)."""
+    import torch
+    if not isinstance(stream, int):
+        return stream
+    if stream in (0, 1):  # the default stream (NULL, cudaStreamLegacy), which torch has no external for
+        return torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(stream, device)
+
+
 class HeadSampler:
     """headloss_sample on torch tensors: one token a row of `logits` (N x V, unit
     column stride, any row stride), from one uniform a row.
@@ -450,7 +460,8 @@ class HeadSampler:
     The settings are per-row tensors (temperature, top_p, min_p fp32; top_k
     int32), numbers for every row, or None (off).  Returns (tokens int64, log p
     at T = 1 of the whole softmax fp32, log p under the distribution drawn from
-    fp32, tokens that could be drawn int32); `out` gives the four buffers."""
+    fp32, tokens that could be drawn int32); `out` gives the four buffers.  With
+    `stream` the call is as under torch.cuda.stream: its own tensors are made there."""
 
     def __init__(self, softcap: float = 0.0, logits_scale: float = 1.0, device="cuda"):
         import torch
@@ -479,6 +490,10 @@ class HeadSampler:
 
     def __call__(self, logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=None,
                  out=None, stream=None):
+        if stream is not None:
+            import torch
+            with torch.cuda.stream(_torch_stream(stream, self.index)):
+                return self(logits, uniforms, temperature, top_k, top_p, min_p, out)
         if (logits.dim() != 2 or logits.get_device() != self.index or logits.shape[1] < 1 or
                 (logits.shape[1] > 1 and logits.stride(1) != 1)):
             raise ValueError("logits: an N x V tensor with unit column stride on "
@@ -506,8 +521,7 @@ class HeadSampler:
         status = self._call(logits.data_ptr(), N, V, logits.stride(0) if N > 1 else V, code, u, t,
                             k, p, m, self.softcap, self.logits_scale, out[0].data_ptr(),
                             out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(),
-                            self.err.data_ptr(),
-                            _raw_stream(self.index) if stream is None else _stream(stream))
+                            self.err.data_ptr(), _raw_stream(self.index))
         if status:
             _check(status, "headloss_sample")
         return out
@@ -529,7 +543,8 @@ class HeadSampler:
 class GradClipper:
     """headloss_clip_grads on torch tensors: the global norm over `grads` and one
     factor on all of them, into `outs` (None: in place).  The tensors are held;
-    `bind` takes others.  Calling it returns the device tensor (norm, factor)."""
+    `bind` takes others.  Calling it returns the device tensor (norm, factor), made on
+    `stream` as under torch.cuda.stream."""
 
     def __init__(self, grads, outs=None, max_grads: int = 0):
         self.h = None
@@ -569,11 +584,14 @@ class GradClipper:
         self._empty, self._f32 = torch.empty, torch.float32
 
     def __call__(self, max_norm: float, inv_scale: float = 1.0, stats=None, stream=None):
+        if stream is not None:
+            import torch
+            with torch.cuda.stream(_torch_stream(stream, self.index)):
+                return self(max_norm, inv_scale, stats)
         if stats is None:
             stats = self._empty(2, dtype=self._f32, device=self.device)
         status = self._call(self.h, self.table, len(self.grads), max_norm, inv_scale,
-                            stats.data_ptr(),
-                            _raw_stream(self.index) if stream is None else _stream(stream))
+                            stats.data_ptr(), _raw_stream(self.index))
         if status:
             _check(status, "headloss_clip_grads")
         return stats

@@ -531,10 +531,8 @@ class HeadSampler:
         out of range; bit 1: a copy wait gave up)."""
         import torch
         if stream is None:
-            stream = torch.cuda.current_stream()
-        elif isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream)
-        with torch.cuda.stream(stream):
+            stream = torch.cuda.current_stream(self.index)
+        with torch.cuda.stream(_torch_stream(stream, self.index)):
             e = int(self.err.item())
             self.err.zero_()
         return e

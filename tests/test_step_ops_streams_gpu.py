@@ -87,3 +87,14 @@ def test_the_default_stream_by_its_handle(handle):
         got = [*sampler(late, u, stream=handle), clipper(1e9, stream=handle)]
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("handle", [0, 1])
+def test_device_error_waits_for_the_default_stream(handle):
+    x, u = noise(8, 500, "bf16", seed=7)
+    sampler = pkg.HeadSampler()
+    bad = torch.full((8,), -1.0, device="cuda")
+    torch.cuda._sleep(BUSY)
+    sampler(x, u, temperature=bad)
+    assert sampler.device_error(handle) == 1
+    assert sampler.device_error(handle) == 0

@@ -8,6 +8,7 @@ is not built, every call raises.
 from __future__ import annotations
 
 import array
+import contextlib
 import ctypes
 import os
 
@@ -430,7 +431,7 @@ class HeadLoss:
             pass
 
 
-_get_raw_stream = None
+_get_raw_stream = _get_device = None
 
 
 def _raw_stream(device: int) -> int:
@@ -443,14 +444,34 @@ def _raw_stream(device: int) -> int:
     return _get_raw_stream(device)
 
 
+def _current_device() -> int:
+    """The device that the library's calls launch on."""
+    global _get_device
+    if _get_device is None:
+        import torch
+        _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _get_device()
+
+
 def _torch_stream(stream, device: int):
     """The torch stream of a `stream` argument (a torch stream or a handle)."""
     import torch
     if not isinstance(stream, int):
+        if stream.device.index != device:
+            raise ValueError(f"stream: one of cuda:{device} is wanted, not of {stream.device}")
         return stream
     if stream in (0, 1):  # the default stream (NULL, cudaStreamLegacy), which torch has no external for
         return torch.cuda.default_stream(device)
     return torch.cuda.ExternalStream(stream, device)
+
+
+@contextlib.contextmanager
+def _on(device: int, stream):
+    """`device` and a stream of it (None: its current one) as the current ones."""
+    import torch
+    with torch.cuda.device(device), torch.cuda.stream(
+            None if stream is None else _torch_stream(stream, device)):
+        yield
 
 
 class HeadSampler:
@@ -490,9 +511,8 @@ class HeadSampler:
 
     def __call__(self, logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=None,
                  out=None, stream=None):
-        if stream is not None:
-            import torch
-            with torch.cuda.stream(_torch_stream(stream, self.index)):
+        if stream is not None or _current_device() != self.index:
+            with _on(self.index, stream):
                 return self(logits, uniforms, temperature, top_k, top_p, min_p, out)
         if (logits.dim() != 2 or logits.get_device() != self.index or logits.shape[1] < 1 or
                 (logits.shape[1] > 1 and logits.stride(1) != 1)):
@@ -529,10 +549,7 @@ class HeadSampler:
     def device_error(self, stream=None) -> int:
         """Synchronise `stream`, then read and clear the error word (bit 0: settings
         out of range; bit 1: a copy wait gave up)."""
-        import torch
-        if stream is None:
-            stream = torch.cuda.current_stream(self.index)
-        with torch.cuda.stream(_torch_stream(stream, self.index)):
+        with _on(self.index, stream):
             e = int(self.err.item())
             self.err.zero_()
         return e
@@ -549,7 +566,8 @@ class GradClipper:
         self.max_grads = max(int(max_grads), len(grads), 1)
         self.bind(grads, outs)
         self._call = load_library().headloss_clip_grads
-        self.h = headloss_clip_create(self.max_grads)
+        with _on(self.index, None):
+            self.h = headloss_clip_create(self.max_grads)
 
     def bind(self, grads, outs=None) -> None:
         import torch
@@ -582,9 +600,8 @@ class GradClipper:
         self._empty, self._f32 = torch.empty, torch.float32
 
     def __call__(self, max_norm: float, inv_scale: float = 1.0, stats=None, stream=None):
-        if stream is not None:
-            import torch
-            with torch.cuda.stream(_torch_stream(stream, self.index)):
+        if stream is not None or _current_device() != self.index:
+            with _on(self.index, stream):
                 return self(max_norm, inv_scale, stats)
         if stats is None:
             stats = self._empty(2, dtype=self._f32, device=self.device)

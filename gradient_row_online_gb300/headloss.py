@@ -578,7 +578,13 @@ class GradClipper:
                              f"{self.max_grads})")
         codes = {torch.float32: HEADLOSS_FP32, torch.bfloat16: HEADLOSS_BF16,
                  torch.float16: HEADLOSS_FP16}
+        if self.h:  # the workspace's device
+            index = self.index
+        else:
+            index = grads[0].get_device() if grads else torch.cuda.current_device()
         for g, o in zip(grads, outs):
+            if g.get_device() != index:
+                raise ValueError(f"gradients: tensors on cuda:{index} are wanted, not on {g.device}")
             if not g.is_cuda or not g.is_contiguous() or o is not g and (
                     not o.is_contiguous() or o.dtype is not g.dtype or o.shape != g.shape or
                     o.get_device() != g.get_device()):
@@ -595,8 +601,7 @@ class GradClipper:
             words[4 * j + 3] = codes[g.dtype]
         self.grads, self.outs, self.words = grads, outs, words
         self.table = ctypes.cast(words.buffer_info()[0], ctypes.POINTER(headloss_gradient))
-        self.index = grads[0].get_device() if grads else torch.cuda.current_device()
-        self.device = torch.device("cuda", self.index)
+        self.index, self.device = index, torch.device("cuda", index)
         self._empty, self._f32 = torch.empty, torch.float32
 
     def __call__(self, max_norm: float, inv_scale: float = 1.0, stats=None, stream=None):

@@ -157,3 +157,20 @@ def test_tensors_of_another_device_are_refused(machine):
         with pytest.raises(ValueError):
             s(Tensor((3, 10), device=x), Tensor((3,), torch.float64, u))
     assert not machine.calls
+
+
+def test_gradients_of_two_devices_are_refused(machine):
+    for devices in ((0, 1), (1, 0), (0, -1)):
+        with pytest.raises(ValueError):
+            hlb.GradClipper([Tensor((5,), device=d) for d in devices])
+    assert not machine.calls
+
+
+def test_binding_to_another_device_than_the_workspaces_is_refused(machine):
+    c = clipper_on(machine, 1)
+    with pytest.raises(ValueError):
+        c.bind([Tensor((5,), device=0)])
+    c.bind([Tensor((7,), device=1)])
+    c.bind([])  # stays on its device
+    c(1.0, stats=Tensor((2,), device=1))
+    assert machine.calls[-1][1] == 1

@@ -610,6 +610,9 @@ class GradClipper:
                 return self(max_norm, inv_scale, stats)
         if stats is None:
             stats = self._empty(2, dtype=self._f32, device=self.device)
+        elif (stats.dtype is not self._f32 or stats.numel() != 2 or
+              stats.get_device() != self.index or not stats.is_contiguous()):
+            raise ValueError(f"stats: a contiguous {self._f32} tensor of 2 on {self.device} is wanted")
         status = self._call(self.h, self.table, len(self.grads), max_norm, inv_scale,
                             stats.data_ptr(), _raw_stream(self.index))
         if status:

@@ -174,3 +174,16 @@ def test_binding_to_another_device_than_the_workspaces_is_refused(machine):
     c.bind([])  # stays on its device
     c(1.0, stats=Tensor((2,), device=1))
     assert machine.calls[-1][1] == 1
+
+
+@pytest.mark.parametrize("stats", [Tensor((2,), torch.float64), Tensor((2,), torch.int32), Tensor((1,)),
+                                   Tensor((3,)), Tensor((0,)), Tensor((2,), device=1), Tensor((2,), device=-1),
+                                   Tensor((2,), contiguous=False)])
+def test_stats_that_the_call_cannot_write_are_refused(machine, stats):
+    c = clipper_on(machine, 0)
+    machine.calls.clear()
+    with pytest.raises(ValueError):
+        c(1.0, stats=stats)
+    assert not machine.calls
+    mine = Tensor((2,))
+    assert c(1.0, stats=mine) is mine and len(machine.calls) == 1

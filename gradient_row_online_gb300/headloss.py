@@ -563,6 +563,7 @@ class GradClipper:
 
     def __init__(self, grads, outs=None, max_grads: int = 0):
         self.h = None
+        grads = list(grads)
         self.max_grads = max(int(max_grads), len(grads), 1)
         self.bind(grads, outs)
         self._call = load_library().headloss_clip_grads

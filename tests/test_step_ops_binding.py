@@ -187,3 +187,9 @@ def test_stats_that_the_call_cannot_write_are_refused(machine, stats):
     assert not machine.calls
     mine = Tensor((2,))
     assert c(1.0, stats=mine) is mine and len(machine.calls) == 1
+
+
+def test_gradients_and_outputs_from_generators(machine):
+    c = hlb.GradClipper((Tensor((n,)) for n in (3, 4)), (Tensor((n,)) for n in (3, 4)))
+    machine.clippers.append(c)
+    assert c.max_grads == 2 and [g.shape for g in c.grads] == [(3,), (4,)] and len(c.outs) == 2

@@ -245,9 +245,10 @@ __device__ __forceinline__ double sum_tile(const Entry& t, uint32_t tile, int la
     }
     const float sum = (s[0] + s[1]) + (s[2] + s[3]);
     if (sum >= 1e-24f && sum <= 1e36f) return double(sum);
+    // (2^100: a sum below 1e-24 comes to 1.6e36 at most, the least subnormal's square to 2^-98)
     const bool low = sum < 1e-24f;
-    return double(any_tile<D>(t, tile, lane, low ? 0x1p+60f : 0x1p-70f, false)) *
-           (low ? 0x1p-120 : 0x1p+140);
+    return double(any_tile<D>(t, tile, lane, low ? 0x1p+100f : 0x1p-70f, false)) *
+           (low ? 0x1p-200 : 0x1p+140);
 }
 
 // The clipped tile; `here`: the lane's part is in d and `edge`.

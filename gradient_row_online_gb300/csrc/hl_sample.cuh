@@ -479,7 +479,10 @@ struct Row {
                 m.add(v);
             }
         }
-        return warp_add(m.sum());
+        // (a segment of the longest row holds 2^25 tokens, their sum 2^61 units; 64 segments of
+        // rows that are not resident are added in units of 2^-32, up to 2^63)
+        const u64 sum = warp_add(m.sum());
+        return RES ? sum : (sum + 8) >> 4;
     }
 
     // Bin of the order: 1/32 octave of mass a bin without a softcap (with one, of the raw
@@ -534,7 +537,7 @@ struct Row {
         const float zz = z(v);
         if (a.logprobs)
             a.logprobs[row] = (zz == zm ? 0.f : __fsub_rn(zz, zm) * a.K * LN2) -
-                              logf(float(model) * 0x1p-36f);
+                              logf(float(model) * (RES ? 0x1p-36f : 0x1p-32f));
         if (a.draw_logprobs)
             a.draw_logprobs[row] = exponent(v) * LN2 - logf(float(W) * 0x1p-30f);
         if (a.n_kept) a.n_kept[row] = kept;

@@ -46,3 +46,15 @@ def test_capped_rows_with_infinite_logits(v, s, t, dtype):
     x[2, ::5] = math.inf
     for f in ({}, dict(p=0.9), dict(p=0.0), dict(k=40, p=0.9), dict(k=700, p=0.5), dict(m=0.5, p=0.7)):
         check(x, u, 30.0, s, t=t, **f)
+
+
+@pytest.mark.parametrize("v", [(1 << 28) - 3, 1 << 28, (1 << 30) + 5])
+def test_log_probs_of_rows_past_two_to_the_28_tokens(v):
+    x = torch.zeros(1, v, dtype=torch.bfloat16, device="cuda")
+    u = torch.tensor([0.625], dtype=torch.float64, device="cuda")
+    for t in (None, 0.5):
+        tok, lp, dlp, kept = pkg.HeadSampler()(x, u, temperature=t)
+        assert int(tok) == math.floor(0.625 * v) and int(kept) == v
+        want = -math.log(v)
+        assert abs(float(lp) - want) <= 2e-6 + 2e-6 * abs(want)
+        assert abs(float(dlp) - want) <= 2e-6 + 2e-6 * abs(want)

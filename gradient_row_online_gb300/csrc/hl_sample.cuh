@@ -321,6 +321,7 @@ struct Row {
     int par = 0;
     bool inf_row = false;
     float top, zm, c;
+    float zt;            // the largest logit's z in the model's log-prob (CAPPED)
 
     __device__ Row(const Args& a_, Shared& s_) : a(a_), s(s_) {}
 
@@ -418,36 +419,48 @@ struct Row {
             return u64(int64_t(high) * (1 << 23) + int64_t(low));
         }
     };
-    // z of a word for the model's mass: with a softcap by the loss's degree-5 fit of tanh (5.8e-8
-    // relative on |x / c| <= 0.8) where all of the word allows it, two logits an instruction; the
+    // z of the model's log-prob: with a softcap by the loss's degree-5 fit of tanh (5.8e-8
+    // relative on |x / c| <= 0.8) where a logit allows it, two logits an instruction; the
     // library's tanhf, which the draw's integer weights take, would be most of the pass
-    // (38 instructions a token instead of 26 on capped rows).
+    // (38 instructions a token instead of 26 on capped rows).  Fit and tanhf differ by up to 8e-6 at
+    // c = 50, so which of them a logit takes depends on that logit alone, in the sum, for the
+    // largest and for the drawn token: a row's one dominant token has log p = 0.
+    __device__ __forceinline__ hl::f2 fit_z(hl::f2 x) const {
+        const hl::f2 y = hl::mul2(x, hl::pk1(a.inv_cap)), y2 = hl::mul2(y, y);
+        hl::f2 p = hl::fma2(hl::pk1(HL_TANH_B_C5), y2, hl::pk1(HL_TANH_B_C4));
+        p = hl::fma2(p, y2, hl::pk1(HL_TANH_B_C3));
+        p = hl::fma2(p, y2, hl::pk1(HL_TANH_B_C2));
+        p = hl::fma2(p, y2, hl::pk1(HL_TANH_B_C1));
+        p = hl::fma2(p, y2, hl::pk1(HL_TANH_B_C0));
+        return hl::mul2(x, p);  // c tanh(x / c) = x P((x / c)^2)
+    }
+    __device__ __forceinline__ bool fits(float v) const {  // (a NaN, which has no mass, either way)
+        return __fmul_rn(fabsf(v), a.inv_cap) <= HL_TANH_B_Y0;
+    }
+    __device__ __forceinline__ float model_z(float v) const {
+        if constexpr (CAPPED) return fits(v) ? hl::lo_of(fit_z(hl::pk1(v))) : z(v);
+        else return v;
+    }
+    __device__ __forceinline__ float model_top() const {
+        if constexpr (CAPPED) return zt;
+        else return zm;
+    }
     __device__ __forceinline__ void model_z(const float* v, hl::f2* zz) const {
         if constexpr (CAPPED) {
             float far = 0.f;
 #pragma unroll
             for (int e = 0; e < EPW; ++e) far = fmaxf(far, fabsf(v[e]));
-            if (far * a.inv_cap <= HL_TANH_B_Y0) {
-                const hl::f2 inv = hl::pk1(a.inv_cap);
+            if (fits(far)) {
 #pragma unroll
-                for (int i = 0; i < PAIRS; ++i) {
-                    const hl::f2 x = hl::pk(v[2 * i], v[2 * i + 1]), y = hl::mul2(x, inv);
-                    const hl::f2 y2 = hl::mul2(y, y);
-                    hl::f2 p = hl::fma2(hl::pk1(HL_TANH_B_C5), y2, hl::pk1(HL_TANH_B_C4));
-                    p = hl::fma2(p, y2, hl::pk1(HL_TANH_B_C3));
-                    p = hl::fma2(p, y2, hl::pk1(HL_TANH_B_C2));
-                    p = hl::fma2(p, y2, hl::pk1(HL_TANH_B_C1));
-                    p = hl::fma2(p, y2, hl::pk1(HL_TANH_B_C0));
-                    zz[i] = hl::mul2(x, p);  // c tanh(x / c) = x P((x / c)^2)
-                }
+                for (int i = 0; i < PAIRS; ++i) zz[i] = fit_z(hl::pk(v[2 * i], v[2 * i + 1]));
                 return;
             }
         }
 #pragma unroll
-        for (int i = 0; i < PAIRS; ++i) zz[i] = hl::pk(z(v[2 * i]), z(v[2 * i + 1]));
+        for (int i = 0; i < PAIRS; ++i) zz[i] = hl::pk(model_z(v[2 * i]), model_z(v[2 * i + 1]));
     }
     __device__ __forceinline__ void add_model(Model& m, const float* v) const {
-        const hl::f2 nz = hl::pk1(-zm), kk = hl::pk1(a.K);
+        const hl::f2 nz = hl::pk1(-model_top()), kk = hl::pk1(a.K);
         float sh[EPW];
         hl::f2 zz[PAIRS];
         model_z(v, zz);
@@ -471,10 +484,10 @@ struct Row {
                 float v[EPW];
                 values(i, v);
                 for (int e = 0; e < EPW; ++e) {
-                    const float zz = z(v[e]);
+                    const float zz = model_z(v[e]), zt = model_top();
                     v[e] = !(v[e] > -CUDART_INF_F) ? 0.f
-                           : zz == zm              ? 1.f
-                                      : ex2f(__fmul_rn(__fsub_rn(zz, zm), a.K));
+                           : zz == zt              ? 1.f
+                                      : ex2f(__fmul_rn(__fsub_rn(zz, zt), a.K));
                 }
                 m.add(v);
             }
@@ -534,9 +547,9 @@ struct Row {
     }
     __device__ void answer(float v, int idx, u64 W, u64 model, int kept) const {
         a.tokens[row] = idx;
-        const float zz = z(v);
+        const float zz = model_z(v), zt = model_top();
         if (a.logprobs)
-            a.logprobs[row] = (zz == zm ? 0.f : __fsub_rn(zz, zm) * a.K * LN2) -
+            a.logprobs[row] = (zz == zt ? 0.f : __fsub_rn(zz, zt) * a.K * LN2) -
                               logf(float(model) * (RES ? 0x1p-36f : 0x1p-32f));
         if (a.draw_logprobs)
             a.draw_logprobs[row] = exponent(v) * LN2 - logf(float(W) * 0x1p-30f);
@@ -1469,6 +1482,7 @@ __global__ void __launch_bounds__(THREADS, 4) sample_kernel(const __grid_constan
         return;
     }
     r.zm = r.z(r.top);
+    if constexpr (CAPPED) r.zt = r.model_z(r.top);
 
     if (small_k) {
         const uint32_t edge = max(__reduce_max_sync(FULL, uint32_t(edges >> 32)),

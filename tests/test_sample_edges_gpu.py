@@ -58,3 +58,21 @@ def test_log_probs_of_rows_past_two_to_the_28_tokens(v):
         want = -math.log(v)
         assert abs(float(lp) - want) <= 2e-6 + 2e-6 * abs(want)
         assert abs(float(dlp) - want) <= 2e-6 + 2e-6 * abs(want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("cap", [30.0, 50.0])
+@pytest.mark.parametrize("beside", [0.0, 0.95])
+def test_a_dominant_token_of_a_capped_row(beside, cap, dtype):
+    """Its log-prob is 0 whatever its logit, in the range of the fit of tanh or past it, alone in its
+    word or beside a logit past the fit's range."""
+    n, v = 96, 1000
+    x, _ = noise(n, v, dtype, seed=1, sigma=0.01)
+    x -= 0.5 * cap
+    at = torch.arange(n, device="cuda") * 10 + 5
+    x[torch.arange(n), at] = (cap * torch.linspace(0.45, 0.9, n, device="cuda")).to(x.dtype)
+    if beside:
+        x[torch.arange(n), at + 1] = -beside * cap
+    u = torch.full((n,), 0.5, dtype=torch.float64, device="cuda")
+    for f in ({}, dict(t=0.8, k=40, p=0.9), dict(p=0.9), dict(k=500)):
+        assert np.array_equal(check(x, u, cap, **f), at.cpu().numpy())

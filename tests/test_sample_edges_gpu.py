@@ -76,3 +76,22 @@ def test_a_dominant_token_of_a_capped_row(beside, cap, dtype):
     u = torch.full((n,), 0.5, dtype=torch.float64, device="cuda")
     for f in ({}, dict(t=0.8, k=40, p=0.9), dict(p=0.9), dict(k=500)):
         assert np.array_equal(check(x, u, cap, **f), at.cpu().numpy())
+
+
+@pytest.mark.parametrize("dtype,v", [("bf16", 800_003), ("fp16", 1_000_001), ("fp32", 500_009)])
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+def test_rows_that_are_not_resident(cap, dtype, v):
+    """Rows past eight CTAs' shared memory, read from global memory in every pass: ordinary ones,
+    few-valued ones, masked ones and +inf, on every way through the kernel."""
+    x, u = noise(6, v, dtype, seed=v, sigma=2.0, pitch=v + 3)
+    x[1] = (x[1].float() / 2).round().to(x.dtype)  # a few values
+    x[2, ::3] = -math.inf
+    x[2, 1::7] = math.nan
+    x[3, [5, v // 2, v - 1]] = math.inf
+    x[4] = -math.inf
+    x[5, :v - 9] = -math.inf
+    for f in ({}, dict(t=0.7, k=40, p=0.9), dict(p=0.9), dict(p=0.3, m=0.2), dict(k=5000), dict(k=3000, p=0.9),
+              dict(t=0.0), dict(m=0.05)):
+        tok = check(x, u, cap, **f)
+        assert tok[4] == -1 and tok[5] >= v - 9
+        assert cap or tok[3] in (5, v // 2, v - 1)

@@ -6,6 +6,17 @@
 #include "headloss_sample.h"
 #include "hl_sample.cuh"
 
+#ifdef HL_FAULT_INJECT
+// Test builds alone: the calls that follow leave out the copies of row `drop_row` (-1: none), and
+// their waits give up after `wait_ns` (0: the usual limit).
+static int64_t g_drop_row = -1;
+static unsigned long long g_wait_ns = hl_sample::WAIT_NS;
+extern "C" void headloss_sample_test_inject(int64_t drop_row, unsigned long long wait_ns) {
+    g_drop_row = drop_row;
+    g_wait_ns = wait_ns ? wait_ns : hl_sample::WAIT_NS;
+}
+#endif
+
 extern "C" int headloss_sample(const void* logits, int64_t N, int64_t V, int64_t ld, int dtype,
                                const double* uniforms, const float* temperature,
                                const int32_t* top_k, const float* top_p, const float* min_p,
@@ -47,6 +58,10 @@ extern "C" int headloss_sample(const void* logits, int64_t N, int64_t V, int64_t
     a.draw_logprobs = draw_logprobs;
     a.n_kept = n_kept;
     a.err = err;
+#ifdef HL_FAULT_INJECT
+    a.drop_row = g_drop_row;
+    a.wait_ns = g_wait_ns;
+#endif
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int device = 0, sms = 0;
     if (cudaGetDevice(&device) != cudaSuccess ||

@@ -90,6 +90,10 @@ struct Args {
     float* draw_logprobs;
     int32_t* n_kept;
     int* err;
+#ifdef HL_FAULT_INJECT
+    int64_t drop_row;  // its copies are left out (-1: none)
+    unsigned long long wait_ns;
+#endif
 };
 
 typedef unsigned long long u64;
@@ -1422,6 +1426,9 @@ __global__ void __launch_bounds__(THREADS, 4) sample_kernel(const __grid_constan
             hl::fence_proxy_async();
             if (f1 > f0) {
                 hl::mbar_arrive_expect_tx(bar, uint32_t(f1 - f0) * 16);
+#ifdef HL_FAULT_INJECT
+                if (r.row != a.drop_row)
+#endif
                 bulk_g2s(smem_addr(words + f0), r.gwords + r.w0 + f0, uint32_t(f1 - f0) * 16, bar);
             }
         }
@@ -1451,9 +1458,14 @@ __global__ void __launch_bounds__(THREADS, 4) sample_kernel(const __grid_constan
         r.clear_histogram();
     }
     if constexpr (RES) {
-        if (f1 > f0 && !hl::mbar_wait_bounded(bar, 0, WAIT_NS)) {
+#ifdef HL_FAULT_INJECT
+        const unsigned long long limit = a.wait_ns;
+#else
+        constexpr unsigned long long limit = WAIT_NS;
+#endif
+        if (f1 > f0 && !hl::mbar_wait_bounded(bar, 0, limit)) {
             lost = true;
-            hl::mbar_wait_bounded(bar, 0, WAIT_NS);  // so that the copy does not land later
+            hl::mbar_wait_bounded(bar, 0, limit);  // so that the copy does not land later
         }
         __syncwarp();
     }
@@ -1556,8 +1568,9 @@ constexpr int SLICE = 38 * 1024;
 constexpr int SLICE_UNFILTERED = 50 * 1024;
 constexpr int SLICE_MOST = 192 * 1024;
 
+// (static, so that `done` is this library's own where a process holds two copies of it)
 template <typename DT, bool CAPPED>
-int launch(Args a, int64_t N, int device, int sms, cudaStream_t st) {
+static int launch(Args a, int64_t N, int device, int sms, cudaStream_t st) {
     const int64_t words = (int64_t(a.V) * sizeof(DT) + 30) / 16;  // at most, wherever rows start
     auto slice = [&](int c) { return (words + c - 1) / c * 16; };
     int C = 1;

@@ -1447,7 +1447,7 @@ __global__ void __launch_bounds__(THREADS, 4) sample_kernel(const __grid_constan
     const bool bad = !(temp >= 0.f && temp < CUDART_INF_F) ||
                      !(ubits < 0x3ff0000000000000ull || ubits == 0x8000000000000000ull) ||
                      !(p >= 0.f) || !(least >= 0.f && least <= 1.f);
-    r.c = __fdiv_rn(a.K, temp + 0.f);  // (-0 as +0: a negative c would send the bins out of range)
+    r.c = __fdiv_rn(a.K, fabsf(temp));  // (of -0 too: a negative c would send the bins out of range)
     const bool greedy = !(r.c < CUDART_INF_F);
     if (greedy) r.c = a.K;
     const int k = greedy ? 1 : want_k <= 0 || want_k > a.V ? a.V : want_k;

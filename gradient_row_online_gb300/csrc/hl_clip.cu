@@ -5,7 +5,8 @@
 // across two tensors; a CTA takes a contiguous run of tiles, its warps in turn, eight words a
 // lane in flight.
 //   phase 1   squares, in fp32 over a lane's share of one tile (at most 64), in
-//             fp64 from there on, in an order that the sizes and the grid fix;
+//             fp64 from there on, in an order that the sizes, the addresses modulo 16 and the
+//             grid fix;
 //   barrier   over the grid (bounded); the last CTA to arrive joins the CTAs' sums in
 //             their order and publishes the factor.  A CTA that waits too long publishes a
 //             failure instead; whichever comes first holds for all, and after a failure none
@@ -14,9 +15,11 @@
 //   phase 2   the run again, backwards: the last tile is still in registers, the ones before it
 //             still in L2.  In place with factor 1 it is left out.
 // The factor needs the whole norm first, so gradients beyond what the chip holds are read
-// twice: 3 n bytes where the operator's own floor is 2 n.  Measured on 4.23 GB of fp32 in 288 tensors:
-// 1,870-1,910 us, the measured copy bandwidth on 3 n; on 59 MB of bf16 in 448: 28.6 us against 17.5
-// at 2 n, the barrier and the short phases' starts being the difference.
+// twice: 3 n bytes where the operator's own floor is 2 n.  Measured on 4.23 GB of fp32 in 353 tensors:
+// 1,890 us, the measured copy bandwidth on 3 n; on 59 MB of bf16 in 448, whose second read is from L2:
+// 30.7 us (28.6 on the GPU alone) against 17.5 at 2 n, the barrier and the short phases' starts being
+// the difference.  In place without clipping the second phase is left out: 288 tensors of 1.06 G
+// fp32 640 us, one read at the copy bandwidth.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>

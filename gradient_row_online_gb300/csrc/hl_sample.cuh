@@ -30,7 +30,7 @@
 // What bounds it: barriers and the leader's last step, two to four a row, each a microsecond
 // or two, at 56-62% of the issue slots; every logit comes from HBM once.  Measured (logits' bytes
 // over the time): 1024 x 151936 bf16 unfiltered 118 us, 2.6 TB/s; 1024 x 128256 top-p 248 us,
-// 1.1 TB/s; 8192 x 32000 top-k and top-p 263 us, 2.0 TB/s; 512 x 128256 fp16 capped 83 us, 1.6 TB/s;
+// 1.1 TB/s; 8192 x 32000 top-k and top-p 264 us, 2.0 TB/s; 512 x 128256 fp16 capped 86 us, 1.5 TB/s;
 // one row of 32000 8.3 us.
 #pragma once
 #include <cuda_bf16.h>

@@ -9,10 +9,11 @@
  * inv_scale takes off what the loss's grad_scale put on.  A norm that is not finite leaves
  * the factor at inv_scale: the caller reads the norm and skips the step.
  *
- * Squares are summed in fp32 over at most a few hundred elements and from there on in fp64,
- * in an order that depends on the sizes alone (the same result every time); a run of squares that leaves
- * fp32's range is summed again from scaled values, so the norm is right over the whole range
- * of the types.
+ * Squares are summed in fp32 over at most a few hundred elements and from there on in fp64, in
+ * an order that the sizes, the addresses modulo 16 bytes and the GPU's number of SMs fix (the same
+ * result every time for the same list on the same GPU); a run of squares that leaves
+ * fp32's range, or comes near its lower end, is summed again from scaled values, so the sum is right
+ * over the whole range of the types, subnormal values among them; the norm is its root, rounded to fp32.
  *
  * Status codes are those of headloss.h.
  */

@@ -482,7 +482,8 @@ class HeadSampler:
     int32), numbers for every row, or None (off).  Returns (tokens int64, log p
     at T = 1 of the whole softmax fp32, log p under the distribution drawn from
     fp32, tokens that could be drawn int32); `out` gives the four buffers.  With
-    `stream` the call is as under torch.cuda.stream: its own tensors are made there."""
+    `stream` the call is as under torch.cuda.stream: its own tensors are made there.
+    (The error word is made with the sampler, on the stream that is current then.)"""
 
     def __init__(self, softcap: float = 0.0, logits_scale: float = 1.0, device="cuda"):
         import torch

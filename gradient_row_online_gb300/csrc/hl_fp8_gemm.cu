@@ -1,0 +1,684 @@
+// hl_fp8_gemm.cu -- headloss_fp8_matmul (include/headloss_fp8.h): out = a . b^T of 8-bit
+// matrices, a's scales for each row and 128 columns, b's for each 128 x 128.
+//
+// The tensor cores sum a K block of 128 (four tcgen05.mma kind::f8f6f4, K = 32 each) into one of
+// two TMEM accumulators; the epilogue warps read it back and add it, times its scales, to fp32
+// sums in registers while the next block's MMAs fill the other accumulator.  So each block's
+// scale is applied exactly once, in fp32, and a sum over K never lives in the accumulator for more
+// than 128 products.
+//
+// wide_kernel (more than 64 rows of a): persistent, one CTA an SM, 128 x 256 tiles of out; per K
+// block the MMAs take 512 cycles at the full rate and the scaled sums 32768 FMAs, 256 cycles of the
+// FMA pipe.  With fewer tiles than half the SMs, K is split; the parts go to the workspace in fp32
+// and a second kernel adds them in order.
+// narrow_kernel (up to 64 rows of a): b's rows are the MMA's 128 rows and a's its 16, 32 or 64
+// columns, so that b streams through once at HBM's rate.  A cluster of up to 8 CTAs splits K
+// and joins its sums over DSMEM.
+// Every wait is bounded; one that gives up sets bit 0 of *err, and the kernel drains what it issued.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "headloss.h"
+#include "headloss_fp8.h"
+#include "hl_pack.cuh"
+#include "hl_tc.cuh"
+
+namespace hl_fp8 {
+
+using namespace hl_tc;
+
+constexpr int BK = 128;              // one scale block, one swizzle row of bytes
+constexpr uint32_t IDESC_FIXED = 1u << 4;  // D is fp32; A and B K-major
+
+__host__ __device__ constexpr uint32_t idesc_of(int m, int n, int a_type, int b_type) {
+    return IDESC_FIXED | uint32_t(a_type) << 7 | uint32_t(b_type) << 10 | uint32_t(n >> 3) << 17 |
+           uint32_t(m >> 4) << 24;
+}
+
+template <int OT>
+__device__ __forceinline__ uint32_t round2(float a, float b) {  // two 16-bit outputs
+    if (OT == HEADLOSS_BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <int OT>
+__device__ __forceinline__ void store1(void* out, int64_t i, float v) {
+    if (OT == HEADLOSS_FP32) static_cast<float*>(out)[i] = v;
+    else if (OT == HEADLOSS_BF16) static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
+    else static_cast<__half*>(out)[i] = __float2half_rn(v);
+}
+
+// ------------------------------------------------------------------ wide ----
+
+constexpr int WM = 128, WN = 256;
+constexpr int W_STAGES = 4;
+constexpr int WA_BYTES = WM * BK, WB_BYTES = WN * BK;      // 16 KB, 32 KB
+constexpr int W_STAGE_BYTES = WA_BYTES + WB_BYTES;
+constexpr int W_EPI_WARPS = 8;                              // 2 for each TMEM lane quadrant
+constexpr int W_THREADS = 128 + 32 * W_EPI_WARPS;
+// Launched with 168 registers a thread (64512 a CTA); the warpgroup of the copies and MMAs
+// gives up its share to the two that hold the sums: 128 * 40 + 256 * 224 = 62464.
+constexpr int W_LAUNCH_REGS = 168, W_FEW_REGS = 40, W_SUM_REGS = 224;
+static_assert(128 * W_FEW_REGS + 32 * W_EPI_WARPS * W_SUM_REGS <= W_THREADS * W_LAUNCH_REGS, "registers");
+constexpr int W_OUT_BYTES = 32 * 128;                       // 32 rows x 128 bytes of one warp
+constexpr int W_OUT_OFF = W_STAGES * W_STAGE_BYTES;
+constexpr int W_BAR_OFF = W_OUT_OFF + W_EPI_WARPS * W_OUT_BYTES;
+constexpr int W_SMEM = W_BAR_OFF + 256 + 1024;
+static_assert(W_SMEM <= 232448, "shared memory");
+constexpr int GN = 16;                                      // column tiles a group of the tile order
+
+struct WideArgs {
+    const float* a_scales;  // [KB][M]
+    const float* b_scales;  // [NB][KB]
+    int64_t M, N;
+    int KB, NB, MT, NT;
+    int splits;
+    int64_t mpad;           // rows between two parts of the workspace
+    void* out;
+    int64_t ldo;
+    int tma_out;            // rows of out start on 16-byte boundaries
+    int n_even;             // and end on them
+    uint32_t idesc;
+    int* err;
+};
+
+// Position i of the tile order: GN column tiles at a time, every row tile within a group.
+__device__ __forceinline__ void tile_at(uint32_t i, uint32_t MT, uint32_t NT, int& m, int& n) {
+    const uint32_t per = MT * GN, g = i / per;
+    const uint32_t w = i - g * per, wide = min(NT - g * GN, uint32_t(GN));
+    m = int(w / wide);
+    n = int(g * GN + w % wide);
+}
+
+template <int OT>
+__global__ void __launch_bounds__(W_THREADS, 1)
+    wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                const __grid_constant__ CUtensorMap map_o, const WideArgs p) {
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + W_BAR_OFF);
+    uint64_t* empty = full + W_STAGES;
+    uint64_t* tfull = empty + W_STAGES;  // [2] a block's sums are in the accumulator
+    uint64_t* tempty = tfull + 2;        // [2] the accumulator was read (an arrival a warp)
+    uint64_t* mma_done = tempty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+    volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t items = uint32_t(p.MT) * p.NT * p.splits;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < W_STAGES; ++s) {
+            mbar_init(su32(&full[s]), 1);
+            mbar_init(su32(&empty[s]), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(su32(&tfull[a]), 1);
+            mbar_init(su32(&tempty[a]), W_EPI_WARPS);
+        }
+        mbar_init(su32(mma_done), 1);
+        *abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc(su32(tmem_slot), 512);
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp < 4) {
+        give_registers<W_FEW_REGS>();
+        if (warp == 0 && lane == 0) {  // copies
+            uint32_t it = 0;
+            bool go = true;
+            for (uint32_t i = blockIdx.x; go && i < items; i += gridDim.x) {
+                int m, n;
+                tile_at(i / p.splits, p.MT, p.NT, m, n);
+                const int sp = int(i % p.splits);
+                const int k0 = int(int64_t(p.KB) * sp / p.splits), k1 = int(int64_t(p.KB) * (sp + 1) / p.splits);
+                for (int kb = k0; kb < k1; ++kb, ++it) {
+                    const int s = int(it % W_STAGES);
+                    const uint32_t ph = (it / W_STAGES) & 1u;
+                    if (!wait_phase(su32(&empty[s]), ph ^ 1u, abort, p.err)) {
+                        go = false;
+                        break;
+                    }
+                    const uint32_t a = su32(smem + s * W_STAGE_BYTES), bar = su32(&full[s]);
+                    mbar_expect_tx(bar, W_STAGE_BYTES);
+                    tma_load_2d(a, &map_a, kb * BK, m * WM, bar);
+                    tma_load_2d(a + WA_BYTES, &map_b, kb * BK, n * WN, bar);
+                }
+            }
+            for (uint32_t j = it > W_STAGES ? it - W_STAGES : 0; j < it; ++j)  // what was issued has landed
+                drain_phase(su32(&full[j % W_STAGES]), (j / W_STAGES) & 1u, p.err);
+        } else if (warp == 1 && lane == 0) {  // MMAs
+            uint32_t it = 0;
+            bool go = true;
+            for (uint32_t i = blockIdx.x; go && i < items; i += gridDim.x) {
+                const int sp = int(i % p.splits);
+                const int k0 = int(int64_t(p.KB) * sp / p.splits), k1 = int(int64_t(p.KB) * (sp + 1) / p.splits);
+                for (int kb = k0; kb < k1; ++kb, ++it) {
+                    const int s = int(it % W_STAGES), acc = int(it & 1u);
+                    if (!wait_phase(su32(&tempty[acc]), ((it >> 1) & 1u) ^ 1u, abort, p.err) ||
+                        !wait_phase(su32(&full[s]), (it / W_STAGES) & 1u, abort, p.err)) {
+                        go = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a = su32(smem + s * W_STAGE_BYTES), b = a + WA_BYTES;
+#pragma unroll
+                    for (int k = 0; k < BK / 32; ++k)
+                        mma_f8(tmem + uint32_t(acc * WN), smem_desc(a + 32 * k), smem_desc(b + 32 * k), p.idesc, k != 0);
+                    mma_commit(su32(&empty[s]));
+                    mma_commit(su32(&tfull[acc]));
+                }
+            }
+            if (it) {  // what was issued is done before TMEM is freed
+                mma_commit(su32(mma_done));
+                drain_phase(su32(mma_done), 0u, p.err);
+            }
+        }
+        __syncwarp();
+    } else {  // scaled sums: warp w has TMEM lanes 32 (w % 4) .., columns 128 h ..
+        take_registers<W_SUM_REGS>();
+        const int q = warp & 3, h = (warp - 4) >> 2;
+        unsigned char* stage = smem + W_OUT_OFF + (warp - 4) * W_OUT_BYTES;
+        uint32_t it = 0;
+        bool go = true;
+        for (uint32_t i = blockIdx.x; go && i < items; i += gridDim.x) {
+            int m, n;
+            tile_at(i / p.splits, p.MT, p.NT, m, n);
+            const int sp = int(i % p.splits);
+            const int k0 = int(int64_t(p.KB) * sp / p.splits), k1 = int(int64_t(p.KB) * (sp + 1) / p.splits);
+            const int64_t row = int64_t(m) * WM + 32 * q + lane;
+            const int nb = min(2 * n + h, p.NB - 1);
+            const bool in = row < p.M;
+            const float* sa = p.a_scales + (in ? row : 0);
+            const float* sb = p.b_scales + int64_t(nb) * p.KB;
+            hl::f2 sum[64];
+#pragma unroll
+            for (int j = 0; j < 64; ++j) sum[j] = 0ull;
+            float fa = in ? __ldg(sa + int64_t(k0) * p.M) : 0.f, fb = __ldg(sb + k0);
+            for (int kb = k0; kb < k1; ++kb, ++it) {
+                const float s = fa * fb;
+                if (kb + 1 < k1) {
+                    fa = in ? __ldg(sa + int64_t(kb + 1) * p.M) : 0.f;
+                    fb = __ldg(sb + kb + 1);
+                }
+                const int acc = int(it & 1u);
+                if (!wait_phase(su32(&tfull[acc]), (it >> 1) & 1u, abort, p.err)) {
+                    go = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t t = tmem + (uint32_t(32 * q) << 16) + uint32_t(acc * WN + 128 * h);
+                const hl::f2 s2 = hl::pk1(s);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float v[32];
+                    tmem_ld32(t + 32 * c, v);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        sum[16 * c + j] = hl::fma2(hl::pk(v[2 * j], v[2 * j + 1]), s2, sum[16 * c + j]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(su32(&tempty[acc]));
+            }
+            if (!go) break;
+            // 128 bytes of 32 rows at a time through shared memory (128-byte swizzle)
+            constexpr int COLS = OT == HEADLOSS_FP32 ? 32 : 64;
+            const int64_t base = p.splits > 1 ? sp * p.mpad : 0;  // rows before this part's
+            const int64_t r0 = int64_t(m) * WM + 32 * q, n0 = int64_t(n) * WN + 128 * h;
+#pragma unroll
+            for (int g = 0; g < 128 / COLS; ++g) {
+                if (lane == 0) bulk_wait_read0();
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    uint4 w;
+                    float f[8];
+                    if (OT == HEADLOSS_FP32) {
+                        hl::upk(sum[16 * g + 2 * c], f[0], f[1]);
+                        hl::upk(sum[16 * g + 2 * c + 1], f[2], f[3]);
+                        w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                                       __float_as_uint(f[3]));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) hl::upk(sum[32 * g + 4 * c + j], f[2 * j], f[2 * j + 1]);
+                        w = make_uint4(round2<OT>(f[0], f[1]), round2<OT>(f[2], f[3]), round2<OT>(f[4], f[5]),
+                                       round2<OT>(f[6], f[7]));
+                    }
+                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) * 16)) = w;
+                }
+                const int64_t c0 = n0 + g * COLS;
+                // a store that TMA clips at N would still write whole 16-byte units
+                if (p.tma_out && (p.n_even || c0 + COLS <= p.N)) {
+                    fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0 && r0 < p.M && c0 < p.N) {
+                        tma_store_2d(&map_o, int(c0), int(base + r0), su32(stage));
+                        bulk_commit();
+                    }
+                } else {
+                    __syncwarp();
+                    constexpr int SIZE = OT == HEADLOSS_FP32 ? 4 : 2;
+                    for (int r = 0; r < 32 && r0 + r < p.M; ++r)
+#pragma unroll
+                        for (int x = 0; x < COLS / 32; ++x) {
+                            const int e = lane + 32 * x, byte = e * SIZE;
+                            const unsigned char* src = stage + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15);
+                            if (c0 + e < p.N) {
+                                const int64_t at = (r0 + r) * p.ldo + c0 + e;
+                                if (SIZE == 4) static_cast<uint32_t*>(p.out)[at] = *reinterpret_cast<const uint32_t*>(src);
+                                else static_cast<uint16_t*>(p.out)[at] = *reinterpret_cast<const uint16_t*>(src);
+                            }
+                        }
+                    __syncwarp();
+                }
+            }
+        }
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// The parts of a split K, added in their order.
+template <int OT>
+__global__ void __launch_bounds__(256) join_kernel(const float* __restrict__ parts, int splits, int64_t mpad,
+                                                   int64_t ldw, int64_t M, int64_t N, void* out, int64_t ldo) {
+    const int64_t words = ldw / 4, total = M * words;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
+        const int64_t row = i / words, col = (i - row * words) * 4;
+        float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s = 0; s < splits; ++s) {
+            const float4 u = *reinterpret_cast<const float4*>(parts + (s * mpad + row) * ldw + col);
+            t.x += u.x, t.y += u.y, t.z += u.z, t.w += u.w;
+        }
+        const float f[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (col + j < N) store1<OT>(out, row * ldo + col + j, f[j]);
+    }
+}
+
+// ---------------------------------------------------------------- narrow ----
+
+constexpr int N_STAGES = 4;
+constexpr int N_EPI_WARPS = 4;
+constexpr int N_THREADS = 64 + 32 * N_EPI_WARPS;
+constexpr int NW_BYTES = 128 * BK;  // 128 rows of b, a K block
+
+template <int NT>
+struct Narrow {
+    static constexpr int STAGE = NW_BYTES + NT * BK;
+    static constexpr int SCALE_OFF = N_STAGES * STAGE;          // [2][NT] products of scales
+    static constexpr int BAR_OFF = SCALE_OFF + 2 * NT * 4;
+    static constexpr int SMEM = BAR_OFF + 256 + 1024;
+    static constexpr int TMEM = 2 * NT < 32 ? 32 : 2 * NT;
+};
+
+struct NarrowArgs {
+    const float* a_scales;
+    const float* b_scales;
+    int M;
+    int64_t N;
+    int KB;
+    int splits;  // the cluster
+    void* out;
+    int64_t ldo;
+    uint32_t idesc;
+    int* err;
+};
+
+template <int NT, int OT>
+__global__ void __launch_bounds__(N_THREADS)
+    narrow_kernel(const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_a,
+                  const NarrowArgs p) {
+    using L = Narrow<NT>;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float* scale = reinterpret_cast<float*>(smem + L::SCALE_OFF);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
+    uint64_t* empty = full + N_STAGES;
+    uint64_t* tfull = empty + N_STAGES;
+    uint64_t* tempty = tfull + 2;
+    uint64_t* mma_done = tempty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+    volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int S = p.splits, rank = S > 1 ? int(cluster_rank()) : 0;
+    const int tile = blockIdx.x / S;
+    const int k0 = int(int64_t(p.KB) * rank / S), k1 = int(int64_t(p.KB) * (rank + 1) / S);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < N_STAGES; ++s) {
+            mbar_init(su32(&full[s]), 1);
+            mbar_init(su32(&empty[s]), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(su32(&tfull[a]), 1);
+            mbar_init(su32(&tempty[a]), N_EPI_WARPS);
+        }
+        mbar_init(su32(mma_done), 1);
+        *abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc(su32(tmem_slot), L::TMEM);
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    float sum[NT];
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            for (int kb = k0; kb < k1; ++kb, ++it) {
+                const int s = int(it % N_STAGES);
+                const uint32_t ph = (it / N_STAGES) & 1u;
+                if (!wait_phase(su32(&empty[s]), ph ^ 1u, abort, p.err)) break;
+                const uint32_t w = su32(smem + s * L::STAGE), bar = su32(&full[s]);
+                mbar_expect_tx(bar, L::STAGE);
+                tma_load_2d(w, &map_b, kb * BK, tile * 128, bar);
+                tma_load_2d(w + NW_BYTES, &map_a, kb * BK, 0, bar);
+            }
+            for (uint32_t j = it > N_STAGES ? it - N_STAGES : 0; j < it; ++j)
+                drain_phase(su32(&full[j % N_STAGES]), (j / N_STAGES) & 1u, p.err);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            bool issued = false;
+            for (int kb = k0; kb < k1; ++kb) {
+                const uint32_t it = uint32_t(kb - k0);
+                const int s = int(it % N_STAGES), acc = int(it & 1u);
+                if (!wait_phase(su32(&tempty[acc]), ((it >> 1) & 1u) ^ 1u, abort, p.err) ||
+                    !wait_phase(su32(&full[s]), (it / N_STAGES) & 1u, abort, p.err))
+                    break;
+                tc_fence_after();
+                const uint32_t w = su32(smem + s * L::STAGE), x = w + NW_BYTES;
+#pragma unroll
+                for (int k = 0; k < BK / 32; ++k)
+                    mma_f8(tmem + uint32_t(acc * NT), smem_desc(w + 32 * k), smem_desc(x + 32 * k), p.idesc, k != 0);
+                mma_commit(su32(&empty[s]));
+                mma_commit(su32(&tfull[acc]));
+                issued = true;
+            }
+            if (issued) {
+                mma_commit(su32(mma_done));
+                drain_phase(su32(mma_done), 0u, p.err);
+            }
+        }
+    } else {  // a thread has one row of b, every row of a
+        const int q = warp & 3, t = threadIdx.x - 64;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) sum[j] = 0.f;
+        const float* sb = p.b_scales + int64_t(tile) * p.KB;
+        const bool mine = t < NT, in = t < p.M;
+        float next = mine && in && k0 < k1 ? __ldg(p.a_scales + int64_t(k0) * p.M + t) * __ldg(sb + k0) : 0.f;
+        for (int kb = k0; kb < k1; ++kb) {
+            const uint32_t it = uint32_t(kb - k0);
+            const int acc = int(it & 1u);
+            if (mine) scale[acc * NT + t] = next;
+            if (mine && in && kb + 1 < k1) next = __ldg(p.a_scales + int64_t(kb + 1) * p.M + t) * __ldg(sb + kb + 1);
+            named_sync(1, 32 * N_EPI_WARPS);  // the scales of this block; those two blocks back were read
+            if (!wait_phase(su32(&tfull[acc]), (it >> 1) & 1u, abort, p.err)) *abort = 1;
+            tc_fence_after();
+            const uint32_t at = tmem + (uint32_t(32 * q) << 16) + uint32_t(acc * NT);
+#pragma unroll
+            for (int c = 0; c < NT / 16; ++c) {
+                float v[16];
+                tmem_ld16(at + 16 * c, v);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) sum[16 * c + j] = fmaf(v[j], scale[acc * NT + 16 * c + j], sum[16 * c + j]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(su32(&tempty[acc]));
+        }
+    }
+    const int v = (warp & 3) * 32 + lane;  // the tile's row of b (epilogue warps)
+    const int64_t col = int64_t(tile) * 128 + v;
+    if (S == 1) {
+        if (warp >= 2 && col < p.N)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                if (j < p.M) store1<OT>(p.out, j * p.ldo + col, sum[j]);
+    } else {
+        // each CTA of the cluster gets its share of a's rows from all of them: [source][row][128]
+        const int share = NT / S;
+        __syncthreads();
+        __syncwarp();
+        cluster_sync();  // no CTA's ring is in use any more
+        if (warp >= 2)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const int peer = j / share;
+                const uint32_t at = su32(smem) + uint32_t(((rank * share + j - peer * share) * 128 + v) * 4);
+                st_peer(map_peer(at, uint32_t(peer)), sum[j]);
+            }
+        cluster_sync();
+        if (warp >= 2) {
+            const float* part = reinterpret_cast<const float*>(smem);
+            for (int j = 0; j < share; ++j) {
+                float t = 0.f;
+                for (int r = 0; r < S; ++r) t += part[(r * share + j) * 128 + v];
+                const int64_t row = rank * share + j;
+                if (row < p.M && col < p.N) store1<OT>(p.out, row * p.ldo + col, t);
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, L::TMEM);
+    }
+}
+
+// ------------------------------------------------------------------ host ----
+
+int make_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, int64_t rows, int64_t cols,
+             int64_t pitch_bytes, int box_rows, int box_cols) {
+    auto fn = encode_tiled();
+    if (!fn) return 1;
+    const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(pitch_bytes)};
+    const cuuint32_t box[2] = {cuuint32_t(box_cols), cuuint32_t(box_rows)};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(m, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS;
+}
+
+struct Plan {
+    int narrow;    // 0, or the MMA's columns
+    int splits;
+    int64_t mpad, ldw, bytes;
+};
+
+Plan plan_of(int64_t M, int64_t N, int64_t K, int sms) {
+    Plan r = {};
+    const int64_t KB = (K + BK - 1) / BK;
+    r.splits = 1;
+    if (M <= 64) {
+        r.narrow = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+        const int64_t tiles = (N + 127) / 128;
+        // CTAs enough for three an SM, each with four blocks of K at least
+        while (r.splits < 8 && tiles * r.splits < 3 * sms && KB >= 8 * r.splits) r.splits *= 2;
+        return r;
+    }
+    const int64_t tiles = ((M + WM - 1) / WM) * ((N + WN - 1) / WN);
+    if (2 * tiles <= sms && KB >= 8) {
+        int64_t s = sms / tiles;
+        if (s > KB / 4) s = KB / 4;
+        if (s > 32) s = 32;
+        r.splits = int(s);
+        r.mpad = (M + WM - 1) / WM * WM;
+        r.ldw = (N + 3) / 4 * 4;
+        r.bytes = r.splits * r.mpad * r.ldw * 4;
+    }
+    return r;
+}
+
+bool sizes_ok(int64_t M, int64_t N, int64_t K) {
+    const int64_t most = (int64_t(1) << 31) - 256;
+    if (M < 0 || N < 0 || K < 1 || M >= most || N >= most || K >= most) return false;
+    return ((M + WM - 1) / WM) * ((N + WN - 1) / WN) <= INT32_MAX;
+}
+
+int sm_count(int* sms) {
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess &&
+           cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
+}
+
+template <int OT>
+int launch_wide(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo, const WideArgs& a, int sms,
+                cudaStream_t s) {
+    const void* fn = reinterpret_cast<const void*>(&wide_kernel<OT>);
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, W_SMEM) != cudaSuccess)
+        return HEADLOSS_ERR_CUDA;
+    const int64_t items = int64_t(a.MT) * a.NT * a.splits;
+    const int grid = int(items < sms ? items : sms);
+    wide_kernel<OT><<<grid, W_THREADS, W_SMEM, s>>>(ma, mb, mo, a);
+    return cudaGetLastError() == cudaSuccess ? HEADLOSS_OK : HEADLOSS_ERR_CUDA;
+}
+
+template <int NT, int OT>
+int launch_narrow(const CUtensorMap& mb, const CUtensorMap& ma, const NarrowArgs& a, cudaStream_t s) {
+    const void* fn = reinterpret_cast<const void*>(&narrow_kernel<NT, OT>);
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Narrow<NT>::SMEM) != cudaSuccess)
+        return HEADLOSS_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned((a.N + 127) / 128 * a.splits));
+    cfg.blockDim = dim3(N_THREADS);
+    cfg.dynamicSmemBytes = Narrow<NT>::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(a.splits);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, narrow_kernel<NT, OT>, mb, ma, a) == cudaSuccess ? HEADLOSS_OK
+                                                                                    : HEADLOSS_ERR_CUDA;
+}
+template <int NT>
+int launch_narrow_as(int ot, const CUtensorMap& mb, const CUtensorMap& ma, const NarrowArgs& a, cudaStream_t s) {
+    return ot == HEADLOSS_FP32   ? launch_narrow<NT, HEADLOSS_FP32>(mb, ma, a, s)
+           : ot == HEADLOSS_BF16 ? launch_narrow<NT, HEADLOSS_BF16>(mb, ma, a, s)
+                                 : launch_narrow<NT, HEADLOSS_FP16>(mb, ma, a, s);
+}
+
+}  // namespace hl_fp8
+
+extern "C" int64_t headloss_fp8_workspace(int64_t M, int64_t N, int64_t K) {
+    using namespace hl_fp8;
+    int sms = 0;
+    if (!sizes_ok(M, N, K) || !sm_count(&sms)) return -1;
+    return M && N ? plan_of(M, N, K, sms).bytes : 0;
+}
+
+extern "C" int headloss_fp8_matmul(const void* a, int64_t lda, const float* a_scales, int a_type,
+                                   const void* b, int64_t ldb, const float* b_scales, int b_type, int64_t M,
+                                   int64_t N, int64_t K, void* out, int64_t ldo, int out_dtype,
+                                   void* workspace, int64_t workspace_bytes, int* err, void* stream) {
+    using namespace hl_fp8;
+    if (!sizes_ok(M, N, K) || lda < K || ldb < K || ldo < N) return HEADLOSS_ERR_ARG;
+    auto known = [](int t) { return t == HEADLOSS_E4M3 || t == HEADLOSS_E5M2; };
+    if (!known(a_type) || !known(b_type)) return HEADLOSS_ERR_ARG;
+    if (out_dtype != HEADLOSS_FP32 && out_dtype != HEADLOSS_BF16 && out_dtype != HEADLOSS_FP16)
+        return HEADLOSS_ERR_DTYPE;
+    if (M == 0 || N == 0) return HEADLOSS_OK;
+    if (!a || !b || !a_scales || !b_scales || !out || !err) return HEADLOSS_ERR_ARG;
+    const int size = out_dtype == HEADLOSS_FP32 ? 4 : 2;
+    auto bits = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
+    if (((bits(a) | bits(b) | bits(workspace)) & 15) || ((lda | ldb) & 15) ||
+        ((bits(a_scales) | bits(b_scales) | bits(err)) & 3) || (bits(out) & (size - 1)))
+        return HEADLOSS_ERR_ALIGN;
+    int sms = 0;
+    if (!sm_count(&sms)) return HEADLOSS_ERR_CUDA;
+    const Plan plan = plan_of(M, N, K, sms);
+    if (plan.bytes > 0 && (!workspace || workspace_bytes < plan.bytes)) return HEADLOSS_ERR_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int KB = int((K + BK - 1) / BK);
+    CUtensorMap ma, mb, mo;
+    const auto U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    if (plan.narrow) {
+        if (make_map(&mb, U8, b, N, K, ldb, 128, BK) || make_map(&ma, U8, a, M, K, lda, plan.narrow, BK))
+            return HEADLOSS_ERR_CUDA;
+        NarrowArgs n = {};
+        n.a_scales = a_scales;
+        n.b_scales = b_scales;
+        n.M = int(M);
+        n.N = N;
+        n.KB = KB;
+        n.splits = plan.splits;
+        n.out = out;
+        n.ldo = ldo;
+        n.idesc = idesc_of(128, plan.narrow, b_type, a_type);
+        n.err = err;
+        return plan.narrow == 16   ? launch_narrow_as<16>(out_dtype, mb, ma, n, s)
+               : plan.narrow == 32 ? launch_narrow_as<32>(out_dtype, mb, ma, n, s)
+                                   : launch_narrow_as<64>(out_dtype, mb, ma, n, s);
+    }
+    WideArgs w = {};
+    w.a_scales = a_scales;
+    w.b_scales = b_scales;
+    w.M = M;
+    w.N = N;
+    w.KB = KB;
+    w.NB = int((N + 127) / 128);
+    w.MT = int((M + WM - 1) / WM);
+    w.NT = int((N + WN - 1) / WN);
+    w.splits = plan.splits;
+    w.mpad = plan.mpad;
+    w.out = out;
+    w.ldo = ldo;
+    w.tma_out = !(bits(out) & 15) && !((ldo * size) & 15);
+    w.n_even = !((N * size) & 15);
+    w.idesc = idesc_of(WM, WN, a_type, b_type);
+    w.err = err;
+    if (make_map(&ma, U8, a, M, K, lda, WM, BK) || make_map(&mb, U8, b, N, K, ldb, WN, BK))
+        return HEADLOSS_ERR_CUDA;
+    if (plan.splits > 1) {
+        w.tma_out = w.n_even = 1;
+        if (make_map(&mo, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, workspace, plan.splits * plan.mpad, plan.ldw, plan.ldw * 4, 32, 32))
+            return HEADLOSS_ERR_CUDA;
+        const int rc = launch_wide<HEADLOSS_FP32>(ma, mb, mo, w, sms, s);
+        if (rc != HEADLOSS_OK) return rc;
+        const int64_t words = M * (plan.ldw / 4);
+        const int grid = int((words + 255) / 256 < 8 * sms ? (words + 255) / 256 : 8 * sms);
+        const float* parts = static_cast<const float*>(workspace);
+        if (out_dtype == HEADLOSS_FP32)
+            join_kernel<HEADLOSS_FP32><<<grid, 256, 0, s>>>(parts, plan.splits, plan.mpad, plan.ldw, M, N, out, ldo);
+        else if (out_dtype == HEADLOSS_BF16)
+            join_kernel<HEADLOSS_BF16><<<grid, 256, 0, s>>>(parts, plan.splits, plan.mpad, plan.ldw, M, N, out, ldo);
+        else
+            join_kernel<HEADLOSS_FP16><<<grid, 256, 0, s>>>(parts, plan.splits, plan.mpad, plan.ldw, M, N, out, ldo);
+        return cudaGetLastError() == cudaSuccess ? HEADLOSS_OK : HEADLOSS_ERR_CUDA;
+    }
+    if (w.tma_out) {
+        const auto type = out_dtype == HEADLOSS_FP32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                          : out_dtype == HEADLOSS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+        if (make_map(&mo, type, out, M, N, ldo * size, 32, 128 / size)) return HEADLOSS_ERR_CUDA;
+    } else {
+        mo = ma;  // not used
+    }
+    return out_dtype == HEADLOSS_FP32   ? launch_wide<HEADLOSS_FP32>(ma, mb, mo, w, sms, s)
+           : out_dtype == HEADLOSS_BF16 ? launch_wide<HEADLOSS_BF16>(ma, mb, mo, w, sms, s)
+                                        : launch_wide<HEADLOSS_FP16>(ma, mb, mo, w, sms, s);
+}

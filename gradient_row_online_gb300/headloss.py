@@ -28,6 +28,9 @@ HEADLOSS_ENTROPY = 1 << 7
 # enum headloss_dtype
 HEADLOSS_FP32, HEADLOSS_BF16, HEADLOSS_FP16 = 0, 1, 2
 
+# enum headloss_fp8
+HEADLOSS_E4M3, HEADLOSS_E5M2 = 0, 1
+
 # enum headloss_status
 STATUS = {0: "HEADLOSS_OK", 1: "HEADLOSS_ERR_ARG", 2: "HEADLOSS_ERR_DTYPE",
           3: "HEADLOSS_ERR_ALIGN", 4: "HEADLOSS_ERR_MISSING_INPUT", 5: "HEADLOSS_ERR_CUDA",
@@ -55,7 +58,8 @@ EXPORTS = ("headloss_create", "headloss_forward_backward", "headloss_get_device_
            "headloss_gspo_seam", "headloss_forward_backward_rowstats",
            "headloss_lmhead_logits", "headloss_lmhead_logits_rowstats",
            "headloss_sample", "headloss_clip_create", "headloss_clip_grads",
-           "headloss_clip_destroy")
+           "headloss_clip_destroy", "headloss_fp8_quantize", "headloss_fp8_workspace",
+           "headloss_fp8_matmul")
 
 
 # enum headloss_kernel
@@ -155,6 +159,14 @@ def load_library(path: str = LIB_PATH):
     lib.headloss_clip_grads.restype = i32
     lib.headloss_clip_destroy.argtypes = [vp]
     lib.headloss_clip_destroy.restype = None
+    lib.headloss_fp8_quantize.argtypes = [vp, i64, i64, i64, i32, i32, vp, i64, vp, i32, vp, i64, vp,
+                                          i32, vp]
+    lib.headloss_fp8_quantize.restype = i32
+    lib.headloss_fp8_workspace.argtypes = [i64, i64, i64]
+    lib.headloss_fp8_workspace.restype = i64
+    lib.headloss_fp8_matmul.argtypes = [vp, i64, vp, i32, vp, i64, vp, i32, i64, i64, i64, vp, i64, i32,
+                                        vp, i64, vp, vp]
+    lib.headloss_fp8_matmul.restype = i32
     _lib = lib
     return lib
 
@@ -338,6 +350,31 @@ def headloss_clip_grads(h, grads, n_grads, max_norm, inv_scale, stats_out, strea
 def headloss_clip_destroy(h) -> None:
     if h:
         load_library().headloss_clip_destroy(h)
+
+
+def headloss_fp8_quantize(x, rows, cols, ld, dtype, type, q, ldq, scales, block, qt, ldqt, scales_t,
+                          block_t, stream=None) -> None:
+    """A matrix and / or its transpose in 8 bits (include/headloss_fp8.h); raises
+    HeadlossError on a bad status."""
+    _check(load_library().headloss_fp8_quantize(
+        _ptr(x), int(rows), int(cols), int(ld), int(dtype), int(type), _ptr(q), int(ldq),
+        _ptr(scales), int(block), _ptr(qt), int(ldqt), _ptr(scales_t), int(block_t),
+        _stream(stream)), "headloss_fp8_quantize")
+
+
+def headloss_fp8_workspace(M, N, K) -> int:
+    return load_library().headloss_fp8_workspace(int(M), int(N), int(K))
+
+
+def headloss_fp8_matmul(a, lda, a_scales, a_type, b, ldb, b_scales, b_type, M, N, K, out, ldo,
+                        out_dtype, workspace, workspace_bytes, err, stream=None) -> None:
+    """out = a . b^T of 8-bit matrices (include/headloss_fp8.h); raises HeadlossError on
+    a bad status."""
+    _check(load_library().headloss_fp8_matmul(
+        _ptr(a), int(lda), _ptr(a_scales), int(a_type), _ptr(b), int(ldb), _ptr(b_scales),
+        int(b_type), int(M), int(N), int(K), _ptr(out), int(ldo), int(out_dtype),
+        _ptr(workspace), int(workspace_bytes), _ptr(err), _stream(stream)),
+        "headloss_fp8_matmul")
 
 
 def headloss_get_device_error(h, stream=None) -> int:
@@ -633,3 +670,206 @@ class GradClipper:
             self.close()
         except Exception:
             pass
+
+
+class Fp8Head:
+    """The LM head's products in 8 bits with an fp32 scale for each block of 128
+    (include/headloss_fp8.h) on torch tensors: `logits`, and with train=True `backward`.
+
+    `weight` (V x D, unit column stride) is quantised once, in 128 x 128 blocks of e4m3;
+    `set_weight` does so again after an optimiser's step, into the same buffers (order it
+    with calls on other streams).  `grads` is the 8-bit type of the loss's gradient, "e4m3"
+    or "e5m2".  A call's own buffers are made on the stream it runs on."""
+
+    _TYPES = {"e4m3": HEADLOSS_E4M3, "e5m2": HEADLOSS_E5M2}
+
+    def __init__(self, weight, train: bool = False, grads: str = "e4m3"):
+        V, D = self._matrix("weight", weight, weight.get_device())
+        self._setup(V, D, weight, train, grads)
+        with _on(self.index, None):
+            self._make()
+        self.set_weight(weight)
+
+    @classmethod
+    def from_quantized(cls, q, scales, train: bool = False, grads: str = "e4m3"):
+        """A checkpoint's weight: `q` V x D float8_e4m3fn or float8_e5m2, `scales` fp32
+        ceil(V / 128) x ceil(D / 128).  The codes are held without a copy where their
+        rows are contiguous and on the 16-byte grid."""
+        import torch
+        types = {torch.float8_e4m3fn: HEADLOSS_E4M3, torch.float8_e5m2: HEADLOSS_E5M2}
+        if q.dim() != 2 or q.dtype not in types or not q.is_cuda or min(q.shape) < 1:
+            raise ValueError("q: a V x D float8 tensor on a GPU is wanted")
+        V, D = q.shape
+        if (scales.dtype is not torch.float32 or scales.get_device() != q.get_device() or
+                tuple(scales.shape) != (-(-V // 128), -(-D // 128))):
+            raise ValueError(f"scales: an fp32 tensor of {-(-V // 128)} x {-(-D // 128)} on {q.device} "
+                             "is wanted")
+        self = cls.__new__(cls)
+        self._setup(V, D, q, train, grads)
+        self.type = types[q.dtype]
+        with _on(self.index, None):
+            codes = q.view(torch.uint8)
+            self.scales = scales.contiguous()
+            if codes.is_contiguous() and D % 16 == 0 and codes.data_ptr() % 16 == 0:
+                self.q, self.ldq = codes, D
+            else:
+                self.q, self.ldq = torch.zeros(V, -(-D // 16) * 16, dtype=torch.uint8, device=q.device), -(-D // 16) * 16
+                self.q[:, :D].copy_(codes)
+            if train:
+                self.qt = torch.zeros(D, -(-V // 16) * 16, dtype=torch.uint8, device=q.device)
+                self.qt[:, :V].copy_(codes.t())
+                self.ldqt, self.scales_t = self.qt.shape[1], self.scales.t().contiguous()
+        return self
+
+    def _setup(self, V, D, like, train, grads):
+        import torch
+        if grads not in self._TYPES:
+            raise ValueError('grads: "e4m3" or "e5m2" is wanted')
+        self._lib = load_library()
+        self.V, self.D, self.train, self.type = V, D, bool(train), HEADLOSS_E4M3
+        self.grads = self._TYPES[grads]
+        self.index, self.device = like.get_device(), like.device
+        self.weight_dtype = torch.bfloat16
+        self._empty, self._u8, self._f32 = torch.empty, torch.uint8, torch.float32
+        self._codes = {torch.float32: HEADLOSS_FP32, torch.bfloat16: HEADLOSS_BF16,
+                       torch.float16: HEADLOSS_FP16}
+        self._needs = {}
+        with _on(self.index, None):
+            self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
+
+    def _make(self):
+        u8, f32, dev = self._u8, self._f32, self.device
+        vb, db = -(-self.V // 128), -(-self.D // 128)
+        self.ldq = -(-self.D // 16) * 16
+        self.q = self._empty(self.V, self.ldq, dtype=u8, device=dev)
+        self.scales = self._empty(vb, db, dtype=f32, device=dev)
+        if self.train:
+            self.ldqt = -(-self.V // 16) * 16
+            self.qt = self._empty(self.D, self.ldqt, dtype=u8, device=dev)
+            self.scales_t = self._empty(db, vb, dtype=f32, device=dev)
+
+    @staticmethod
+    def _matrix(name, a, index):
+        import torch
+        if (a.dim() != 2 or index < 0 or a.get_device() != index or
+                a.dtype not in (torch.float32, torch.bfloat16, torch.float16) or
+                (a.shape[1] > 1 and a.stride(1) != 1) or
+                (a.shape[0] > 1 and a.stride(0) < a.shape[1])):
+            raise ValueError(f"{name}: an fp32, bf16 or fp16 matrix with unit column stride on "
+                             f"cuda:{max(index, 0)} is wanted")
+        if name == "weight" and min(a.shape) < 1:
+            raise ValueError("weight: at least one row and one column are wanted")
+        return a.shape
+
+    def _out(self, name, out, rows, cols, dtype):
+        if out is None:
+            return self._empty(rows, cols, dtype=dtype, device=self.device)
+        self._matrix(name, out, self.index)
+        if tuple(out.shape) != (rows, cols):
+            raise ValueError(f"{name}: {rows} x {cols} is wanted")
+        return out
+
+    def _quantize(self, x, type, q=None, ldq=0, scales=None, block=0, qt=None, ldqt=0, scales_t=None,
+                  block_t=0):
+        rows, cols = x.shape
+        status = self._lib.headloss_fp8_quantize(
+            x.data_ptr(), rows, cols, x.stride(0) if rows > 1 else cols, self._codes[x.dtype], type, q,
+            ldq, scales, block, qt, ldqt, scales_t, block_t, _raw_stream(self.index))
+        if status:
+            _check(status, "headloss_fp8_quantize")
+
+    def _matmul(self, a, lda, a_scales, a_type, b, ldb, b_scales, b_type, M, N, K, out):
+        need = self._needs.get((M, N, K))
+        if need is None:
+            need = self._needs[M, N, K] = self._lib.headloss_fp8_workspace(M, N, K)
+        work = self._empty(need, dtype=self._u8, device=self.device) if need > 0 else None
+        status = self._lib.headloss_fp8_matmul(
+            a, lda, a_scales, a_type, b, ldb, b_scales, b_type, M, N, K, out.data_ptr(),
+            out.stride(0) if M > 1 else N, self._codes[out.dtype],
+            work.data_ptr() if work is not None else None, need, self.err.data_ptr(),
+            _raw_stream(self.index))
+        if status:
+            _check(status, "headloss_fp8_matmul")
+
+    def set_weight(self, weight, stream=None) -> None:
+        if stream is not None or _current_device() != self.index:
+            with _on(self.index, stream):
+                return self.set_weight(weight)
+        self._matrix("weight", weight, self.index)
+        if tuple(weight.shape) != (self.V, self.D):
+            raise ValueError(f"weight: {self.V} x {self.D} is wanted")
+        if self.type != HEADLOSS_E4M3:
+            raise ValueError("set_weight: the head holds a checkpoint's e5m2 codes")
+        t, self.weight_dtype = self.train, weight.dtype
+        self._quantize(weight, HEADLOSS_E4M3, self.q.data_ptr(), self.ldq, self.scales.data_ptr(), 128,
+                       self.qt.data_ptr() if t else None, self.ldqt if t else 0,
+                       self.scales_t.data_ptr() if t else None, 128)
+
+    def logits(self, hidden, out=None, dtype=None, stream=None):
+        """hidden . weight^T (tokens x V) in `dtype` (None: the hidden states'), into `out`
+        if given."""
+        if stream is not None or _current_device() != self.index:
+            with _on(self.index, stream):
+                return self.logits(hidden, out, dtype)
+        N, D = self._matrix("hidden", hidden, self.index)
+        if D != self.D:
+            raise ValueError(f"hidden: {self.D} columns are wanted")
+        dtype = dtype or (hidden.dtype if out is None else out.dtype)
+        if dtype not in self._codes or (out is not None and out.dtype is not dtype):
+            raise ValueError("logits: fp32, bf16 or fp16 and `out` of that type are wanted")
+        out = self._out("out", out, N, self.V, dtype)
+        if N == 0:
+            return out
+        pitch, blocks = -(-D // 16) * 16, -(-D // 128)
+        buf = self._empty(N * (pitch + 4 * blocks), dtype=self._u8, device=self.device)
+        q = buf.data_ptr()
+        scales = q + N * pitch
+        self._quantize(hidden, HEADLOSS_E4M3, q, pitch, scales, 1)
+        self._matmul(q, pitch, scales, HEADLOSS_E4M3, self.q.data_ptr(), self.ldq, self.scales.data_ptr(),
+                     self.type, N, self.V, D, out)
+        return out
+
+    def backward(self, grad, hidden, grad_hidden=None, grad_weight=None, weight_dtype=None, stream=None):
+        """(grad . weight, grad^T . hidden) of the loss's gradient `grad` (tokens x V) and the
+        hidden states: tokens x D in the hidden states' type and V x D in `weight_dtype` (None: that
+        of the weight last given, a checkpoint's: bf16), into the buffers given.  The gradient and the hidden states of the
+        second product are quantised over the tokens."""
+        if stream is not None or _current_device() != self.index:
+            with _on(self.index, stream):
+                return self.backward(grad, hidden, grad_hidden, grad_weight, weight_dtype)
+        if not self.train:
+            raise ValueError("backward: a head made with train=True is wanted")
+        N, V = self._matrix("grad", grad, self.index)
+        if V != self.V or tuple(self._matrix("hidden", hidden, self.index)) != (N, self.D):
+            raise ValueError(f"grad, hidden: N x {self.V} and N x {self.D} are wanted")
+        D = self.D
+        weight_dtype = weight_dtype or (self.weight_dtype if grad_weight is None else grad_weight.dtype)
+        if weight_dtype not in self._codes or (grad_weight is not None and grad_weight.dtype is not weight_dtype):
+            raise ValueError("grad_weight: fp32, bf16 or fp16 and a buffer of that type are wanted")
+        grad_hidden = self._out("grad_hidden", grad_hidden, N, D, hidden.dtype)
+        grad_weight = self._out("grad_weight", grad_weight, V, D, weight_dtype)
+        if N == 0:
+            return grad_hidden, grad_weight.zero_()
+        vp, np_ = -(-V // 16) * 16, -(-N // 16) * 16
+        vb, nb, db = -(-V // 128), -(-N // 128), -(-D // 128)
+        sizes = (N * vp, V * np_, D * np_, 4 * N * vb, 4 * V * nb, 4 * db * nb)
+        buf = self._empty(sum(-(-s // 16) * 16 for s in sizes), dtype=self._u8, device=self.device)
+        at, parts = buf.data_ptr(), []
+        for s in sizes:
+            parts.append(at)
+            at += -(-s // 16) * 16
+        gq, gt, xt, gs, gts, xts = parts
+        self._quantize(grad, self.grads, gq, vp, gs, 1, gt, np_, gts, 1)
+        self._quantize(hidden, HEADLOSS_E4M3, qt=xt, ldqt=np_, scales_t=xts, block_t=128)
+        self._matmul(gq, vp, gs, self.grads, self.qt.data_ptr(), self.ldqt, self.scales_t.data_ptr(), self.type,
+                     N, D, V, grad_hidden)
+        self._matmul(gt, np_, gts, self.grads, xt, np_, xts, HEADLOSS_E4M3, V, D, N, grad_weight)
+        return grad_hidden, grad_weight
+
+    def device_error(self, stream=None) -> int:
+        """Synchronise `stream`, then read and clear the error word (bit 0: a wait inside a
+        product gave up)."""
+        with _on(self.index, stream):
+            e = int(self.err.item())
+            self.err.zero_()
+        return e

@@ -5,7 +5,8 @@ include/headloss.h); `headloss` is its thin ctypes binding and `workloads`
 the seeded synthetic inputs it is measured on.
 """
 from . import headloss, workloads  # noqa: F401
-from .headloss import Fp8Head, GradClipper, HeadLoss, HeadSampler  # noqa: F401
+from .headloss import (  # noqa: F401
+    BeamSelector, Fp8Head, GradClipper, HeadLoss, HeadSampler, StateReorder)
 
 LOSS_BITS = {
     "ce": headloss.HEADLOSS_CE, "z": headloss.HEADLOSS_Z, "dist_ce": headloss.HEADLOSS_DIST_CE,

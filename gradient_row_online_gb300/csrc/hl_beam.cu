@@ -1,0 +1,612 @@
+// hl_beam.cu -- headloss_beam_select (include/headloss_beam.h).
+//
+// slice_kernel: a row's 16-byte words are split into slices of up to 2048, a CTA each, which it holds
+// in registers (eight words a thread, all in flight at once): one read of the logits. The slice's
+// largest logit and a bound for its candidates come from the maxima of groups of threads: the
+// keep-th largest of them has at least `keep` logits at or above it, and hardly more. The sum of
+// exponentials follows in fp32; the few logits at the bound and above go to the workspace.
+// merge_kernel: a CTA a request joins the beams' sums and takes the candidates of all slices in two
+// steps: fp32 scores with a bound of their error leave hardly more than `keep`, which are scored in
+// fp64 and ranked. So the order between beams does not hang on fp32 rounding of the scores.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "headloss.h"
+#include "headloss_beam.h"
+#include "hl_pack.cuh"
+
+namespace hl_beam {
+
+constexpr int ST = 256;               // threads of a slice
+constexpr int WORDS = 8;              // 16-byte words a thread
+constexpr int SLICE_WORDS = ST * WORDS;
+constexpr int MT = 1024;              // threads of a merge
+constexpr int MAX_BEAMS = 64, MAX_KEEP = 128;
+constexpr int LIST = 1024;            // survivors that are ranked at once
+constexpr float NEG = -INFINITY;
+
+struct __align__(16) Head {
+    float top;   // the slice's largest logit
+    float sum;   // of 2^((z - z(top)) K)
+    int n;       // candidates
+    int pad;
+};
+struct Cand {
+    float x;
+    int at;
+};
+
+struct Args {
+    const void* logits;
+    int64_t ld;
+    int V;
+    const float* scores;
+    const uint8_t* ended;
+    int64_t eos;
+    int beams, keep, stay;
+    float cap, inv_cap;
+    float scale, K;       // logits_scale, logits_scale * log2(e)
+    int slices, cap_list; // slices a row, candidates a slice
+    Head* heads;
+    Cand* cands;
+    float* out_scores;
+    int32_t* parents;
+    int64_t* tokens;
+    uint8_t* out_ended;
+};
+
+__device__ __forceinline__ uint32_t key_of(float x) {
+    const uint32_t b = __float_as_uint(x);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ uint64_t key_of(double x) {
+    const uint64_t b = uint64_t(__double_as_longlong(x));
+    return b >> 63 ? ~b : b | (uint64_t(1) << 63);
+}
+
+// z(x) - z(top), top >= x: exact without a cap; with one through tanh of the difference,
+// -c tanh(b - y) (1 - tanh b tanh y), whose error is relative to the difference
+__device__ __forceinline__ float fall(float x, float top, float cap, float inv_cap) {
+    if (x == top) return 0.f;
+    if (cap == 0.f) return x - top;
+    const float y = x * inv_cap, b = top * inv_cap;
+    if (isinf(b)) return cap * (tanhf(y) - tanhf(b));
+    return -cap * tanhf(b - y) * (1.f - tanhf(b) * tanhf(y));
+}
+__device__ __forceinline__ double fall64(float x, float top, float cap) {
+    if (x == top) return 0.0;
+    if (cap == 0.f) return double(x) - double(top);
+    return cap * (tanh(double(x) / cap) - tanh(double(top) / cap));
+}
+
+template <int DT>
+struct Words {
+    static constexpr int SIZE = DT == HEADLOSS_FP32 ? 4 : 2, PER = 16 / SIZE;
+    static constexpr uint32_t NONE = DT == HEADLOSS_FP32 ? 0xff800000u
+                                     : DT == HEADLOSS_BF16 ? 0xff80ff80u : 0xfc00fc00u;
+    // the larger of each pair (or value); a NaN loses
+    static __device__ __forceinline__ uint32_t top2(uint32_t a, uint32_t b) {
+        if (DT == HEADLOSS_FP32) return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+        if (DT == HEADLOSS_BF16) {
+            const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                             *reinterpret_cast<const __nv_bfloat162*>(&b));
+            return *reinterpret_cast<const uint32_t*>(&r);
+        }
+        const __half2 r = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&r);
+    }
+    static __device__ __forceinline__ float2 pair(uint32_t a) {
+        if (DT == HEADLOSS_BF16) return make_float2(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+        return __half22float2(*reinterpret_cast<const __half2*>(&a));
+    }
+    static __device__ __forceinline__ float top_of(uint32_t a) {
+        if (DT == HEADLOSS_FP32) return __uint_as_float(a);
+        const float2 f = pair(a);
+        return fmaxf(f.x, f.y);
+    }
+    // element e of a word held as four registers (e known at compile time)
+    static __device__ __forceinline__ float element(const uint32_t (&w)[4], int e) {
+        if (DT == HEADLOSS_FP32) return __uint_as_float(w[e]);
+        const float2 f = pair(w[e >> 1]);
+        return e & 1 ? f.y : f.x;
+    }
+    static __device__ __forceinline__ float value(const char* row, int64_t e) {
+        if (DT == HEADLOSS_FP32) return reinterpret_cast<const float*>(row)[e];
+        if (DT == HEADLOSS_BF16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[e]);
+        return __half2float(reinterpret_cast<const __half*>(row)[e]);
+    }
+    static __device__ __forceinline__ uint32_t bits(const void* p) {
+        return SIZE == 4 ? *static_cast<const uint32_t*>(p) : *static_cast<const uint16_t*>(p);
+    }
+};
+
+// 2^((z - zt) K) of two logits
+template <bool CAP>
+__device__ __forceinline__ float mass(float x, float ztop, const Args& a) {
+    if (!CAP) return hl::ex2f((x - ztop) * a.K);
+    if (x == NEG) return 0.f;
+    const float y = x * a.inv_cap, w = hl::ex2f(-2.8853900817779268f * fabsf(y));
+    const float z = a.cap * copysignf((1.f - w) * hl::rcpf(1.f + w), y);
+    return hl::ex2f((z - ztop) * a.K);
+}
+
+template <int DT, bool CAP>
+__global__ void __launch_bounds__(ST) slice_kernel(const Args a) {
+    using W = Words<DT>;
+    __shared__ float tops[ST];
+    __shared__ float part[ST / 32];
+    __shared__ int count, found[ST / 32];
+    __shared__ float bound_at;
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t row = blockIdx.x / a.slices;
+    const int slice = int(blockIdx.x - row * a.slices);
+    Head* head = a.heads + row * a.slices + slice;
+    Cand* cands = a.cands + (row * a.slices + slice) * a.cap_list;
+    if (!(a.scores[row] > NEG) || (a.ended && a.ended[row])) return;  // the merge does not look here either
+
+    const char* base = static_cast<const char*>(a.logits) + row * a.ld * W::SIZE;
+    const int off = int(reinterpret_cast<uintptr_t>(base) & 15) / W::SIZE;  // elements of the first word before the row
+    const int words = (off + a.V + W::PER - 1) / W::PER;
+    const int j0 = int(int64_t(words) * slice / a.slices), j1 = int(int64_t(words) * (slice + 1) / a.slices);
+    if (tid == 0) count = 0;
+
+    uint32_t w[WORDS][4], wt[WORDS];
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+        const int j = j0 + i * ST + tid, lo = j * W::PER - off;
+        if (j < j1 && lo >= 0 && lo + W::PER <= a.V) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4*>(base + int64_t(lo) * W::SIZE));
+            w[i][0] = u.x, w[i][1] = u.y, w[i][2] = u.z, w[i][3] = u.w;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                w[i][k] = W::NONE;
+                if (j < j1) {
+                    if (DT == HEADLOSS_FP32) {
+                        const int e = lo + k;
+                        if (e >= 0 && e < a.V) w[i][k] = W::bits(base + int64_t(e) * 4);
+                    } else {
+                        const int e = lo + 2 * k;
+                        if (e >= 0 && e < a.V) w[i][k] = (w[i][k] & 0xffff0000u) | W::bits(base + int64_t(e) * 2);
+                        if (e + 1 >= 0 && e + 1 < a.V)
+                            w[i][k] = (w[i][k] & 0xffffu) | W::bits(base + int64_t(e + 1) * 2) << 16;
+                    }
+                }
+            }
+        }
+    }
+    uint32_t all = W::NONE;
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[i][k] = W::top2(w[i][k], W::NONE);  // NaN to -inf
+        wt[i] = W::top2(W::top2(w[i][0], w[i][1]), W::top2(w[i][2], w[i][3]));
+        all = W::top2(all, wt[i]);
+    }
+    const float mine = W::top_of(all);
+    float top, bound;
+    if (a.keep <= 16) {  // the maxima of 32 groups of eight threads, sorted by every warp
+        float v = mine;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+        if ((lane & 7) == 0) tops[tid >> 3] = v;
+        __syncthreads();
+        v = tops[lane];
+#pragma unroll
+        for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+            for (int o = k >> 1; o; o >>= 1) {
+                const float u = __shfl_xor_sync(0xffffffffu, v, o);
+                const bool larger = ((lane & o) == 0) == ((lane & k) == 0);  // falling where the k bit is clear
+                v = larger ? fmaxf(v, u) : fminf(v, u);
+            }
+        top = __shfl_sync(0xffffffffu, v, 0);
+        bound = __shfl_sync(0xffffffffu, v, a.keep - 1);
+    } else {  // the threads' maxima, ranked
+        tops[tid] = mine;
+        __syncthreads();
+        int rank = 0;
+        top = NEG;
+        for (int k = 0; k < ST; ++k) {
+            const float u = tops[k];
+            top = fmaxf(top, u);
+            rank += u > mine || (u == mine && k < tid);
+        }
+        if (rank == a.keep - 1) bound_at = mine;
+        __syncthreads();
+        bound = bound_at;
+    }
+    if (top == NEG) {  // nothing is allowed here
+        if (tid == 0) *head = Head{NEG, 0.f, 0, 0};
+        return;
+    }
+    // the sum of exponentials
+    float sum = 0.f;
+    const float ztop = CAP ? a.cap * tanhf(top * a.inv_cap) : top;
+    if (!CAP && top == INFINITY) {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i)
+#pragma unroll
+            for (int e = 0; e < W::PER; ++e) sum += W::element(w[i], e) == INFINITY ? 1.f : 0.f;
+    } else {
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i)
+#pragma unroll
+            for (int e = 0; e < W::PER; e += 2) {
+                s0 += mass<CAP>(W::element(w[i], e), ztop, a);
+                s1 += mass<CAP>(W::element(w[i], e + 1), ztop, a);
+            }
+        sum = s0 + s1;
+    }
+    // the candidates; under a cap theirs, which are most of the mass, enter the sum more exactly
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+        const float u = W::top_of(wt[i]);
+        if (u >= bound && u > NEG) {
+#pragma unroll
+            for (int e = 0; e < W::PER; ++e) {
+                const float x = W::element(w[i], e);
+                if (x >= bound && x > NEG) {
+                    const int p = atomicAdd(&count, 1);
+                    if (p < a.cap_list) cands[p] = Cand{x, (j0 + i * ST + tid) * W::PER - off + e};
+                    if (CAP) sum += exp2f(fall(x, top, a.cap, a.inv_cap) * a.K) - mass<CAP>(x, ztop, a);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) part[warp] = sum;
+    __syncthreads();
+    int n = count;
+    if (n > a.cap_list) {
+        // Many equal logits (or hardly any groups with one): the keep-th largest by bisection of the
+        // ordered bits, then the lowest indices of those that equal it.
+        // The slice is read again for it, so that the usual way keeps its registers.
+        const int e0 = max(0, j0 * W::PER - off), e1 = min(a.V, j1 * W::PER - off);
+        auto counted = [&](auto take) {
+            int c = 0;
+#pragma unroll 1
+            for (int e = e0 + tid; e < e1; e += ST) {
+                const float x = W::value(base, e);
+                c += x > NEG && take(key_of(x), e);
+            }
+            c = __reduce_add_sync(0xffffffffu, c);
+            __syncthreads();
+            if (lane == 0) found[warp] = c;
+            __syncthreads();
+            c = 0;
+#pragma unroll
+            for (int k = 0; k < ST / 32; ++k) c += found[k];
+            return c;
+        };
+        uint32_t T = 0;
+        for (int bit = 31; bit >= 0; --bit) {
+            const uint32_t t = T | 1u << bit;
+            if (counted([&](uint32_t k, int) { return k >= t; }) >= a.keep) T = t;
+        }
+        const int need = a.keep - counted([&](uint32_t k, int) { return k > T; });
+        int J = 0;
+        for (int bit = 30; bit >= 0; --bit) {
+            const int t = J | 1 << bit;
+            if (counted([&](uint32_t k, int at) { return k == T && at < t; }) < need) J = t;
+        }
+        if (tid == 0) count = 0;
+        __syncthreads();
+#pragma unroll 1
+        for (int e = e0 + tid; e < e1; e += ST) {
+            const float x = W::value(base, e);
+            const uint32_t k = key_of(x);
+            if (x > NEG && (k > T || (k == T && e <= J))) {
+                const int p = atomicAdd(&count, 1);
+                if (p < a.cap_list) cands[p] = Cand{x, e};
+            }
+        }
+        __syncthreads();
+        n = count;
+    }
+    if (tid == 0) {
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < ST / 32; ++k) s += part[k];
+        *head = Head{top, s, min(n, a.cap_list), 0};
+    }
+}
+
+// ----------------------------------------------------------------- merge ----
+
+struct Best {
+    uint64_t key;   // of the fp64 score
+    int beam;
+    float x;
+    int token;
+};
+// Whether a stands before b.
+__device__ __forceinline__ bool before(const Best& a, const Best& b) {
+    if (a.key != b.key) return a.key > b.key;
+    if (a.beam != b.beam) return a.beam < b.beam;
+    if (a.x != b.x) return a.x > b.x;
+    return a.token < b.token;
+}
+
+constexpr uint64_t NO_KEY = 0;  // below every score that a candidate can have
+
+__global__ void __launch_bounds__(MT) merge_kernel(const Args a) {
+    __shared__ double log_mass[MAX_BEAMS], before_of[MAX_BEAMS];
+    __shared__ float top_of[MAX_BEAMS], log_of[MAX_BEAMS];
+    __shared__ uint8_t kind[MAX_BEAMS];  // 0: no candidates, 1: its row's, 2: ended
+    __shared__ Best list[LIST];
+    __shared__ Best kept[MAX_KEEP];
+    __shared__ int count;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t r = blockIdx.x;
+    const int B = a.beams, S = a.slices;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Head* heads = a.heads + r * B * S;
+    const Cand* cands = a.cands + r * B * S * a.cap_list;
+    if (tid == 0) count = 0;
+    // the beams' sums: a warp a beam
+    for (int b = warp; b < B; b += MT / 32) {
+        const float s = a.scores[r * B + b];
+        const bool over = a.ended && a.ended[r * B + b];
+        const bool live = s > NEG;
+        if (live && !over) {
+            float top = NEG;
+            for (int k = lane; k < S; k += 32) top = fmaxf(top, heads[b * S + k].top);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            double total = 0.0;
+            if (top > NEG)
+                for (int k = lane; k < S; k += 32) {
+                    const Head h = heads[b * S + k];
+                    if (h.top > NEG) total += double(h.sum * exp2f(fall(h.top, top, a.cap, a.inv_cap) * a.K));
+                }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+            if (lane == 0) {
+                kind[b] = top > NEG;
+                top_of[b] = top;
+                log_mass[b] = log(total);
+                log_of[b] = float(log_mass[b]);
+            }
+        } else if (lane == 0) {
+            kind[b] = live ? 2 : 0;
+        }
+        if (lane == 0) before_of[b] = double(s);
+    }
+    __syncthreads();
+
+    // An entry's score in fp64, and in fp32 with a bound of its error.
+    auto exact = [&](int b, const Cand& c) {
+        Best t;
+        t.beam = b;
+        t.x = c.x;
+        t.token = c.at;
+        const double s = before_of[b] + (fall64(c.x, top_of[b], a.cap) * double(a.scale) - log_mass[b]);
+        t.key = s > -INFINITY ? key_of(s) : NO_KEY;
+        return t;
+    };
+    auto ended = [&](int b) {
+        return Best{key_of(before_of[b]), b, 0.f, int(a.eos)};
+    };
+    auto rough = [&](int b, float x, float& off) {
+        const float s = float(before_of[b]), d = fall(x, top_of[b], a.cap, a.inv_cap) * a.scale;
+        // fall() times the scale is within 2^-20 of itself and, where tanh saturates, of the cap's; the
+        // rest rounds three times
+        off = 9.5367432e-7f * (fabsf(s) + fabsf(d) + fabsf(log_of[b]) + a.cap * a.scale + 1.f);
+        return s + (d - log_of[b]);
+    };
+    // f(beam, entry) for every candidate of the rows: a warp a list
+    auto each = [&](auto f) {
+        for (int l = warp; l < B * S; l += MT / 32) {
+            const int b = l / S;
+            if (kind[b] != 1) continue;
+            const int n = heads[l].n;
+            for (int e = lane; e < n; e += 32) f(b, cands[int64_t(l) * a.cap_list + e]);
+        }
+    };
+    // a bound: `keep` threads have a candidate whose score is not below it
+    float mine = NEG;
+    each([&](int b, const Cand& c) {
+        float off;
+        const float s = rough(b, c.x, off);
+        mine = fmaxf(mine, s - off);
+    });
+    if (tid < B && kind[tid] == 2) mine = fmaxf(mine, float(before_of[tid]));
+    const uint32_t my_key = mine > NEG ? key_of(mine) : 0u;
+    uint32_t T = 0;
+    for (int bit = 31; bit >= 8; --bit) {  // from below, to 16 bits of the fraction
+        const uint32_t t = T | 1u << bit;
+        if (__syncthreads_count(my_key >= t) >= a.keep) T = t;
+    }
+    each([&](int b, const Cand& c) {
+        float off;
+        const float s = rough(b, c.x, off);
+        const float high = s + off;
+        if (!(high > NEG) || key_of(high) >= T) {  // (an overflow or NaN is left to fp64)
+            const Best t = exact(b, c);
+            if (t.key != NO_KEY) {
+                const int p = atomicAdd(&count, 1);
+                if (p < LIST) list[p] = t;
+            }
+        }
+    });
+    if (tid < B && kind[tid] == 2) {
+        const int p = atomicAdd(&count, 1);
+        if (p < LIST) list[p] = ended(tid);
+    }
+    __syncthreads();
+    const int n = count;
+    __syncthreads();
+    int m = min(n, a.keep);
+    if (n <= LIST) {
+        if (tid < n) {
+            const Best t = list[tid];
+            int rank = 0;
+            for (int k = 0; k < n; ++k) rank += before(list[k], t);
+            if (rank < m) kept[rank] = t;
+        }
+    } else {
+        // Too many to rank (rows of equal logits): the best one after the last, `keep` times.
+        for (int k = 0; k < a.keep; ++k) {
+            const Best last = k ? kept[k - 1] : Best{~uint64_t(0), -1, INFINITY, -1};
+            Best best = {NO_KEY, MAX_BEAMS, NEG, INT32_MAX};
+            auto offer = [&](const Best& t) {
+                if (t.key != NO_KEY && (k == 0 || before(last, t)) && before(t, best)) best = t;
+            };
+            each([&](int b, const Cand& c) { offer(exact(b, c)); });
+            if (tid < B && kind[tid] == 2) offer(ended(tid));
+            list[tid] = best;
+            __syncthreads();
+            for (int o = MT / 2; o; o >>= 1) {
+                if (tid < o && before(list[tid + o], list[tid])) list[tid] = list[tid + o];
+                __syncthreads();
+            }
+            if (tid == 0) kept[k] = list[0];
+            __syncthreads();
+        }
+    }
+    __syncthreads();
+    // places: in order, or a parent's first child in its place
+    __shared__ int place[MAX_KEEP];
+    if (a.stay) {
+        if (tid == 0) {
+            uint64_t taken = 0;
+            for (int k = 0; k < m; ++k) {
+                const uint64_t bit = uint64_t(1) << kept[k].beam;
+                place[k] = taken & bit ? -1 : kept[k].beam;
+                taken |= bit;
+            }
+            int next = 0;
+            for (int k = 0; k < a.keep; ++k)
+                if (k >= m || place[k] < 0) {
+                    while (taken >> next & 1) ++next;
+                    place[k] = next;
+                    taken |= uint64_t(1) << next;
+                }
+        }
+        __syncthreads();
+    }
+    if (tid < a.keep) {
+        const int64_t at = r * a.keep + (a.stay ? place[tid] : tid);
+        if (tid < m) {
+            const Best t = kept[tid];
+            const uint64_t b = t.key >> 63 ? t.key & ~(uint64_t(1) << 63) : ~t.key;
+            a.out_scores[at] = float(__longlong_as_double(int64_t(b)));
+            a.parents[at] = t.beam;
+            a.tokens[at] = t.token;
+            if (a.out_ended) a.out_ended[at] = a.eos >= 0 && t.token == a.eos;
+        } else {
+            a.out_scores[at] = NEG;
+            a.parents[at] = -1;
+            a.tokens[at] = -1;
+            if (a.out_ended) a.out_ended[at] = 0;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ host ----
+
+struct Plan {
+    int slices, cap_list;
+    int64_t heads, bytes;
+};
+Plan plan_of(int64_t requests, int beams, int64_t V, int dtype, int keep) {
+    Plan p;
+    const int per = dtype == HEADLOSS_FP32 ? 4 : 8;
+    const int64_t words = (V + per - 1 + per - 1) / per;  // of a row that starts anywhere in a word
+    p.slices = int((words + SLICE_WORDS - 1) / SLICE_WORDS);
+    p.cap_list = keep <= 16 ? 64 : 4 * keep;
+    const int64_t n = requests * beams * p.slices;
+    p.heads = n * int64_t(sizeof(Head));
+    p.bytes = p.heads + n * p.cap_list * int64_t(sizeof(Cand));
+    return p;
+}
+bool sizes_ok(int64_t requests, int beams, int64_t V, int keep) {
+    return requests >= 0 && requests <= INT32_MAX && beams >= 1 && beams <= MAX_BEAMS && keep >= 1 &&
+           keep <= MAX_KEEP && V >= 1 && V < (int64_t(1) << 31) - 4096 && requests * beams <= INT32_MAX;
+}
+
+template <int DT>
+void launch(const Args& a, unsigned grid, cudaStream_t s) {
+    if (a.cap > 0.f) slice_kernel<DT, true><<<grid, ST, 0, s>>>(a);
+    else slice_kernel<DT, false><<<grid, ST, 0, s>>>(a);
+}
+
+}  // namespace hl_beam
+
+extern "C" int64_t headloss_beam_workspace(int64_t requests, int beams, int64_t V, int dtype, int keep) {
+    using namespace hl_beam;
+    if (!sizes_ok(requests, beams, V, keep) || dtype < HEADLOSS_FP32 || dtype > HEADLOSS_FP16) return -1;
+    const Plan p = plan_of(requests, beams, V, dtype, keep);
+    return requests * beams * p.slices > INT32_MAX ? -1 : p.bytes;
+}
+
+extern "C" int headloss_beam_select(const void* logits, int64_t requests, int beams, int64_t V, int64_t ld,
+                                    int dtype, const float* scores, const uint8_t* ended, int64_t eos,
+                                    int keep, int stay, float softcap, float logits_scale,
+                                    float* out_scores, int32_t* parents, int64_t* tokens,
+                                    uint8_t* out_ended, void* workspace, int64_t workspace_bytes,
+                                    void* stream) {
+    using namespace hl_beam;
+    if (!sizes_ok(requests, beams, V, keep) || ld < V || eos < -1 || eos >= V || (ended && eos < 0) ||
+        (stay != 0 && stay != 1) || (stay && keep != beams))
+        return HEADLOSS_ERR_ARG;
+    if (!(softcap >= 0.f) || !isfinite(softcap) || !(logits_scale > 0.f) || !isfinite(logits_scale))
+        return HEADLOSS_ERR_ARG;
+    const float inv_cap = softcap > 0.f ? float(1.0 / double(softcap)) : 0.f;
+    const float K = float(double(logits_scale) * 1.4426950408889634);
+    if (!isfinite(inv_cap) || !isfinite(K)) return HEADLOSS_ERR_ARG;
+    if (dtype != HEADLOSS_FP32 && dtype != HEADLOSS_BF16 && dtype != HEADLOSS_FP16) return HEADLOSS_ERR_DTYPE;
+    if (requests == 0) return HEADLOSS_OK;
+    if (!logits || !scores || !out_scores || !parents || !tokens || !workspace) return HEADLOSS_ERR_ARG;
+    auto bits = [](const void* q) { return reinterpret_cast<uintptr_t>(q); };
+    if ((bits(logits) & (dtype == HEADLOSS_FP32 ? 3u : 1u)) || (bits(tokens) & 7u) || (bits(workspace) & 15u) ||
+        ((bits(scores) | bits(out_scores) | bits(parents)) & 3u))
+        return HEADLOSS_ERR_ALIGN;
+    const Plan p = plan_of(requests, beams, V, dtype, keep);
+    const int64_t grid = requests * beams * p.slices;
+    if (grid > INT32_MAX || workspace_bytes < p.bytes) return HEADLOSS_ERR_ARG;
+    Args a = {};
+    a.logits = logits;
+    a.ld = ld;
+    a.V = int(V);
+    a.scores = scores;
+    a.ended = ended;
+    a.eos = eos;
+    a.beams = beams;
+    a.keep = keep;
+    a.stay = stay;
+    a.cap = softcap;
+    a.inv_cap = inv_cap;
+    a.scale = logits_scale;
+    a.K = K;
+    a.slices = p.slices;
+    a.cap_list = p.cap_list;
+    a.heads = static_cast<Head*>(workspace);
+    a.cands = reinterpret_cast<Cand*>(static_cast<char*>(workspace) + p.heads);
+    a.out_scores = out_scores;
+    a.parents = parents;
+    a.tokens = tokens;
+    a.out_ended = out_ended;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (dtype == HEADLOSS_FP32) launch<HEADLOSS_FP32>(a, unsigned(grid), s);
+    else if (dtype == HEADLOSS_BF16) launch<HEADLOSS_BF16>(a, unsigned(grid), s);
+    else launch<HEADLOSS_FP16>(a, unsigned(grid), s);
+    if (cudaGetLastError() != cudaSuccess) return HEADLOSS_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(requests));
+    cfg.blockDim = dim3(MT);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, merge_kernel, a) == cudaSuccess ? HEADLOSS_OK : HEADLOSS_ERR_CUDA;
+}

@@ -59,7 +59,8 @@ EXPORTS = ("headloss_create", "headloss_forward_backward", "headloss_get_device_
            "headloss_lmhead_logits", "headloss_lmhead_logits_rowstats",
            "headloss_sample", "headloss_clip_create", "headloss_clip_grads",
            "headloss_clip_destroy", "headloss_fp8_quantize", "headloss_fp8_workspace",
-           "headloss_fp8_matmul")
+           "headloss_fp8_matmul", "headloss_beam_workspace", "headloss_beam_select",
+           "headloss_reorder_create", "headloss_reorder", "headloss_reorder_destroy")
 
 
 # enum headloss_kernel
@@ -79,6 +80,13 @@ class headloss_gradient(ctypes.Structure):
     """struct headloss_gradient: one tensor of a clipping call."""
     _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64),
                 ("dtype", ctypes.c_int)]
+
+
+class headloss_state(ctypes.Structure):
+    """struct headloss_state: one tensor of beams' states."""
+    _fields_ = [("state", ctypes.c_void_p), ("out", ctypes.c_void_p)] + [
+        (n, ctypes.c_int64) for n in ("outer", "positions", "run_bytes", "row_stride",
+                                      "outer_stride", "position_stride")]
 
 
 class headloss_plan_desc(ctypes.Structure):
@@ -167,6 +175,18 @@ def load_library(path: str = LIB_PATH):
     lib.headloss_fp8_matmul.argtypes = [vp, i64, vp, i32, vp, i64, vp, i32, i64, i64, i64, vp, i64, i32,
                                         vp, i64, vp, vp]
     lib.headloss_fp8_matmul.restype = i32
+    lib.headloss_beam_workspace.argtypes = [i64, i32, i64, i32, i32]
+    lib.headloss_beam_workspace.restype = i64
+    lib.headloss_beam_select.argtypes = [vp, i64, i32, i64, i64, i32, vp, vp, i64, i32, i32, f32, f32,
+                                         vp, vp, vp, vp, vp, i64, vp]
+    lib.headloss_beam_select.restype = i32
+    lib.headloss_reorder_create.argtypes = [ctypes.POINTER(headloss_state), i32, i32,
+                                            ctypes.POINTER(vp)]
+    lib.headloss_reorder_create.restype = i32
+    lib.headloss_reorder.argtypes = [vp, vp, i64, vp, vp, vp]
+    lib.headloss_reorder.restype = i32
+    lib.headloss_reorder_destroy.argtypes = [vp]
+    lib.headloss_reorder_destroy.restype = None
     _lib = lib
     return lib
 
@@ -375,6 +395,43 @@ def headloss_fp8_matmul(a, lda, a_scales, a_type, b, ldb, b_scales, b_type, M, N
         int(b_type), int(M), int(N), int(K), _ptr(out), int(ldo), int(out_dtype),
         _ptr(workspace), int(workspace_bytes), _ptr(err), _stream(stream)),
         "headloss_fp8_matmul")
+
+
+def headloss_beam_workspace(requests, beams, V, dtype, keep) -> int:
+    return load_library().headloss_beam_workspace(int(requests), int(beams), int(V), int(dtype),
+                                                  int(keep))
+
+
+def headloss_beam_select(logits, requests, beams, V, ld, dtype, scores, ended, eos, keep, stay,
+                         softcap, logits_scale, out_scores, parents, tokens, out_ended, workspace,
+                         workspace_bytes, stream=None) -> None:
+    """The best continuations of each request's beams (include/headloss_beam.h); raises
+    HeadlossError on a bad status."""
+    _check(load_library().headloss_beam_select(
+        _ptr(logits), int(requests), int(beams), int(V), int(ld), int(dtype), _ptr(scores),
+        _ptr(ended), int(eos), int(keep), int(stay), float(softcap), float(logits_scale),
+        _ptr(out_scores), _ptr(parents), _ptr(tokens), _ptr(out_ended), _ptr(workspace),
+        int(workspace_bytes), _stream(stream)), "headloss_beam_select")
+
+
+def headloss_reorder_create(states, n: int, beams: int) -> int:
+    """A handle for `n` states (an array of headloss_state) of beams."""
+    h = ctypes.c_void_p()
+    _check(load_library().headloss_reorder_create(states, int(n), int(beams), ctypes.byref(h)),
+           "headloss_reorder_create")
+    return h.value
+
+
+def headloss_reorder(h, parents, requests, begin=None, end=None, stream=None) -> None:
+    """The beams take their parents' states (include/headloss_beam.h); raises HeadlossError
+    on a bad status."""
+    _check(load_library().headloss_reorder(h, _ptr(parents), int(requests), _ptr(begin), _ptr(end),
+                                           _stream(stream)), "headloss_reorder")
+
+
+def headloss_reorder_destroy(h) -> None:
+    if h:
+        load_library().headloss_reorder_destroy(h)
 
 
 def headloss_get_device_error(h, stream=None) -> int:
@@ -873,3 +930,178 @@ class Fp8Head:
             e = int(self.err.item())
             self.err.zero_()
         return e
+
+
+class BeamSelector:
+    """headloss_beam_select on torch tensors: the `keep` (None: `beams`) best continuations of
+    each request's `beams` rows of logits.
+
+    Called with logits ((requests * beams) x V, unit column stride, any row stride), the
+    beams' scores (requests x beams fp32) and, where hypotheses can end, a bool tensor of
+    those that have (requests x beams).  Returns (scores fp32, parents int32, tokens int64,
+    ended bool), requests x keep each; `out` gives the four buffers.  `eos` is the token that
+    ends a hypothesis (None: none does).  `stay` (keep == beams alone) leaves a beam that goes
+    on in its place, so that states that are reordered in place move least."""
+
+    def __init__(self, beams: int, keep=None, softcap: float = 0.0, logits_scale: float = 1.0, eos=None,
+                 stay: bool = False, device="cuda"):
+        import torch
+        self.beams, self.keep = int(beams), int(beams if keep is None else keep)
+        self.softcap, self.logits_scale = float(softcap), float(logits_scale)
+        self.eos, self.stay = -1 if eos is None else int(eos), int(bool(stay))
+        if not 1 <= self.beams <= 64 or not 1 <= self.keep <= 128 or (self.stay and self.keep != self.beams):
+            raise ValueError("beams in 1 .. 64 and keep in 1 .. 128 are wanted, and keep == beams with stay")
+        device = torch.device(device)
+        self.index = device.index if device.index is not None else torch.cuda.current_device()
+        self.device = torch.device("cuda", self.index)
+        lib = load_library()
+        self._call, self._need = lib.headloss_beam_select, lib.headloss_beam_workspace
+        self._empty, self._u8, self._bool = torch.empty, torch.uint8, torch.bool
+        self._f32, self._i32, self._i64 = torch.float32, torch.int32, torch.int64
+        self._codes = {torch.float32: HEADLOSS_FP32, torch.bfloat16: HEADLOSS_BF16,
+                       torch.float16: HEADLOSS_FP16}
+
+    def _given(self, name, a, dtype, shape):
+        if (a.dtype is not dtype or tuple(a.shape) != shape or a.get_device() != self.index or
+                not a.is_contiguous()):
+            raise ValueError(f"{name}: a contiguous {dtype} tensor of {shape[0]} x {shape[1]} on "
+                             f"{self.device} is wanted")
+        return a.data_ptr()
+
+    def __call__(self, logits, scores, ended=None, out=None, stream=None):
+        if stream is not None or _current_device() != self.index:
+            with _on(self.index, stream):
+                return self(logits, scores, ended, out)
+        if (logits.dim() != 2 or logits.get_device() != self.index or logits.shape[1] < 1 or
+                logits.shape[0] % self.beams or (logits.shape[1] > 1 and logits.stride(1) != 1)):
+            raise ValueError(f"logits: a (requests * {self.beams}) x V tensor with unit column stride on "
+                             f"{self.device} is wanted")
+        N, V = logits.shape
+        code = self._codes.get(logits.dtype)
+        if code is None:
+            raise HeadlossError(HEADLOSS_ERR_DTYPE, "headloss_beam_select")
+        R, k = N // self.beams, self.keep
+        s = self._given("scores", scores, self._f32, (R, self.beams))
+        e = None if ended is None else self._given("ended", ended, self._bool, (R, self.beams))
+        if e is not None and self.eos < 0:
+            raise ValueError("ended: a selector made with eos is wanted")
+        empty, device = self._empty, self.device
+        if out is None:
+            out = (empty(R, k, dtype=self._f32, device=device), empty(R, k, dtype=self._i32, device=device),
+                   empty(R, k, dtype=self._i64, device=device), empty(R, k, dtype=self._bool, device=device))
+        else:
+            for name, a, d in zip(("scores", "parents", "tokens", "ended"), out,
+                                  (self._f32, self._i32, self._i64, self._bool)):
+                self._given("out's " + name, a, d, (R, k))
+        need = self._need(R, self.beams, V, code, k)
+        work = empty(max(need, 0), dtype=self._u8, device=device)
+        status = self._call(logits.data_ptr(), R, self.beams, V, logits.stride(0) if N > 1 else V, code, s, e,
+                            self.eos, k, self.stay, self.softcap, self.logits_scale, out[0].data_ptr(),
+                            out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(), work.data_ptr(), need,
+                            _raw_stream(self.index))
+        if status:
+            _check(status, "headloss_beam_select")
+        return out
+
+
+class StateReorder:
+    """headloss_reorder on torch tensors: the beams take their parents' states, in place or into
+    `outs` (buffers of the same layout).  The tensors are held.
+
+    `states` are tensors of requests * beams rows (or more: those behind stay as they are).  With
+    `axis` the dimension of the positions (a cache's): a call's `begin` and `end` (int32, one a
+    request) then name the positions to take, say those behind a prompt that the beams share.
+    Called with parents (requests x beams int32, as the selection gives them); returns the
+    reordered tensors."""
+
+    def __init__(self, states, beams: int, outs=None, axis=None):
+        import torch
+        self.h = None
+        states = list(states)
+        outs = states if outs is None else list(outs)
+        if not states or len(outs) != len(states) or not 1 <= int(beams) <= 64:
+            raise ValueError("at least one state, as many outs, and beams in 1 .. 64 are wanted")
+        self.beams, self.axis = int(beams), axis
+        self.index = states[0].get_device()
+        table = (headloss_state * len(states))()
+        self.rows = min(t.shape[0] if t.dim() else 0 for t in states)
+        for t, o, entry in zip(states, outs, table):
+            if (not t.is_cuda or t.get_device() != self.index or t.dim() < 1 or o.get_device() != self.index or
+                    o is not t and (o.dtype is not t.dtype or o.shape != t.shape or o.stride() != t.stride())):
+                raise ValueError(f"states: tensors on cuda:{max(self.index, 0)}, and outs of their types, "
+                                 "shapes and strides, are wanted")
+            entry.state, entry.out = t.data_ptr(), o.data_ptr()
+            self._layout(t, entry)
+        self.states, self.outs = states, outs
+        self.device = torch.device("cuda", self.index)
+        self._i32 = torch.int32
+        self._call = load_library().headloss_reorder
+        live = [e for e, t in zip(table, states) if t.numel()]
+        if live:
+            with _on(self.index, None):
+                self.h = headloss_reorder_create((headloss_state * len(live))(*live), len(live), self.beams)
+
+    def _layout(self, t, entry):
+        """Rows, outer dimensions that go as one, positions, and a run of contiguous elements."""
+        size, axis = t.element_size(), self.axis
+        if any(n > 1 and s <= 0 for n, s in zip(t.shape, t.stride())):
+            raise ValueError("states: expanded dimensions are refused")
+
+        def joined(dims):
+            """The number and the stride of the elements of `dims`, where they go as one."""
+            n, stride = 1, 0
+            for d in reversed(dims):
+                if t.shape[d] == 1:
+                    continue
+                if stride and t.stride(d) != n * stride:
+                    raise ValueError("states: dimensions before the positions that go as one, and contiguous "
+                                     "ones behind them, are wanted")
+                stride = stride or t.stride(d)
+                n *= t.shape[d]
+            return n, stride
+        if axis is not None and not 1 <= axis < t.dim():
+            raise ValueError("axis: a dimension behind the rows is wanted")
+        behind = range(1 if axis is None else axis + 1, t.dim())
+        run, stride = joined(list(behind))
+        if run > 1 and stride != 1:
+            raise ValueError("states: contiguous elements behind the positions are wanted")
+        entry.row_stride = t.stride(0) * size
+        entry.run_bytes = run * size
+        entry.outer, outer_stride = joined(list(range(1, axis))) if axis is not None else (1, 0)
+        entry.outer_stride = outer_stride * size
+        entry.positions = t.shape[axis] if axis is not None else 1
+        entry.position_stride = t.stride(axis) * size if axis is not None else run * size
+
+    def __call__(self, parents, begin=None, end=None, stream=None):
+        if stream is not None or _current_device() != self.index:
+            with _on(self.index, stream):
+                return self(parents, begin, end)
+        if (parents.dim() != 2 or parents.shape[1] != self.beams or parents.dtype is not self._i32 or
+                parents.get_device() != self.index or not parents.is_contiguous() or
+                parents.numel() > self.rows):
+            raise ValueError(f"parents: a contiguous int32 tensor of requests x {self.beams} on {self.device}, "
+                             f"for {self.rows} rows at most, is wanted")
+        R = parents.shape[0]
+        if (begin is None) != (end is None) or (begin is not None and self.axis is None):
+            raise ValueError("begin and end: both or none, and none for states without positions")
+        for name, a in (("begin", begin), ("end", end)):
+            if a is not None and (a.dtype is not self._i32 or a.dim() != 1 or a.numel() != R or
+                                  a.get_device() != self.index or not a.is_contiguous()):
+                raise ValueError(f"{name}: a contiguous int32 tensor of {R} on {self.device} is wanted")
+        if self.h:
+            status = self._call(self.h, parents.data_ptr(), R, begin.data_ptr() if begin is not None else None,
+                                end.data_ptr() if end is not None else None, _raw_stream(self.index))
+            if status:
+                _check(status, "headloss_reorder")
+        return self.outs
+
+    def close(self):
+        if self.h:
+            headloss_reorder_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass

@@ -17,15 +17,16 @@
 #include "headloss.h"
 #include "headloss_beam.h"
 #include "hl_pack.cuh"
+#include "hl_tanh_poly.h"
 
 namespace hl_beam {
 
 constexpr int ST = 256;               // threads of a slice
 constexpr int WORDS = 8;              // 16-byte words a thread
 constexpr int SLICE_WORDS = ST * WORDS;
-constexpr int MT = 1024;              // threads of a merge
+constexpr int MT = 512;               // threads of a merge
 constexpr int MAX_BEAMS = 64, MAX_KEEP = 128;
-constexpr int LIST = 1024;            // survivors that are ranked at once
+constexpr int LIST = MT;              // survivors that are ranked at once
 constexpr float NEG = -INFINITY;
 
 struct __align__(16) Head {
@@ -49,6 +50,8 @@ struct Args {
     int beams, keep, stay;
     float cap, inv_cap;
     float scale, K;       // logits_scale, logits_scale * log2(e)
+    float cap_K, near;    // cap * K; the magnitudes that `poly` covers
+    float poly[6];        // z K = x poly(x^2)
     int slices, cap_list; // slices a row, candidates a slice
     Head* heads;
     Cand* cands;
@@ -76,12 +79,6 @@ __device__ __forceinline__ float fall(float x, float top, float cap, float inv_c
     if (isinf(b)) return cap * (tanhf(y) - tanhf(b));
     return -cap * tanhf(b - y) * (1.f - tanhf(b) * tanhf(y));
 }
-__device__ __forceinline__ double fall64(float x, float top, float cap) {
-    if (x == top) return 0.0;
-    if (cap == 0.f) return double(x) - double(top);
-    return cap * (tanh(double(x) / cap) - tanh(double(top) / cap));
-}
-
 template <int DT>
 struct Words {
     static constexpr int SIZE = DT == HEADLOSS_FP32 ? 4 : 2, PER = 16 / SIZE;
@@ -118,41 +115,79 @@ struct Words {
         if (DT == HEADLOSS_BF16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[e]);
         return __half2float(reinterpret_cast<const __half*>(row)[e]);
     }
-    static __device__ __forceinline__ uint32_t bits(const void* p) {
-        return SIZE == 4 ? *static_cast<const uint32_t*>(p) : *static_cast<const uint16_t*>(p);
+    // a word that is not the row's alone: elements lo .. of it, -inf outside
+    static __device__ __forceinline__ void edge(const char* row, int lo, int V, uint32_t (&w)[4]) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (DT == HEADLOSS_FP32) {
+                const int e = lo + k;
+                if (e >= 0 && e < V) w[k] = reinterpret_cast<const uint32_t*>(row)[e];
+            } else {
+                const int e = lo + 2 * k;
+                const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
+                if (e >= 0 && e < V) w[k] = (w[k] & 0xffff0000u) | p[e];
+                if (e + 1 >= 0 && e + 1 < V) w[k] = (w[k] & 0xffffu) | uint32_t(p[e + 1]) << 16;
+            }
+        }
+    }
+    // whether every magnitude of a word is at most `most` (of two 16-bit values: packed); not with a NaN
+    // that has the sign of its neighbours' maximum alone: such sums end as NaN and are taken again
+    static __device__ __forceinline__ bool within(const uint32_t (&w)[4], float most) {
+        if (DT == HEADLOSS_FP32)
+            return fmaxf(fmaxf(fabsf(__uint_as_float(w[0])), fabsf(__uint_as_float(w[1]))),
+                         fmaxf(fabsf(__uint_as_float(w[2])), fabsf(__uint_as_float(w[3])))) <= most;
+        uint32_t m;
+        if (DT == HEADLOSS_BF16) {
+            using P = hl::Pack16<__nv_bfloat16>;
+            m = P::absmax2(P::absmax2(w[0], w[1]), P::absmax2(w[2], w[3]));
+        } else {
+            using P = hl::Pack16<__half>;
+            m = P::absmax2(P::absmax2(w[0], w[1]), P::absmax2(w[2], w[3]));
+        }
+        const float2 f = pair(m);
+        return fmaxf(fabsf(f.x), fabsf(f.y)) <= most;
     }
 };
 
-// 2^((z - zt) K) of two logits
-template <bool CAP>
-__device__ __forceinline__ float mass(float x, float ztop, const Args& a) {
-    if (!CAP) return hl::ex2f((x - ztop) * a.K);
+// 2^(z K - zt) of a capped logit, tanh through two MUFU operations: any x.
+__device__ __forceinline__ float mass_any(float x, float zt, const Args& a) {
     if (x == NEG) return 0.f;
     const float y = x * a.inv_cap, w = hl::ex2f(-2.8853900817779268f * fabsf(y));
-    const float z = a.cap * copysignf((1.f - w) * hl::rcpf(1.f + w), y);
-    return hl::ex2f((z - ztop) * a.K);
+    return hl::ex2f(fmaf(a.cap_K, copysignf((1.f - w) * hl::rcpf(1.f + w), y), -zt));
+}
+// The same of two logits within HL_TANH_B_Y0 caps: z K = x Q(x^2), the cap and K in the coefficients.
+__device__ __forceinline__ hl::f2 mass_near(hl::f2 x, hl::f2 minus_zt, const Args& a) {
+    const hl::f2 t = hl::mul2(x, x);
+    hl::f2 q = hl::pk1(a.poly[5]);
+#pragma unroll
+    for (int i = 4; i >= 0; --i) q = hl::fma2(q, t, hl::pk1(a.poly[i]));
+    return hl::ex2p(hl::fma2(x, q, minus_zt));
 }
 
+constexpr int HITS = 256;  // words with a candidate that a slice lists
+
 template <int DT, bool CAP>
-__global__ void __launch_bounds__(ST) slice_kernel(const Args a) {
+__global__ void __launch_bounds__(ST, 4) slice_kernel(const __grid_constant__ Args a) {
     using W = Words<DT>;
+    __shared__ __align__(16) uint4 hit[HITS];
+    __shared__ int hit_at[HITS];  // the word's place, and whether its sum went through mass_any
     __shared__ float tops[ST];
     __shared__ float part[ST / 32];
-    __shared__ int count, found[ST / 32];
+    __shared__ int hits, count, found[ST / 32];
     __shared__ float bound_at;
     asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t row = blockIdx.x / a.slices;
-    const int slice = int(blockIdx.x - row * a.slices);
-    Head* head = a.heads + row * a.slices + slice;
-    Cand* cands = a.cands + (row * a.slices + slice) * a.cap_list;
+    const int row = int(blockIdx.x / unsigned(a.slices));
+    const int slice = int(blockIdx.x) - row * a.slices;
+    Head* head = a.heads + blockIdx.x;
+    Cand* cands = a.cands + int64_t(blockIdx.x) * a.cap_list;
     if (!(a.scores[row] > NEG) || (a.ended && a.ended[row])) return;  // the merge does not look here either
 
     const char* base = static_cast<const char*>(a.logits) + row * a.ld * W::SIZE;
     const int off = int(reinterpret_cast<uintptr_t>(base) & 15) / W::SIZE;  // elements of the first word before the row
     const int words = (off + a.V + W::PER - 1) / W::PER;
     const int j0 = int(int64_t(words) * slice / a.slices), j1 = int(int64_t(words) * (slice + 1) / a.slices);
-    if (tid == 0) count = 0;
+    if (tid == 0) hits = count = 0;
 
     uint32_t w[WORDS][4], wt[WORDS];
 #pragma unroll
@@ -163,28 +198,14 @@ __global__ void __launch_bounds__(ST) slice_kernel(const Args a) {
             w[i][0] = u.x, w[i][1] = u.y, w[i][2] = u.z, w[i][3] = u.w;
         } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                w[i][k] = W::NONE;
-                if (j < j1) {
-                    if (DT == HEADLOSS_FP32) {
-                        const int e = lo + k;
-                        if (e >= 0 && e < a.V) w[i][k] = W::bits(base + int64_t(e) * 4);
-                    } else {
-                        const int e = lo + 2 * k;
-                        if (e >= 0 && e < a.V) w[i][k] = (w[i][k] & 0xffff0000u) | W::bits(base + int64_t(e) * 2);
-                        if (e + 1 >= 0 && e + 1 < a.V)
-                            w[i][k] = (w[i][k] & 0xffffu) | W::bits(base + int64_t(e + 1) * 2) << 16;
-                    }
-                }
-            }
+            for (int k = 0; k < 4; ++k) w[i][k] = W::NONE;
+            if (j < j1) W::edge(base, lo, a.V, w[i]);
         }
     }
     uint32_t all = W::NONE;
 #pragma unroll
-    for (int i = 0; i < WORDS; ++i) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) w[i][k] = W::top2(w[i][k], W::NONE);  // NaN to -inf
-        wt[i] = W::top2(W::top2(w[i][0], w[i][1]), W::top2(w[i][2], w[i][3]));
+    for (int i = 0; i < WORDS; ++i) {  // (a NaN loses every comparison)
+        wt[i] = W::top2(W::top2(w[i][0], w[i][1]), W::top2(W::top2(w[i][2], w[i][3]), W::NONE));
         all = W::top2(all, wt[i]);
     }
     const float mine = W::top_of(all);
@@ -224,37 +245,57 @@ __global__ void __launch_bounds__(ST) slice_kernel(const Args a) {
         if (tid == 0) *head = Head{NEG, 0.f, 0, 0};
         return;
     }
-    // the sum of exponentials
-    float sum = 0.f;
-    const float ztop = CAP ? a.cap * tanhf(top * a.inv_cap) : top;
-    if (!CAP && top == INFINITY) {
+    // The words with a candidate go to shared memory, so that the code for them exists once.
+    uint32_t through_any = 0;  // of this thread's words
+    float sum;
+    hl::f2 s2 = 0ull;
+    // what is taken off the exponents: of the largest logit, rounded
+    const float zt = CAP ? a.cap_K * tanhf(top * a.inv_cap) : top * a.K;
+    const hl::f2 minus_zt = hl::pk1(-zt), K2 = hl::pk1(a.K);
 #pragma unroll
-        for (int i = 0; i < WORDS; ++i)
+    for (int i = 0; i < WORDS; ++i) {
+        bool near = true;
+        if (CAP) near = __all_sync(0xffffffffu, W::within(w[i], a.near));
+        if (CAP && !near) {
+            float s = 0.f;
 #pragma unroll
-            for (int e = 0; e < W::PER; ++e) sum += W::element(w[i], e) == INFINITY ? 1.f : 0.f;
-    } else {
-        float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-        for (int i = 0; i < WORDS; ++i)
+            for (int e = 0; e < W::PER; ++e) s += mass_any(W::element(w[i], e), zt, a);
+            s2 = hl::add2(s2, hl::pk(s, 0.f));
+            through_any |= 1u << i;
+        } else {
 #pragma unroll
             for (int e = 0; e < W::PER; e += 2) {
-                s0 += mass<CAP>(W::element(w[i], e), ztop, a);
-                s1 += mass<CAP>(W::element(w[i], e + 1), ztop, a);
+                const hl::f2 x = hl::pk(W::element(w[i], e), W::element(w[i], e + 1));
+                s2 = hl::add2(s2, CAP ? mass_near(x, minus_zt, a) : hl::ex2p(hl::fma2(x, K2, minus_zt)));
             }
-        sum = s0 + s1;
+        }
     }
-    // the candidates; under a cap theirs, which are most of the mass, enter the sum more exactly
 #pragma unroll
     for (int i = 0; i < WORDS; ++i) {
         const float u = W::top_of(wt[i]);
         if (u >= bound && u > NEG) {
-#pragma unroll
-            for (int e = 0; e < W::PER; ++e) {
-                const float x = W::element(w[i], e);
-                if (x >= bound && x > NEG) {
-                    const int p = atomicAdd(&count, 1);
-                    if (p < a.cap_list) cands[p] = Cand{x, (j0 + i * ST + tid) * W::PER - off + e};
-                    if (CAP) sum += exp2f(fall(x, top, a.cap, a.inv_cap) * a.K) - mass<CAP>(x, ztop, a);
+            const int p = atomicAdd(&hits, 1);
+            if (p < HITS) {
+                hit[p] = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+                hit_at[p] = (j0 + i * ST + tid) * 2 | int(through_any >> i & 1u);
+            }
+        }
+    }
+    sum = hl::hsum(s2);
+    __syncthreads();
+    const bool crowded = hits > HITS;
+    if (!crowded) {
+        for (int k = tid; k < hits * W::PER; k += ST) {
+            const int h = k / W::PER, e = k % W::PER;
+            const float x = W::value(reinterpret_cast<const char*>(&hit[h]), e);
+            if (x >= bound && x > NEG) {
+                const int p = atomicAdd(&count, 1);
+                if (p < a.cap_list) cands[p] = Cand{x, (hit_at[h] >> 1) * W::PER - off + e};
+                if (CAP) {
+                    // the candidates have most of the mass: theirs enters more exactly, relative to the
+                    // largest logit's own z
+                    const float had = hit_at[h] & 1 ? mass_any(x, zt, a) : hl::lo_of(mass_near(hl::pk1(x), minus_zt, a));
+                    sum += exp2f(fall(x, top, a.cap, a.inv_cap) * a.K) - had;
                 }
             }
         }
@@ -263,12 +304,33 @@ __global__ void __launch_bounds__(ST) slice_kernel(const Args a) {
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) part[warp] = sum;
     __syncthreads();
+    sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < ST / 32; ++k) sum += part[k];
+    // 2^(top K - zt) is taken off again: zt was rounded
+    if (!CAP) sum *= hl::ex2f(-fmaf(top, a.K, -zt));
     int n = count;
-    if (n > a.cap_list) {
+    const int e0 = max(0, j0 * W::PER - off), e1 = min(a.V, j1 * W::PER - off);
+    if (!(sum > 0.5f && sum < INFINITY)) {  // a NaN, an infinity, zt beyond fp32: from memory, one by one
+        float s = 0.f;
+#pragma unroll 1
+        for (int e = e0 + tid; e < e1; e += ST) {
+            const float x = W::value(base, e);
+            if (x > NEG) s += exp2f(fall(x, top, a.cap, a.inv_cap) * a.K);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        __syncthreads();
+        if (lane == 0) part[warp] = s;
+        __syncthreads();
+        sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < ST / 32; ++k) sum += part[k];
+    }
+    if (crowded || n > a.cap_list) {
         // Many equal logits (or hardly any groups with one): the keep-th largest by bisection of the
         // ordered bits, then the lowest indices of those that equal it.
         // The slice is read again for it, so that the usual way keeps its registers.
-        const int e0 = max(0, j0 * W::PER - off), e1 = min(a.V, j1 * W::PER - off);
         auto counted = [&](auto take) {
             int c = 0;
 #pragma unroll 1
@@ -286,12 +348,14 @@ __global__ void __launch_bounds__(ST) slice_kernel(const Args a) {
             return c;
         };
         uint32_t T = 0;
+#pragma unroll 1
         for (int bit = 31; bit >= 0; --bit) {
             const uint32_t t = T | 1u << bit;
             if (counted([&](uint32_t k, int) { return k >= t; }) >= a.keep) T = t;
         }
         const int need = a.keep - counted([&](uint32_t k, int) { return k > T; });
         int J = 0;
+#pragma unroll 1
         for (int bit = 30; bit >= 0; --bit) {
             const int t = J | 1 << bit;
             if (counted([&](uint32_t k, int at) { return k == T && at < t; }) < need) J = t;
@@ -310,12 +374,7 @@ __global__ void __launch_bounds__(ST) slice_kernel(const Args a) {
         __syncthreads();
         n = count;
     }
-    if (tid == 0) {
-        float s = 0.f;
-#pragma unroll
-        for (int k = 0; k < ST / 32; ++k) s += part[k];
-        *head = Head{top, s, min(n, a.cap_list), 0};
-    }
+    if (tid == 0) *head = Head{top, sum, min(n, a.cap_list), 0};
 }
 
 // ----------------------------------------------------------------- merge ----
@@ -334,12 +393,20 @@ __device__ __forceinline__ bool before(const Best& a, const Best& b) {
     return a.token < b.token;
 }
 
+constexpr int LISTS = 256, HELD = 1920;  // lists and candidates that are held in shared memory
 constexpr uint64_t NO_KEY = 0;  // below every score that a candidate can have
 
 __global__ void __launch_bounds__(MT) merge_kernel(const Args a) {
     __shared__ double log_mass[MAX_BEAMS], before_of[MAX_BEAMS];
     __shared__ float top_of[MAX_BEAMS], log_of[MAX_BEAMS];
+    __shared__ double tanh_top[MAX_BEAMS];
     __shared__ uint8_t kind[MAX_BEAMS];  // 0: no candidates, 1: its row's, 2: ended
+    __shared__ int size_of[LISTS], begin_of[LISTS + 1];
+    __shared__ float high_of[HELD];
+    __shared__ Cand cand_of[HELD];
+    __shared__ uint8_t beam_of[HELD];
+    __shared__ uint16_t alive[LIST];
+    __shared__ int survivors;
     __shared__ Best list[LIST];
     __shared__ Best kept[MAX_KEEP];
     __shared__ int count;
@@ -349,7 +416,7 @@ __global__ void __launch_bounds__(MT) merge_kernel(const Args a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Head* heads = a.heads + r * B * S;
     const Cand* cands = a.cands + r * B * S * a.cap_list;
-    if (tid == 0) count = 0;
+    if (tid == 0) count = survivors = 0;
     // the beams' sums: a warp a beam
     for (int b = warp; b < B; b += MT / 32) {
         const float s = a.scores[r * B + b];
@@ -373,6 +440,7 @@ __global__ void __launch_bounds__(MT) merge_kernel(const Args a) {
                 top_of[b] = top;
                 log_mass[b] = log(total);
                 log_of[b] = float(log_mass[b]);
+                if (a.cap > 0.f) tanh_top[b] = tanh(double(top) / a.cap);
             }
         } else if (lane == 0) {
             kind[b] = live ? 2 : 0;
@@ -387,19 +455,28 @@ __global__ void __launch_bounds__(MT) merge_kernel(const Args a) {
         t.beam = b;
         t.x = c.x;
         t.token = c.at;
-        const double s = before_of[b] + (fall64(c.x, top_of[b], a.cap) * double(a.scale) - log_mass[b]);
+        double d;
+        if (c.x == top_of[b]) d = 0.0;
+        else if (a.cap == 0.f) d = double(c.x) - double(top_of[b]);
+        else d = double(a.cap) * (tanh(double(c.x) / a.cap) - tanh_top[b]);
+        const double s = before_of[b] + (d * double(a.scale) - log_mass[b]);
         t.key = s > -INFINITY ? key_of(s) : NO_KEY;
         return t;
     };
     auto ended = [&](int b) {
         return Best{key_of(before_of[b]), b, 0.f, int(a.eos)};
     };
+    // tanh by two MUFU operations is within 2^-21, so the score within 2^-20 of its parts
     auto rough = [&](int b, float x, float& off) {
-        const float s = float(before_of[b]), d = fall(x, top_of[b], a.cap, a.inv_cap) * a.scale;
-        // fall() times the scale is within 2^-20 of itself and, where tanh saturates, of the cap's; the
-        // rest rounds three times
-        off = 9.5367432e-7f * (fabsf(s) + fabsf(d) + fabsf(log_of[b]) + a.cap * a.scale + 1.f);
-        return s + (d - log_of[b]);
+        const float s = float(before_of[b]), l = log_of[b];
+        float d = x - top_of[b];
+        if (a.cap > 0.f) {
+            const float y = x * a.inv_cap, w = hl::ex2f(-2.8853900817779268f * fabsf(y));
+            d = a.cap * (copysignf((1.f - w) * hl::rcpf(1.f + w), y) - float(tanh_top[b]));
+        }
+        d = x == top_of[b] ? 0.f : d * a.scale;
+        off = 9.5367432e-7f * (fabsf(s) + fabsf(d) + fabsf(l) + a.cap * a.scale + 1.f);
+        return s + (d - l);
     };
     // f(beam, entry) for every candidate of the rows: a warp a list
     auto each = [&](auto f) {
@@ -410,13 +487,55 @@ __global__ void __launch_bounds__(MT) merge_kernel(const Args a) {
             for (int e = lane; e < n; e += 32) f(b, cands[int64_t(l) * a.cap_list + e]);
         }
     };
+    // The candidates once more in shared memory, where they fit; else they are read twice.
+    const int lists = B * S;
+    const bool fits = lists <= LISTS;
+    int entries = 0;
+    if (fits) {
+        if (tid < lists) size_of[tid] = kind[tid / S] == 1 ? heads[tid].n : 0;
+        __syncthreads();
+        if (warp == 0) {  // where each list begins
+            int run = 0;
+            for (int l0 = 0; l0 < lists; l0 += 32) {
+                const int n = l0 + lane < lists ? size_of[l0 + lane] : 0;
+                int up = n;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int u = __shfl_up_sync(0xffffffffu, up, o);
+                    if (lane >= o) up += u;
+                }
+                if (l0 + lane < lists) begin_of[l0 + lane] = run + up - n;
+                run += __shfl_sync(0xffffffffu, up, 31);
+            }
+            if (lane == 0) begin_of[lists] = run;
+        }
+        __syncthreads();
+        entries = begin_of[lists];
+    }
+    const bool held = fits && entries <= HELD;
     // a bound: `keep` threads have a candidate whose score is not below it
     float mine = NEG;
-    each([&](int b, const Cand& c) {
-        float off;
-        const float s = rough(b, c.x, off);
-        mine = fmaxf(mine, s - off);
-    });
+    if (held) {
+        for (int l = warp; l < lists; l += MT / 32) {
+            const int b = l / S, n = size_of[l], at = begin_of[l];
+            for (int e = lane; e < n; e += 32) {
+                const Cand c = cands[int64_t(l) * a.cap_list + e];
+                float off;
+                const float s = rough(b, c.x, off), high = s + off;
+                // (an overflow or NaN is left to fp64)
+                high_of[at + e] = high > NEG ? high : INFINITY;
+                cand_of[at + e] = c;
+                beam_of[at + e] = uint8_t(b);
+                mine = fmaxf(mine, s - off);
+            }
+        }
+    } else {
+        each([&](int b, const Cand& c) {
+            float off;
+            const float s = rough(b, c.x, off);
+            mine = fmaxf(mine, s - off);
+        });
+    }
     if (tid < B && kind[tid] == 2) mine = fmaxf(mine, float(before_of[tid]));
     const uint32_t my_key = mine > NEG ? key_of(mine) : 0u;
     uint32_t T = 0;
@@ -424,18 +543,32 @@ __global__ void __launch_bounds__(MT) merge_kernel(const Args a) {
         const uint32_t t = T | 1u << bit;
         if (__syncthreads_count(my_key >= t) >= a.keep) T = t;
     }
-    each([&](int b, const Cand& c) {
-        float off;
-        const float s = rough(b, c.x, off);
-        const float high = s + off;
-        if (!(high > NEG) || key_of(high) >= T) {  // (an overflow or NaN is left to fp64)
-            const Best t = exact(b, c);
-            if (t.key != NO_KEY) {
-                const int p = atomicAdd(&count, 1);
-                if (p < LIST) list[p] = t;
-            }
+    auto offer_list = [&](int b, const Cand& c) {
+        const Best t = exact(b, c);
+        if (t.key != NO_KEY) {
+            const int p = atomicAdd(&count, 1);
+            if (p < LIST) list[p] = t;
         }
-    });
+    };
+    if (held) {  // the survivors' places first, so that fp64 runs in full warps
+        for (int e = tid; e < entries; e += MT)
+            if (key_of(high_of[e]) >= T) {
+                const int p = atomicAdd(&survivors, 1);
+                if (p < LIST) alive[p] = uint16_t(e);
+            }
+        __syncthreads();
+        if (survivors <= LIST) {
+            if (tid < survivors) offer_list(beam_of[alive[tid]], cand_of[alive[tid]]);
+        } else if (tid == 0) {
+            count = LIST + 1;
+        }
+    } else {
+        each([&](int b, const Cand& c) {
+            float off;
+            const float s = rough(b, c.x, off), high = s + off;
+            if (!(high > NEG) || key_of(high) >= T) offer_list(b, c);
+        });
+    }
     if (tid < B && kind[tid] == 2) {
         const int p = atomicAdd(&count, 1);
         if (p < LIST) list[p] = ended(tid);
@@ -586,6 +719,12 @@ extern "C" int headloss_beam_select(const void* logits, int64_t requests, int be
     a.inv_cap = inv_cap;
     a.scale = logits_scale;
     a.K = K;
+    a.cap_K = softcap * K;
+    // a cap whose powers leave fp32's range takes the other way to tanh throughout
+    const bool fits = softcap > 1e-3f && softcap < 1e6f && K < 1e6f && K > 1e-6f;
+    a.near = fits ? HL_TANH_B_Y0 * softcap : -1.f;
+    const double C[6] = {HL_TANH_B_C0, HL_TANH_B_C1, HL_TANH_B_C2, HL_TANH_B_C3, HL_TANH_B_C4, HL_TANH_B_C5};
+    for (int i = 0; fits && i < 6; ++i) a.poly[i] = float(C[i] * double(K) / pow(double(softcap), 2 * i));
     a.slices = p.slices;
     a.cap_list = p.cap_list;
     a.heads = static_cast<Head*>(workspace);

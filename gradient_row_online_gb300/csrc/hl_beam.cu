@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "headloss.h"
 #include "headloss_beam.h"
@@ -51,7 +52,7 @@ struct Args {
     float cap, inv_cap;
     float scale, K;       // logits_scale, logits_scale * log2(e)
     float cap_K, near;    // cap * K; the magnitudes that `poly` covers
-    float poly[6];        // z K = x poly(x^2)
+    hl::f2 poly[6];       // z K = x poly(x^2), each coefficient twice
     int slices, cap_list; // slices a row, candidates a slice
     Head* heads;
     Cand* cands;
@@ -130,22 +131,47 @@ struct Words {
             }
         }
     }
-    // whether every magnitude of a word is at most `most` (of two 16-bit values: packed); not with a NaN
-    // that has the sign of its neighbours' maximum alone: such sums end as NaN and are taken again
-    static __device__ __forceinline__ bool within(const uint32_t (&w)[4], float most) {
-        if (DT == HEADLOSS_FP32)
-            return fmaxf(fmaxf(fabsf(__uint_as_float(w[0])), fabsf(__uint_as_float(w[1]))),
-                         fmaxf(fabsf(__uint_as_float(w[2])), fabsf(__uint_as_float(w[3])))) <= most;
-        uint32_t m;
+    // a value in both halves, rounded towards zero
+    static __device__ __forceinline__ uint32_t packed(float v) {
+        if (DT == HEADLOSS_FP32) return __float_as_uint(v);
+        if (DT == HEADLOSS_BF16) return (__float_as_uint(v) >> 16) * 0x10001u;
+        return uint32_t(__half_as_ushort(__float2half_rz(v))) * 0x10001u;
+    }
+    // whether every magnitude of a word is at most `most` (a NaN is not)
+    static __device__ __forceinline__ bool within(const uint32_t (&w)[4], uint32_t most) {
+        if (DT == HEADLOSS_FP32) {
+            const float m = __uint_as_float(most);
+            return fabsf(__uint_as_float(w[0])) <= m && fabsf(__uint_as_float(w[1])) <= m &&
+                   fabsf(__uint_as_float(w[2])) <= m && fabsf(__uint_as_float(w[3])) <= m;
+        }
         if (DT == HEADLOSS_BF16) {
             using P = hl::Pack16<__nv_bfloat16>;
-            m = P::absmax2(P::absmax2(w[0], w[1]), P::absmax2(w[2], w[3]));
-        } else {
-            using P = hl::Pack16<__half>;
-            m = P::absmax2(P::absmax2(w[0], w[1]), P::absmax2(w[2], w[3]));
+            const uint32_t m = P::absmax2(P::absmax2(w[0], w[1]), P::absmax2(w[2], w[3])) & 0x7fff7fffu;
+            return __hble2(*reinterpret_cast<const __nv_bfloat162*>(&m), *reinterpret_cast<const __nv_bfloat162*>(&most));
         }
-        const float2 f = pair(m);
-        return fmaxf(fabsf(f.x), fabsf(f.y)) <= most;
+        using P = hl::Pack16<__half>;
+        const uint32_t m = P::absmax2(P::absmax2(w[0], w[1]), P::absmax2(w[2], w[3])) & 0x7fff7fffu;
+        return __hble2(*reinterpret_cast<const __half2*>(&m), *reinterpret_cast<const __half2*>(&most));
+    }
+    // whether a value (of two) is `least` or more, and not -inf
+    static __device__ __forceinline__ bool reaches(uint32_t t, uint32_t least) {
+        if (DT == HEADLOSS_FP32) return __uint_as_float(t) >= __uint_as_float(least) && __uint_as_float(t) > NEG;
+        if (least == NONE) return t != NONE;
+        if (DT == HEADLOSS_BF16)
+            return !__hblt2(*reinterpret_cast<const __nv_bfloat162*>(&t), *reinterpret_cast<const __nv_bfloat162*>(&least));
+        return !__hblt2(*reinterpret_cast<const __half2*>(&t), *reinterpret_cast<const __half2*>(&least));
+    }
+    static __device__ __forceinline__ void unpack(const uint32_t (&w)[4], hl::f2 (&x)[PER / 2]) {
+        if (DT == HEADLOSS_FP32) {
+            x[0] = hl::pk(__uint_as_float(w[0]), __uint_as_float(w[1]));
+            x[1] = hl::pk(__uint_as_float(w[2]), __uint_as_float(w[3]));
+        } else {
+#pragma unroll
+            for (int k = 0; k < PER / 2; ++k) {
+                const float2 f = pair(w[k]);
+                x[k] = hl::pk(f.x, f.y);
+            }
+        }
     }
 };
 
@@ -155,13 +181,27 @@ __device__ __forceinline__ float mass_any(float x, float zt, const Args& a) {
     const float y = x * a.inv_cap, w = hl::ex2f(-2.8853900817779268f * fabsf(y));
     return hl::ex2f(fmaf(a.cap_K, copysignf((1.f - w) * hl::rcpf(1.f + w), y), -zt));
 }
-// The same of two logits within HL_TANH_B_Y0 caps: z K = x Q(x^2), the cap and K in the coefficients.
-__device__ __forceinline__ hl::f2 mass_near(hl::f2 x, hl::f2 minus_zt, const Args& a) {
-    const hl::f2 t = hl::mul2(x, x);
-    hl::f2 q = hl::pk1(a.poly[5]);
+// The same of N pairs of logits within HL_TANH_B_Y0 caps, added up: z K = x Q(x^2), the cap and K in
+// the coefficients, each of which is fetched once for all pairs.
+template <int N>
+__device__ __forceinline__ hl::f2 mass_near(const hl::f2 (&x)[N], hl::f2 minus_zt, const Args& a) {
+    hl::f2 t[N], q[N];
 #pragma unroll
-    for (int i = 4; i >= 0; --i) q = hl::fma2(q, t, hl::pk1(a.poly[i]));
-    return hl::ex2p(hl::fma2(x, q, minus_zt));
+    for (int j = 0; j < N; ++j) {
+        t[j] = hl::mul2(x[j], x[j]);
+        q[j] = hl::fma2(a.poly[5], t[j], a.poly[4]);
+    }
+#pragma unroll
+    for (int i = 3; i >= 0; --i)
+#pragma unroll
+        for (int j = 0; j < N; ++j) q[j] = hl::fma2(q[j], t[j], a.poly[i]);
+    hl::f2 s = 0ull;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const hl::f2 e = hl::ex2p(hl::fma2(x[j], q[j], minus_zt));
+        s = j ? hl::add2(s, e) : e;
+    }
+    return s;
 }
 
 constexpr int HITS = 256;  // words with a candidate that a slice lists
@@ -190,16 +230,21 @@ __global__ void __launch_bounds__(ST, 4) slice_kernel(const __grid_constant__ Ar
     if (tid == 0) hits = count = 0;
 
     uint32_t w[WORDS][4], wt[WORDS];
+    const bool inside = j0 * W::PER >= off && j1 * W::PER - off <= a.V;  // no word is shared with a neighbour
+    const char* at = base + (int64_t(j0 + tid) * W::PER - off) * W::SIZE;
 #pragma unroll
     for (int i = 0; i < WORDS; ++i) {
-        const int j = j0 + i * ST + tid, lo = j * W::PER - off;
-        if (j < j1 && lo >= 0 && lo + W::PER <= a.V) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(base + int64_t(lo) * W::SIZE));
-            w[i][0] = u.x, w[i][1] = u.y, w[i][2] = u.z, w[i][3] = u.w;
-        } else {
+        const int j = j0 + i * ST + tid;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) w[i][k] = W::NONE;
-            if (j < j1) W::edge(base, lo, a.V, w[i]);
+        for (int k = 0; k < 4; ++k) w[i][k] = W::NONE;
+        if (j < j1) {
+            const int lo = j * W::PER - off;
+            if (inside || (lo >= 0 && lo + W::PER <= a.V)) {
+                const uint4 u = __ldg(reinterpret_cast<const uint4*>(at + i * ST * 16));
+                w[i][0] = u.x, w[i][1] = u.y, w[i][2] = u.z, w[i][3] = u.w;
+            } else {
+                W::edge(base, lo, a.V, w[i]);
+            }
         }
     }
     uint32_t all = W::NONE;
@@ -252,35 +297,37 @@ __global__ void __launch_bounds__(ST, 4) slice_kernel(const __grid_constant__ Ar
     // what is taken off the exponents: of the largest logit, rounded
     const float zt = CAP ? a.cap_K * tanhf(top * a.inv_cap) : top * a.K;
     const hl::f2 minus_zt = hl::pk1(-zt), K2 = hl::pk1(a.K);
+    const uint32_t near2 = CAP ? W::packed(a.near) : 0u, bound2 = W::packed(bound);  // (exact: the bound is a logit)
 #pragma unroll
     for (int i = 0; i < WORDS; ++i) {
-        bool near = true;
-        if (CAP) near = __all_sync(0xffffffffu, W::within(w[i], a.near));
-        if (CAP && !near) {
+        hl::f2 x[W::PER / 2];
+        W::unpack(w[i], x);
+        if (CAP && !__all_sync(0xffffffffu, W::within(w[i], near2))) {
             float s = 0.f;
 #pragma unroll
-            for (int e = 0; e < W::PER; ++e) s += mass_any(W::element(w[i], e), zt, a);
+            for (int e = 0; e < W::PER / 2; ++e) {
+                float lo, hi;
+                hl::upk(x[e], lo, hi);
+                s += mass_any(lo, zt, a) + mass_any(hi, zt, a);
+            }
             s2 = hl::add2(s2, hl::pk(s, 0.f));
             through_any |= 1u << i;
+        } else if (CAP) {
+            s2 = hl::add2(s2, mass_near(x, minus_zt, a));
         } else {
 #pragma unroll
-            for (int e = 0; e < W::PER; e += 2) {
-                const hl::f2 x = hl::pk(W::element(w[i], e), W::element(w[i], e + 1));
-                s2 = hl::add2(s2, CAP ? mass_near(x, minus_zt, a) : hl::ex2p(hl::fma2(x, K2, minus_zt)));
-            }
+            for (int e = 0; e < W::PER / 2; ++e) s2 = hl::add2(s2, hl::ex2p(hl::fma2(x[e], K2, minus_zt)));
         }
     }
 #pragma unroll
-    for (int i = 0; i < WORDS; ++i) {
-        const float u = W::top_of(wt[i]);
-        if (u >= bound && u > NEG) {
+    for (int i = 0; i < WORDS; ++i)
+        if (W::reaches(wt[i], bound2)) {
             const int p = atomicAdd(&hits, 1);
             if (p < HITS) {
                 hit[p] = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
                 hit_at[p] = (j0 + i * ST + tid) * 2 | int(through_any >> i & 1u);
             }
         }
-    }
     sum = hl::hsum(s2);
     __syncthreads();
     const bool crowded = hits > HITS;
@@ -294,7 +341,8 @@ __global__ void __launch_bounds__(ST, 4) slice_kernel(const __grid_constant__ Ar
                 if (CAP) {
                     // the candidates have most of the mass: theirs enters more exactly, relative to the
                     // largest logit's own z
-                    const float had = hit_at[h] & 1 ? mass_any(x, zt, a) : hl::lo_of(mass_near(hl::pk1(x), minus_zt, a));
+                    const hl::f2 one[1] = {hl::pk1(x)};
+                    const float had = hit_at[h] & 1 ? mass_any(x, zt, a) : hl::lo_of(mass_near(one, minus_zt, a));
                     sum += exp2f(fall(x, top, a.cap, a.inv_cap) * a.K) - had;
                 }
             }
@@ -724,7 +772,12 @@ extern "C" int headloss_beam_select(const void* logits, int64_t requests, int be
     const bool fits = softcap > 1e-3f && softcap < 1e6f && K < 1e6f && K > 1e-6f;
     a.near = fits ? HL_TANH_B_Y0 * softcap : -1.f;
     const double C[6] = {HL_TANH_B_C0, HL_TANH_B_C1, HL_TANH_B_C2, HL_TANH_B_C3, HL_TANH_B_C4, HL_TANH_B_C5};
-    for (int i = 0; fits && i < 6; ++i) a.poly[i] = float(C[i] * double(K) / pow(double(softcap), 2 * i));
+    for (int i = 0; fits && i < 6; ++i) {
+        const float c = float(C[i] * double(K) / pow(double(softcap), 2 * i));
+        uint32_t u;
+        memcpy(&u, &c, 4);
+        a.poly[i] = uint64_t(u) << 32 | u;
+    }
     a.slices = p.slices;
     a.cap_list = p.cap_list;
     a.heads = static_cast<Head*>(workspace);

@@ -25,7 +25,6 @@
 
 #include "headloss.h"
 #include "headloss_fp8.h"
-#include "hl_pack.cuh"
 #include "hl_tc.cuh"
 
 namespace hl_fp8 {
@@ -112,7 +111,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
     uint64_t* mma_done = tempty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     const uint32_t items = uint32_t(p.MT) * p.NT * p.splits;
 
     if (threadIdx.x == 0) {
@@ -132,10 +131,11 @@ __global__ void __launch_bounds__(W_THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    grid_wait();
 
     if (warp < 4) {
         give_registers<W_FEW_REGS>();
-        if (warp == 0 && lane == 0) {  // copies
+        if (warp == 0) {  // copies
             uint32_t it = 0;
             bool go = true;
             for (uint32_t i = blockIdx.x; go && i < items; i += gridDim.x) {
@@ -146,42 +146,44 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                 for (int kb = k0; kb < k1; ++kb, ++it) {
                     const int s = int(it % W_STAGES);
                     const uint32_t ph = (it / W_STAGES) & 1u;
-                    if (!wait_phase(su32(&empty[s]), ph ^ 1u, abort, p.err)) {
+                    if (!warp_wait(su32(&empty[s]), ph ^ 1u, abort, p.err)) {
                         go = false;
                         break;
                     }
                     const uint32_t a = su32(smem + s * W_STAGE_BYTES), bar = su32(&full[s]);
-                    mbar_expect_tx(bar, W_STAGE_BYTES);
-                    tma_load_2d(a, &map_a, kb * BK, m * WM, bar);
-                    tma_load_2d(a + WA_BYTES, &map_b, kb * BK, n * WN, bar);
+                    warp_expect_tx(bar, W_STAGE_BYTES);
+                    warp_tma_load_2d(a, &map_a, kb * BK, m * WM, bar);
+                    warp_tma_load_2d(a + WA_BYTES, &map_b, kb * BK, n * WN, bar);
                 }
             }
             for (uint32_t j = it > W_STAGES ? it - W_STAGES : 0; j < it; ++j)  // what was issued has landed
                 drain_phase(su32(&full[j % W_STAGES]), (j / W_STAGES) & 1u, p.err);
-        } else if (warp == 1 && lane == 0) {  // MMAs
+        } else if (warp == 1) {  // MMAs
             uint32_t it = 0;
             bool go = true;
             for (uint32_t i = blockIdx.x; go && i < items; i += gridDim.x) {
                 const int sp = int(i % p.splits);
                 const int k0 = int(int64_t(p.KB) * sp / p.splits), k1 = int(int64_t(p.KB) * (sp + 1) / p.splits);
                 for (int kb = k0; kb < k1; ++kb, ++it) {
-                    const int s = int(it % W_STAGES), acc = int(it & 1u);
-                    if (!wait_phase(su32(&tempty[acc]), ((it >> 1) & 1u) ^ 1u, abort, p.err) ||
-                        !wait_phase(su32(&full[s]), (it / W_STAGES) & 1u, abort, p.err)) {
+                    const int s = int(it % W_STAGES);
+                    const uint32_t acc = it & 1u;
+                    const uint32_t a = su32(smem + s * W_STAGE_BYTES);
+                    const uint64_t da = smem_desc(a), db = smem_desc(a + WA_BYTES);
+                    if (!warp_wait(su32(&full[s]), (it / W_STAGES) & 1u, abort, p.err) ||
+                        !warp_wait(su32(&tempty[acc]), ((it >> 1) & 1u) ^ 1u, abort, p.err)) {
                         go = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a = su32(smem + s * W_STAGE_BYTES), b = a + WA_BYTES;
 #pragma unroll
-                    for (int k = 0; k < BK / 32; ++k)
-                        mma_f8(tmem + uint32_t(acc * WN), smem_desc(a + 32 * k), smem_desc(b + 32 * k), p.idesc, k != 0);
-                    mma_commit(su32(&empty[s]));
-                    mma_commit(su32(&tfull[acc]));
+                    for (int k = 0; k < BK / 32; ++k)  // 32 bytes of K each: two units of the descriptor's address
+                        warp_mma_f8(tmem + acc * WN, da + 2 * k, db + 2 * k, p.idesc, k != 0);
+                    warp_mma_commit(su32(&empty[s]));
+                    warp_mma_commit(su32(&tfull[acc]));
                 }
             }
             if (it) {  // what was issued is done before TMEM is freed
-                mma_commit(su32(mma_done));
+                warp_mma_commit(su32(mma_done));
                 drain_phase(su32(mma_done), 0u, p.err);
             }
         }
@@ -202,9 +204,9 @@ __global__ void __launch_bounds__(W_THREADS, 1)
             const bool in = row < p.M;
             const float* sa = p.a_scales + (in ? row : 0);
             const float* sb = p.b_scales + int64_t(nb) * p.KB;
-            hl::f2 sum[64];
+            float sum[128];
 #pragma unroll
-            for (int j = 0; j < 64; ++j) sum[j] = 0ull;
+            for (int j = 0; j < 128; ++j) sum[j] = 0.f;
             float fa = in ? __ldg(sa + int64_t(k0) * p.M) : 0.f, fb = __ldg(sb + k0);
             for (int kb = k0; kb < k1; ++kb, ++it) {
                 const float s = fa * fb;
@@ -219,14 +221,15 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                 }
                 tc_fence_after();
                 const uint32_t t = tmem + (uint32_t(32 * q) << 16) + uint32_t(acc * WN + 128 * h);
-                const hl::f2 s2 = hl::pk1(s);
+                // the next 32 columns are on their way while these are added
+                uint32_t v[2][32];
+                tmem_ld32(t, v[0]);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    float v[32];
-                    tmem_ld32(t + 32 * c, v);
+                    tmem_wait32(v[c & 1]);
+                    if (c < 3) tmem_ld32(t + 32 * (c + 1), v[(c + 1) & 1]);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        sum[16 * c + j] = hl::fma2(hl::pk(v[2 * j], v[2 * j + 1]), s2, sum[16 * c + j]);
+                    for (int j = 0; j < 32; ++j) sum[32 * c + j] = fmaf(__uint_as_float(v[c & 1][j]), s, sum[32 * c + j]);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -244,15 +247,12 @@ __global__ void __launch_bounds__(W_THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     uint4 w;
-                    float f[8];
                     if (OT == HEADLOSS_FP32) {
-                        hl::upk(sum[16 * g + 2 * c], f[0], f[1]);
-                        hl::upk(sum[16 * g + 2 * c + 1], f[2], f[3]);
+                        const float* f = sum + 32 * g + 4 * c;
                         w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
                                        __float_as_uint(f[3]));
                     } else {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) hl::upk(sum[32 * g + 4 * c + j], f[2 * j], f[2 * j + 1]);
+                        const float* f = sum + 64 * g + 8 * c;
                         w = make_uint4(round2<OT>(f[0], f[1]), round2<OT>(f[2], f[3]), round2<OT>(f[4], f[5]),
                                        round2<OT>(f[6], f[7]));
                     }
@@ -319,15 +319,16 @@ __global__ void __launch_bounds__(256) join_kernel(const float* __restrict__ par
 constexpr int N_STAGES = 4;
 constexpr int N_EPI_WARPS = 4;
 constexpr int N_THREADS = 64 + 32 * N_EPI_WARPS;
+constexpr int N_ACCS = 4;           // accumulators: blocks of K between the MMAs and the scaled sums
 constexpr int NW_BYTES = 128 * BK;  // 128 rows of b, a K block
 
 template <int NT>
 struct Narrow {
     static constexpr int STAGE = NW_BYTES + NT * BK;
-    static constexpr int SCALE_OFF = N_STAGES * STAGE;          // [2][NT] products of scales
-    static constexpr int BAR_OFF = SCALE_OFF + 2 * NT * 4;
+    static constexpr int SCALE_OFF = N_STAGES * STAGE;          // [warp][2][NT] products of scales
+    static constexpr int BAR_OFF = SCALE_OFF + N_EPI_WARPS * 2 * NT * 4;
     static constexpr int SMEM = BAR_OFF + 256 + 1024;
-    static constexpr int TMEM = 2 * NT < 32 ? 32 : 2 * NT;
+    static constexpr int TMEM = N_ACCS * NT;                    // 64, 128 or 256 columns
 };
 
 struct NarrowArgs {
@@ -337,6 +338,7 @@ struct NarrowArgs {
     int64_t N;
     int KB;
     int splits;  // the cluster
+    int early;   // b is in place before the launch before this one began
     void* out;
     int64_t ldo;
     uint32_t idesc;
@@ -355,11 +357,11 @@ __global__ void __launch_bounds__(N_THREADS)
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
     uint64_t* empty = full + N_STAGES;
     uint64_t* tfull = empty + N_STAGES;
-    uint64_t* tempty = tfull + 2;
-    uint64_t* mma_done = tempty + 2;
+    uint64_t* tempty = tfull + N_ACCS;
+    uint64_t* mma_done = tempty + N_ACCS;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     const int S = p.splits, rank = S > 1 ? int(cluster_rank()) : 0;
     const int tile = blockIdx.x / S;
     const int k0 = int(int64_t(p.KB) * rank / S), k1 = int(int64_t(p.KB) * (rank + 1) / S);
@@ -369,7 +371,7 @@ __global__ void __launch_bounds__(N_THREADS)
             mbar_init(su32(&full[s]), 1);
             mbar_init(su32(&empty[s]), 1);
         }
-        for (int a = 0; a < 2; ++a) {
+        for (int a = 0; a < N_ACCS; ++a) {
             mbar_init(su32(&tfull[a]), 1);
             mbar_init(su32(&tempty[a]), N_EPI_WARPS);
         }
@@ -384,69 +386,89 @@ __global__ void __launch_bounds__(N_THREADS)
 
     float sum[NT];
     if (warp == 0) {
-        if (lane == 0) {
-            uint32_t it = 0;
-            for (int kb = k0; kb < k1; ++kb, ++it) {
-                const int s = int(it % N_STAGES);
-                const uint32_t ph = (it / N_STAGES) & 1u;
-                if (!wait_phase(su32(&empty[s]), ph ^ 1u, abort, p.err)) break;
-                const uint32_t w = su32(smem + s * L::STAGE), bar = su32(&full[s]);
-                mbar_expect_tx(bar, L::STAGE);
-                tma_load_2d(w, &map_b, kb * BK, tile * 128, bar);
-                tma_load_2d(w + NW_BYTES, &map_a, kb * BK, 0, bar);
-            }
-            for (uint32_t j = it > N_STAGES ? it - N_STAGES : 0; j < it; ++j)
-                drain_phase(su32(&full[j % N_STAGES]), (j / N_STAGES) & 1u, p.err);
+        // the first stages' rows of b before the wait for a's quantisation
+        const int ahead = p.early ? min(N_STAGES, k1 - k0) : 0;
+        for (int s = 0; s < ahead; ++s) {
+            warp_expect_tx(su32(&full[s]), L::STAGE);
+            warp_tma_load_2d(su32(smem + s * L::STAGE), &map_b, (k0 + s) * BK, tile * 128, su32(&full[s]));
         }
+        grid_wait();
+        uint32_t it = 0;
+        for (int kb = k0; kb < k1; ++kb, ++it) {
+            const int s = int(it % N_STAGES);
+            const uint32_t ph = (it / N_STAGES) & 1u;
+            if (!warp_wait(su32(&empty[s]), ph ^ 1u, abort, p.err) && int(it) >= ahead) break;
+            const uint32_t w = su32(smem + s * L::STAGE), bar = su32(&full[s]);
+            if (int(it) >= ahead) {
+                warp_expect_tx(bar, L::STAGE);
+                warp_tma_load_2d(w, &map_b, kb * BK, tile * 128, bar);
+            }
+            warp_tma_load_2d(w + NW_BYTES, &map_a, kb * BK, 0, bar);
+        }
+        for (uint32_t j = it > N_STAGES ? it - N_STAGES : 0; j < it; ++j)
+            drain_phase(su32(&full[j % N_STAGES]), (j / N_STAGES) & 1u, p.err);
     } else if (warp == 1) {
-        if (lane == 0) {
-            bool issued = false;
-            for (int kb = k0; kb < k1; ++kb) {
-                const uint32_t it = uint32_t(kb - k0);
-                const int s = int(it % N_STAGES), acc = int(it & 1u);
-                if (!wait_phase(su32(&tempty[acc]), ((it >> 1) & 1u) ^ 1u, abort, p.err) ||
-                    !wait_phase(su32(&full[s]), (it / N_STAGES) & 1u, abort, p.err))
-                    break;
-                tc_fence_after();
-                const uint32_t w = su32(smem + s * L::STAGE), x = w + NW_BYTES;
+        bool issued = false;
+        for (int kb = k0; kb < k1; ++kb) {
+            const uint32_t it = uint32_t(kb - k0);
+            const int s = int(it % N_STAGES);
+            const uint32_t acc = it % N_ACCS, w = su32(smem + s * L::STAGE);
+            const uint64_t dw = smem_desc(w), dx = smem_desc(w + NW_BYTES);
+            if (!warp_wait(su32(&full[s]), (it / N_STAGES) & 1u, abort, p.err) ||
+                !warp_wait(su32(&tempty[acc]), ((it / N_ACCS) & 1u) ^ 1u, abort, p.err))
+                break;
+            tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < BK / 32; ++k)
-                    mma_f8(tmem + uint32_t(acc * NT), smem_desc(w + 32 * k), smem_desc(x + 32 * k), p.idesc, k != 0);
-                mma_commit(su32(&empty[s]));
-                mma_commit(su32(&tfull[acc]));
-                issued = true;
-            }
-            if (issued) {
-                mma_commit(su32(mma_done));
-                drain_phase(su32(mma_done), 0u, p.err);
-            }
+            for (int k = 0; k < BK / 32; ++k) warp_mma_f8(tmem + acc * NT, dw + 2 * k, dx + 2 * k, p.idesc, k != 0);
+            warp_mma_commit(su32(&empty[s]));
+            warp_mma_commit(su32(&tfull[acc]));
+            issued = true;
+        }
+        if (issued) {
+            warp_mma_commit(su32(mma_done));
+            drain_phase(su32(mma_done), 0u, p.err);
         }
     } else {  // a thread has one row of b, every row of a
-        const int q = warp & 3, t = threadIdx.x - 64;
+        grid_wait();
+        const int q = warp & 3;
 #pragma unroll
         for (int j = 0; j < NT; ++j) sum[j] = 0.f;
         const float* sb = p.b_scales + int64_t(tile) * p.KB;
-        const bool mine = t < NT, in = t < p.M;
-        float next = mine && in && k0 < k1 ? __ldg(p.a_scales + int64_t(k0) * p.M + t) * __ldg(sb + k0) : 0.f;
-        for (int kb = k0; kb < k1; ++kb) {
-            const uint32_t it = uint32_t(kb - k0);
-            const int acc = int(it & 1u);
-            if (mine) scale[acc * NT + t] = next;
-            if (mine && in && kb + 1 < k1) next = __ldg(p.a_scales + int64_t(kb + 1) * p.M + t) * __ldg(sb + kb + 1);
-            named_sync(1, 32 * N_EPI_WARPS);  // the scales of this block; those two blocks back were read
-            if (!wait_phase(su32(&tfull[acc]), (it >> 1) & 1u, abort, p.err)) *abort = 1;
-            tc_fence_after();
-            const uint32_t at = tmem + (uint32_t(32 * q) << 16) + uint32_t(acc * NT);
+        float* mine = scale + (warp - 2) * 2 * NT;  // this warp's products of scales, two blocks of K
+        constexpr int PER = NT < 32 ? 1 : NT / 32;
+        float next[PER];
+        auto fetch = [&](int kb) {
 #pragma unroll
-            for (int c = 0; c < NT / 16; ++c) {
-                float v[16];
-                tmem_ld16(at + 16 * c, v);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) sum[16 * c + j] = fmaf(v[j], scale[acc * NT + 16 * c + j], sum[16 * c + j]);
+            for (int j = 0; j < PER; ++j) {
+                const int t = lane + 32 * j;
+                next[j] = t < NT && t < p.M ? __ldg(p.a_scales + int64_t(kb) * p.M + t) * __ldg(sb + kb) : 0.f;
             }
+        };
+        if (k0 < k1) fetch(k0);
+        for (int kb = k0; kb < k1; ++kb) {
+            const uint32_t it = uint32_t(kb - k0), acc = it % N_ACCS;
+            float* now = mine + (it & 1u) * NT;
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                if (lane + 32 * j < NT) now[lane + 32 * j] = next[j];
+            if (kb + 1 < k1) fetch(kb + 1);
+            __syncwarp();
+            if (!wait_phase(su32(&tfull[acc]), (it / N_ACCS) & 1u, abort, p.err)) break;
+            tc_fence_after();
+            const uint32_t at = tmem + (uint32_t(32 * q) << 16) + acc * NT;
+            uint32_t v[NT];
+            tmem_ld_all<NT>(at, v);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(su32(&tempty[acc]));
+#pragma unroll
+            for (int j = 0; j < NT; j += 4) {
+                const float4 s = *reinterpret_cast<const float4*>(now + j);
+                sum[j] = fmaf(__uint_as_float(v[j]), s.x, sum[j]);
+                sum[j + 1] = fmaf(__uint_as_float(v[j + 1]), s.y, sum[j + 1]);
+                sum[j + 2] = fmaf(__uint_as_float(v[j + 2]), s.z, sum[j + 2]);
+                sum[j + 3] = fmaf(__uint_as_float(v[j + 3]), s.w, sum[j + 3]);
+            }
         }
     }
     const int v = (warp & 3) * 32 + lane;  // the tile's row of b (epilogue warps)
@@ -488,6 +510,14 @@ __global__ void __launch_bounds__(N_THREADS)
 }
 
 // ------------------------------------------------------------------ host ----
+
+int quantize(const void* x, int64_t rows, int64_t cols, int64_t ld, int dtype, int type, void* q, int64_t ldq,
+             float* scales, int block, void* qt, int64_t ldqt, float* scales_t, int block_t, bool leads,
+             cudaStream_t s);  // hl_fp8_quant.cu
+
+// a quantised x of M x K within a workspace: its codes, its scales
+int64_t codes_bytes(int64_t M, int64_t K) { return M * ((K + 15) / 16 * 16); }
+int64_t scales_bytes(int64_t M, int64_t K) { return (M * ((K + 127) / 128) * 4 + 15) / 16 * 16; }
 
 int make_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, int64_t rows, int64_t cols,
              int64_t pitch_bytes, int box_rows, int box_cols) {
@@ -546,14 +576,22 @@ int sm_count(int* sms) {
 
 template <int OT>
 int launch_wide(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo, const WideArgs& a, int sms,
-                cudaStream_t s) {
+                bool early, cudaStream_t s) {
     const void* fn = reinterpret_cast<const void*>(&wide_kernel<OT>);
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, W_SMEM) != cudaSuccess)
         return HEADLOSS_ERR_CUDA;
     const int64_t items = int64_t(a.MT) * a.NT * a.splits;
-    const int grid = int(items < sms ? items : sms);
-    wide_kernel<OT><<<grid, W_THREADS, W_SMEM, s>>>(ma, mb, mo, a);
-    return cudaGetLastError() == cudaSuccess ? HEADLOSS_OK : HEADLOSS_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(items < sms ? items : sms));
+    cfg.blockDim = dim3(W_THREADS);
+    cfg.dynamicSmemBytes = W_SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, wide_kernel<OT>, ma, mb, mo, a) == cudaSuccess ? HEADLOSS_OK : HEADLOSS_ERR_CUDA;
 }
 
 template <int NT, int OT>
@@ -566,12 +604,14 @@ int launch_narrow(const CUtensorMap& mb, const CUtensorMap& ma, const NarrowArgs
     cfg.blockDim = dim3(N_THREADS);
     cfg.dynamicSmemBytes = Narrow<NT>::SMEM;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = unsigned(a.splits);
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = a.early ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, narrow_kernel<NT, OT>, mb, ma, a) == cudaSuccess ? HEADLOSS_OK
                                                                                     : HEADLOSS_ERR_CUDA;
 }
@@ -591,11 +631,13 @@ extern "C" int64_t headloss_fp8_workspace(int64_t M, int64_t N, int64_t K) {
     return M && N ? plan_of(M, N, K, sms).bytes : 0;
 }
 
-extern "C" int headloss_fp8_matmul(const void* a, int64_t lda, const float* a_scales, int a_type,
-                                   const void* b, int64_t ldb, const float* b_scales, int b_type, int64_t M,
-                                   int64_t N, int64_t K, void* out, int64_t ldo, int out_dtype,
-                                   void* workspace, int64_t workspace_bytes, int* err, void* stream) {
-    using namespace hl_fp8;
+namespace hl_fp8 {
+
+// The product; early: the kernel in front of it in the stream is a's quantisation, which leads.
+int matmul(const void* a, int64_t lda, const float* a_scales, int a_type, const void* b, int64_t ldb,
+           const float* b_scales, int b_type, int64_t M, int64_t N, int64_t K, void* out, int64_t ldo,
+           int out_dtype, void* workspace, int64_t workspace_bytes, int* err, bool early, bool check_only,
+           cudaStream_t s) {
     if (!sizes_ok(M, N, K) || lda < K || ldb < K || ldo < N) return HEADLOSS_ERR_ARG;
     auto known = [](int t) { return t == HEADLOSS_E4M3 || t == HEADLOSS_E5M2; };
     if (!known(a_type) || !known(b_type)) return HEADLOSS_ERR_ARG;
@@ -612,7 +654,7 @@ extern "C" int headloss_fp8_matmul(const void* a, int64_t lda, const float* a_sc
     if (!sm_count(&sms)) return HEADLOSS_ERR_CUDA;
     const Plan plan = plan_of(M, N, K, sms);
     if (plan.bytes > 0 && (!workspace || workspace_bytes < plan.bytes)) return HEADLOSS_ERR_ARG;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (check_only) return HEADLOSS_OK;
     const int KB = int((K + BK - 1) / BK);
     CUtensorMap ma, mb, mo;
     const auto U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
@@ -626,6 +668,7 @@ extern "C" int headloss_fp8_matmul(const void* a, int64_t lda, const float* a_sc
         n.N = N;
         n.KB = KB;
         n.splits = plan.splits;
+        n.early = early;
         n.out = out;
         n.ldo = ldo;
         n.idesc = idesc_of(128, plan.narrow, b_type, a_type);
@@ -657,7 +700,7 @@ extern "C" int headloss_fp8_matmul(const void* a, int64_t lda, const float* a_sc
         w.tma_out = w.n_even = 1;
         if (make_map(&mo, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, workspace, plan.splits * plan.mpad, plan.ldw, plan.ldw * 4, 32, 32))
             return HEADLOSS_ERR_CUDA;
-        const int rc = launch_wide<HEADLOSS_FP32>(ma, mb, mo, w, sms, s);
+        const int rc = launch_wide<HEADLOSS_FP32>(ma, mb, mo, w, sms, early, s);
         if (rc != HEADLOSS_OK) return rc;
         const int64_t words = M * (plan.ldw / 4);
         const int grid = int((words + 255) / 256 < 8 * sms ? (words + 255) / 256 : 8 * sms);
@@ -678,7 +721,44 @@ extern "C" int headloss_fp8_matmul(const void* a, int64_t lda, const float* a_sc
     } else {
         mo = ma;  // not used
     }
-    return out_dtype == HEADLOSS_FP32   ? launch_wide<HEADLOSS_FP32>(ma, mb, mo, w, sms, s)
-           : out_dtype == HEADLOSS_BF16 ? launch_wide<HEADLOSS_BF16>(ma, mb, mo, w, sms, s)
-                                        : launch_wide<HEADLOSS_FP16>(ma, mb, mo, w, sms, s);
+    return out_dtype == HEADLOSS_FP32   ? launch_wide<HEADLOSS_FP32>(ma, mb, mo, w, sms, early, s)
+           : out_dtype == HEADLOSS_BF16 ? launch_wide<HEADLOSS_BF16>(ma, mb, mo, w, sms, early, s)
+                                        : launch_wide<HEADLOSS_FP16>(ma, mb, mo, w, sms, early, s);
+}
+
+}  // namespace hl_fp8
+
+extern "C" int headloss_fp8_matmul(const void* a, int64_t lda, const float* a_scales, int a_type,
+                                   const void* b, int64_t ldb, const float* b_scales, int b_type, int64_t M,
+                                   int64_t N, int64_t K, void* out, int64_t ldo, int out_dtype,
+                                   void* workspace, int64_t workspace_bytes, int* err, void* stream) {
+    return hl_fp8::matmul(a, lda, a_scales, a_type, b, ldb, b_scales, b_type, M, N, K, out, ldo, out_dtype,
+                          workspace, workspace_bytes, err, false, false, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int64_t headloss_fp8_linear_workspace(int64_t M, int64_t N, int64_t K) {
+    const int64_t need = headloss_fp8_workspace(M, N, K);
+    return need < 0 ? -1 : hl_fp8::codes_bytes(M, K) + hl_fp8::scales_bytes(M, K) + need;
+}
+
+extern "C" int headloss_fp8_linear(const void* x, int64_t ldx, int dtype, const void* b, int64_t ldb,
+                                   const float* b_scales, int b_type, int64_t M, int64_t N, int64_t K,
+                                   void* out, int64_t ldo, int out_dtype, void* workspace,
+                                   int64_t workspace_bytes, int* err, void* stream) {
+    using namespace hl_fp8;
+    if (!sizes_ok(M, N, K)) return HEADLOSS_ERR_ARG;
+    const int64_t pitch = (K + 15) / 16 * 16, codes = codes_bytes(M, K), scales = scales_bytes(M, K);
+    char* at = static_cast<char*>(workspace);
+    if (M && N && (!at || workspace_bytes < codes + scales)) return HEADLOSS_ERR_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    auto product = [&](bool check_only) {
+        return matmul(at, pitch, reinterpret_cast<float*>(at + codes), HEADLOSS_E4M3, b, ldb, b_scales, b_type, M, N,
+                      K, out, ldo, out_dtype, at + codes + scales, workspace_bytes - codes - scales, err, true,
+                      check_only, s);
+    };
+    int rc = product(true);
+    if (rc != HEADLOSS_OK || M == 0 || N == 0) return rc;
+    rc = quantize(x, M, K, ldx, dtype, HEADLOSS_E4M3, at, pitch, reinterpret_cast<float*>(at + codes), 1, nullptr, 0,
+                  nullptr, 0, true, s);
+    return rc == HEADLOSS_OK ? product(false) : rc;
 }

@@ -2,10 +2,13 @@
 // transpose in 8-bit floating point with a scale for each block of 128.
 //
 // One CTA a 128 x 128 tile, which holds whole blocks of every kind.  A thread has 8 rows x 8
-// columns in registers: the row maxima join over the 16 lanes of a row, the column maxima over
-// the 16 row groups through shared memory.  The transpose's codes are turned 8 x 8 in registers
-// and leave through a 16 KB tile in shared memory whose 8-byte units are placed by XOR, so that
-// both its writes and its reads touch every bank once and global stores are whole 128-byte rows.
+// columns in registers, 16-bit inputs as they came. Magnitudes compare as integers or packed pairs,
+// with a NaN above all. The row maxima join over the 16 lanes of a row by halving exchanges, which
+// leave each lane one row's maximum: a lane computes one scale, not eight. The column maxima join
+// over the 16 row groups through shared memory. Where both outputs have 128 x 128 blocks the codes are
+// the same: they are made once and turned 8 x 8 by byte permutes. The transpose's codes leave through
+// a 16 KB tile in shared memory whose 8-byte units are placed by XOR, so that both its writes and its
+// reads touch every bank once and global stores are whole 128-byte rows.
 // HBM bound: each input element is read once, each code written once.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -26,7 +29,6 @@ struct QuantArgs {
     const void* x;
     int64_t rows, cols, ld;
     int vec;     // rows start on 16-byte boundaries
-    int e5m2;
     float inv_top;
     unsigned char* q;
     int64_t ldq;
@@ -37,140 +39,231 @@ struct QuantArgs {
     float* scales_t;
     int block_t;
     int col_tiles, row_tiles;
+    int leads;   // the kernel launched next waits for this one itself
 };
 
 __device__ __forceinline__ float scale_of(uint32_t amax_bits, float inv_top) {
     if (amax_bits >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
     return fmaxf(__fmul_rn(__uint_as_float(amax_bits), inv_top), LEAST);
 }
-__device__ __forceinline__ uint32_t code2(float a, float b, int e5m2) {
-    return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, e5m2 ? __NV_E5M2 : __NV_E4M3);
+template <int TYPE>
+__device__ __forceinline__ uint32_t code2(float a, float b) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, TYPE == HEADLOSS_E5M2 ? __NV_E5M2 : __NV_E4M3);
 }
-__device__ __forceinline__ uint2 code8(const float (&v)[8], int e5m2) {
-    return make_uint2(code2(v[0], v[1], e5m2) | code2(v[2], v[3], e5m2) << 16,
-                      code2(v[4], v[5], e5m2) | code2(v[6], v[7], e5m2) << 16);
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
+// The transpose of 4 x 4 bytes.
+__device__ __forceinline__ void turn4(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t (&t)[4]) {
+    const uint32_t ab0 = prmt(a, b, 0x5140), ab1 = prmt(a, b, 0x7362);
+    const uint32_t cd0 = prmt(c, d, 0x5140), cd1 = prmt(c, d, 0x7362);
+    t[0] = prmt(ab0, cd0, 0x5410);
+    t[1] = prmt(ab0, cd0, 0x7632);
+    t[2] = prmt(ab1, cd1, 0x5410);
+    t[3] = prmt(ab1, cd1, 0x7632);
 }
 
+// Eight rows x eight columns of a thread.
 template <int DT>
-__device__ __forceinline__ float load1(const void* p, int64_t i) {
-    if (DT == HEADLOSS_FP32) return static_cast<const float*>(p)[i];
-    if (DT == HEADLOSS_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-    return __half2float(static_cast<const __half*>(p)[i]);
-}
-template <int DT>
-__device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
-    if (DT == HEADLOSS_FP32) {
-        const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-        const float4 a = f[0], b = f[1];
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-        const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+struct Tile {
+    uint32_t w[8][4];  // pairs of 16-bit values
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {  // of the magnitudes; the signs are lost
+        uint32_t r;
+        if (DT == HEADLOSS_BF16) asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        else asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ float2 pair(uint32_t u) {
+        if (DT == HEADLOSS_BF16) return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+        return __half22float2(*reinterpret_cast<const __half2*>(&u));
+    }
+    __device__ __forceinline__ void load(int i, const void* x, int64_t at) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at));
+        w[i][0] = u.x, w[i][1] = u.y, w[i][2] = u.z, w[i][3] = u.w;
+    }
+    __device__ __forceinline__ void load_some(int i, const void* x, int64_t at, int n) {
+        const uint16_t* p = static_cast<const uint16_t*>(x) + at;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            w[i][k] = (2 * k < n ? uint32_t(p[2 * k]) : 0u) | (2 * k + 1 < n ? uint32_t(p[2 * k + 1]) << 16 : 0u);
+    }
+    __device__ __forceinline__ void values(int i, int k, float& lo, float& hi) const {
+        const float2 f = pair(w[i][k]);
+        lo = f.x;
+        hi = f.y;
+    }
+    // the bits of the largest magnitude as fp32
+    __device__ __forceinline__ uint32_t row_top(int i) const {
+        const float2 f = pair(larger(larger(w[i][0], w[i][1]), larger(w[i][2], w[i][3])));
+        return max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu);
+    }
+    __device__ __forceinline__ void col_tops(uint32_t (&m)[8]) const {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float2 f = DT == HEADLOSS_BF16
-                                 ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u[k]))
-                                 : __half22float2(*reinterpret_cast<const __half2*>(&u[k]));
-            v[2 * k] = f.x;
-            v[2 * k + 1] = f.y;
+            uint32_t t = w[0][k];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) t = larger(t, w[i][k]);
+            const float2 f = pair(t);
+            m[2 * k] = __float_as_uint(f.x) & 0x7fffffffu;
+            m[2 * k + 1] = __float_as_uint(f.y) & 0x7fffffffu;
         }
     }
-}
-
-template <int DT>
-__global__ void __launch_bounds__(QTHREADS) quantize_kernel(const QuantArgs a) {
-    __shared__ uint32_t wmax[8][QT];            // column maxima of each warp, or the warps' maxima
-    __shared__ float cscale[QT];
-    __shared__ __align__(16) uint2 turned[QT][16];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g = tid >> 4, c = tid & 15;       // row group, column group
-    const int ct = blockIdx.x % a.col_tiles, rt = blockIdx.x / a.col_tiles;
-    const int64_t r0 = int64_t(rt) * QT, c0 = int64_t(ct) * QT;
-    const int64_t row = r0 + g * 8, col = c0 + c * 8;
-
+};
+template <>
+struct Tile<HEADLOSS_FP32> {
     float v[8][8];
-    const bool whole = a.vec && col + 8 <= a.cols;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (whole && row + i < a.rows) {
-            load8<DT>(a.x, (row + i) * a.ld + col, v[i]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[i][j] = row + i < a.rows && col + j < a.cols ? load1<DT>(a.x, (row + i) * a.ld + col + j) : 0.f;
-        }
+    __device__ __forceinline__ void load(int i, const void* x, int64_t at) {
+        const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
+        const float4 a = __ldg(f), b = __ldg(f + 1);
+        v[i][0] = a.x, v[i][1] = a.y, v[i][2] = a.z, v[i][3] = a.w;
+        v[i][4] = b.x, v[i][5] = b.y, v[i][6] = b.z, v[i][7] = b.w;
     }
-    // magnitudes compare as integers, NaN above infinity above the rest
-    uint32_t rm[8] = {}, cm[8] = {};
+    __device__ __forceinline__ void load_some(int i, const void* x, int64_t at, int n) {
+        const float* p = static_cast<const float*>(x) + at;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t m = __float_as_uint(v[i][j]) & 0x7fffffffu;
-            rm[i] = max(rm[i], m);
-            cm[j] = max(cm[j], m);
-        }
-    const bool whole_block = (a.q && a.block == QT) || (a.qt && a.block_t == QT);
-    const bool by_column = a.qt && a.block_t == 1;
-    float ts = 0.f;  // the tile's scale
-    if (whole_block) {
+        for (int j = 0; j < 8; ++j) v[i][j] = j < n ? p[j] : 0.f;
+    }
+    __device__ __forceinline__ void values(int i, int k, float& lo, float& hi) const {
+        lo = v[i][2 * k];
+        hi = v[i][2 * k + 1];
+    }
+    __device__ __forceinline__ uint32_t row_top(int i) const {
         uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, rm[i]);
+        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[i][j]) & 0x7fffffffu);
+        return m;
+    }
+    __device__ __forceinline__ void col_tops(uint32_t (&m)[8]) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            m[j] = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m[j] = max(m[j], __float_as_uint(v[i][j]) & 0x7fffffffu);
+        }
+    }
+};
+
+template <int DT, int TYPE>
+__global__ void __launch_bounds__(QTHREADS) quantize_kernel(const __grid_constant__ QuantArgs a) {
+    __shared__ uint32_t wmax[8][QT];            // column maxima of each warp, or the warps' maxima
+    __shared__ __align__(16) float cinv[QT];    // inverse scales of the columns
+    __shared__ __align__(16) uint2 turned[QT][16];
+    if (a.leads) asm volatile("griddepcontrol.launch_dependents;");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = tid >> 4, c = tid & 15;       // row group, column group
+    const int rt = int(blockIdx.x / unsigned(a.col_tiles)), ct = int(blockIdx.x) - rt * a.col_tiles;
+    const int64_t r0 = int64_t(rt) * QT, c0 = int64_t(ct) * QT;
+    const int64_t row = r0 + g * 8, col = c0 + c * 8;
+    const int rows = int(max(int64_t(0), min(int64_t(8), a.rows - row))), cols = int(max(int64_t(0), min(int64_t(8), a.cols - col)));
+
+    Tile<DT> t;
+    const bool whole = a.vec && cols == 8;
+    const int64_t at = row * a.ld + col;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (whole && i < rows) t.load(i, a.x, at + i * a.ld);
+        else t.load_some(i, a.x, at + i * a.ld, i < rows ? cols : 0);
+    }
+    const bool same = a.q && a.qt && a.block == QT && a.block_t == QT;  // one set of codes
+    const bool by_row = a.q && a.block == 1, by_column = a.qt && a.block_t == 1;
+    float ts = 0.f, tinv = 0.f;  // the tile's scale
+    if ((a.q && !by_row) || (a.qt && !by_column)) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, t.row_top(i));
         m = __reduce_max_sync(0xffffffffu, m);
         if (lane == 0) wmax[warp][0] = m;
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < 8; ++w) m = max(m, wmax[w][0]);
         ts = scale_of(m, a.inv_top);
-        __syncthreads();
+        tinv = __frcp_rn(ts);
+        if (tid == 0 && a.q && !by_row) a.scales[int64_t(rt) * a.col_tiles + ct] = ts;
+        if (tid == 0 && a.qt && !by_column) a.scales_t[int64_t(ct) * a.row_tiles + rt] = ts;
+        if (by_column) __syncthreads();
     }
     if (by_column) {
+        uint32_t cm[8];
+        t.col_tops(cm);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t m = max(cm[j], __shfl_xor_sync(0xffffffffu, cm[j], 16));
-            if (lane < 16) wmax[warp][c * 8 + j] = m;
+        for (int j = 0; j < 8; ++j) cm[j] = max(cm[j], __shfl_xor_sync(0xffffffffu, cm[j], 16));
+        if (lane < 16) {
+            *reinterpret_cast<uint4*>(&wmax[warp][c * 8]) = make_uint4(cm[0], cm[1], cm[2], cm[3]);
+            *reinterpret_cast<uint4*>(&wmax[warp][c * 8 + 4]) = make_uint4(cm[4], cm[5], cm[6], cm[7]);
         }
         __syncthreads();
         if (tid < QT) {
             uint32_t m = 0;
 #pragma unroll
             for (int w = 0; w < 8; ++w) m = max(m, wmax[w][tid]);
-            cscale[tid] = scale_of(m, a.inv_top);
-            if (c0 + tid < a.cols) a.scales_t[int64_t(rt) * a.cols + c0 + tid] = cscale[tid];
+            const float s = scale_of(m, a.inv_top);
+            cinv[tid] = __frcp_rn(s);
+            if (c0 + tid < a.cols) a.scales_t[int64_t(rt) * a.cols + c0 + tid] = s;
         }
         __syncthreads();
     }
     if (a.q) {
-        if (a.block == QT && tid == 0) a.scales[int64_t(rt) * a.col_tiles + ct] = ts;
+        float mine = tinv;  // by rows: the inverse scale of row 4 (c & 8) + 2 (c & 4) + (c & 2) of the eight
+        if (by_row) {
+            uint32_t m[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m[i] = t.row_top(i);
+#pragma unroll
+            for (int n = 4, o = 8; n; n >>= 1, o >>= 1)
+#pragma unroll
+                for (int i = 0; i < n; ++i) {
+                    const bool high = c & o;
+                    const uint32_t give = high ? m[i] : m[i + n], keep = high ? m[i + n] : m[i];
+                    m[i] = max(keep, __shfl_xor_sync(0xffffffffu, give, o));
+                }
+            m[0] = max(m[0], __shfl_xor_sync(0xffffffffu, m[0], 1));
+            const float s = scale_of(m[0], a.inv_top);
+            const int i = (c & 8) / 2 + (c & 4) / 2 + (c & 2) / 2;
+            if (!(c & 1) && i < rows) a.scales[int64_t(ct) * a.rows + row + i] = s;
+            mine = __frcp_rn(s);
+        }
+        uint2 codes[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            float s = ts;
-            if (a.block == 1) {
-                uint32_t m = rm[i];
+            const float inv = by_row ? __shfl_sync(0xffffffffu, mine, (lane & 16) | (i & 4) * 2 | (i & 2) * 2 | (i & 1) * 2) : tinv;
+            uint32_t h[4];
 #pragma unroll
-                for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-                s = scale_of(m, a.inv_top);
-                if (c == 0 && row + i < a.rows) a.scales[int64_t(ct) * a.rows + row + i] = s;
+            for (int k = 0; k < 4; ++k) {
+                float lo, hi;
+                t.values(i, k, lo, hi);
+                h[k] = code2<TYPE>(__fmul_rn(lo, inv), __fmul_rn(hi, inv));
             }
-            const float inv = __frcp_rn(s);
-            float y[8];
+            codes[i] = make_uint2(prmt(h[0], h[1], 0x5410), prmt(h[2], h[3], 0x5410));
+            if (i < rows && cols > 0) *reinterpret_cast<uint2*>(a.q + (row + i) * a.ldq + col) = codes[i];
+        }
+        if (same) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = __fmul_rn(v[i][j], inv);
-            if (row + i < a.rows && col < a.cols)
-                *reinterpret_cast<uint2*>(a.q + (row + i) * a.ldq + col) = code8(y, a.e5m2);
+            for (int h = 0; h < 2; ++h) {
+                uint32_t lo[4], hi[4];
+                turn4(h ? codes[0].y : codes[0].x, h ? codes[1].y : codes[1].x, h ? codes[2].y : codes[2].x,
+                      h ? codes[3].y : codes[3].x, lo);
+                turn4(h ? codes[4].y : codes[4].x, h ? codes[5].y : codes[5].x, h ? codes[6].y : codes[6].x,
+                      h ? codes[7].y : codes[7].x, hi);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) turned[c * 8 + 4 * h + j][g ^ c] = make_uint2(lo[j], hi[j]);
+            }
         }
     }
     if (a.qt) {
-        if (a.block_t == QT && tid == 0) a.scales_t[int64_t(ct) * a.row_tiles + rt] = ts;
+        if (!same) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float inv = __frcp_rn(by_column ? cscale[c * 8 + j] : ts);
-            float y[8];
+            for (int k = 0; k < 4; ++k) {
+                const float2 inv = by_column ? *reinterpret_cast<const float2*>(&cinv[c * 8 + 2 * k]) : make_float2(tinv, tinv);
+                uint32_t h0[4], h1[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(v[i][j], inv);
-            turned[c * 8 + j][g ^ c] = code8(y, a.e5m2);
+                for (int i = 0; i < 4; ++i) {
+                    float a0, a1, b0, b1;
+                    t.values(2 * i, k, a0, a1);
+                    t.values(2 * i + 1, k, b0, b1);
+                    h0[i] = code2<TYPE>(__fmul_rn(a0, inv.x), __fmul_rn(b0, inv.x));
+                    h1[i] = code2<TYPE>(__fmul_rn(a1, inv.y), __fmul_rn(b1, inv.y));
+                }
+                turned[c * 8 + 2 * k][g ^ c] = make_uint2(prmt(h0[0], h0[1], 0x5410), prmt(h0[2], h0[3], 0x5410));
+                turned[c * 8 + 2 * k + 1][g ^ c] = make_uint2(prmt(h1[0], h1[1], 0x5410), prmt(h1[2], h1[3], 0x5410));
+            }
         }
         __syncthreads();
 #pragma unroll
@@ -182,12 +275,15 @@ __global__ void __launch_bounds__(QTHREADS) quantize_kernel(const QuantArgs a) {
     }
 }
 
-}  // namespace hl_fp8
+template <int DT>
+void launch_quantize(const QuantArgs& a, int type, unsigned tiles, cudaStream_t s) {
+    if (type == HEADLOSS_E4M3) quantize_kernel<DT, HEADLOSS_E4M3><<<tiles, QTHREADS, 0, s>>>(a);
+    else quantize_kernel<DT, HEADLOSS_E5M2><<<tiles, QTHREADS, 0, s>>>(a);
+}
 
-extern "C" int headloss_fp8_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld, int dtype,
-                                     int type, void* q, int64_t ldq, float* scales, int block, void* qt,
-                                     int64_t ldqt, float* scales_t, int block_t, void* stream) {
-    using namespace hl_fp8;
+int quantize(const void* x, int64_t rows, int64_t cols, int64_t ld, int dtype, int type, void* q, int64_t ldq,
+             float* scales, int block, void* qt, int64_t ldqt, float* scales_t, int block_t, bool leads,
+             cudaStream_t s) {
     const int64_t most = (int64_t(1) << 31) - QT;
     if (rows < 0 || cols < 0 || rows >= most || cols >= most || ld < cols) return HEADLOSS_ERR_ARG;
     if (type != HEADLOSS_E4M3 && type != HEADLOSS_E5M2) return HEADLOSS_ERR_ARG;
@@ -209,8 +305,7 @@ extern "C" int headloss_fp8_quantize(const void* x, int64_t rows, int64_t cols, 
     a.cols = cols;
     a.ld = ld;
     a.vec = !(bits(x) & 15) && (rows == 1 || !((ld * size) & 15));
-    a.e5m2 = type == HEADLOSS_E5M2;
-    a.inv_top = a.e5m2 ? float(1.0 / 57344.0) : float(1.0 / 448.0);
+    a.inv_top = type == HEADLOSS_E5M2 ? float(1.0 / 57344.0) : float(1.0 / 448.0);
     a.q = static_cast<unsigned char*>(q);
     a.ldq = ldq;
     a.scales = scales;
@@ -223,9 +318,18 @@ extern "C" int headloss_fp8_quantize(const void* x, int64_t rows, int64_t cols, 
     a.row_tiles = int((rows + QT - 1) / QT);
     const int64_t tiles = int64_t(a.col_tiles) * a.row_tiles;
     if (tiles > INT32_MAX) return HEADLOSS_ERR_ARG;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (dtype == HEADLOSS_FP32) quantize_kernel<HEADLOSS_FP32><<<unsigned(tiles), QTHREADS, 0, s>>>(a);
-    else if (dtype == HEADLOSS_BF16) quantize_kernel<HEADLOSS_BF16><<<unsigned(tiles), QTHREADS, 0, s>>>(a);
-    else quantize_kernel<HEADLOSS_FP16><<<unsigned(tiles), QTHREADS, 0, s>>>(a);
+    a.leads = leads;
+    if (dtype == HEADLOSS_FP32) launch_quantize<HEADLOSS_FP32>(a, type, unsigned(tiles), s);
+    else if (dtype == HEADLOSS_BF16) launch_quantize<HEADLOSS_BF16>(a, type, unsigned(tiles), s);
+    else launch_quantize<HEADLOSS_FP16>(a, type, unsigned(tiles), s);
     return cudaGetLastError() == cudaSuccess ? HEADLOSS_OK : HEADLOSS_ERR_CUDA;
+}
+
+}  // namespace hl_fp8
+
+extern "C" int headloss_fp8_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld, int dtype,
+                                     int type, void* q, int64_t ldq, float* scales, int block, void* qt,
+                                     int64_t ldqt, float* scales_t, int block_t, void* stream) {
+    return hl_fp8::quantize(x, rows, cols, ld, dtype, type, q, ldq, scales, block, qt, ldqt, scales_t, block_t,
+                            false, static_cast<cudaStream_t>(stream));
 }

@@ -59,7 +59,8 @@ EXPORTS = ("headloss_create", "headloss_forward_backward", "headloss_get_device_
            "headloss_lmhead_logits", "headloss_lmhead_logits_rowstats",
            "headloss_sample", "headloss_clip_create", "headloss_clip_grads",
            "headloss_clip_destroy", "headloss_fp8_quantize", "headloss_fp8_workspace",
-           "headloss_fp8_matmul", "headloss_beam_workspace", "headloss_beam_select",
+           "headloss_fp8_matmul", "headloss_fp8_linear_workspace", "headloss_fp8_linear",
+           "headloss_beam_workspace", "headloss_beam_select",
            "headloss_reorder_create", "headloss_reorder", "headloss_reorder_destroy")
 
 
@@ -175,6 +176,11 @@ def load_library(path: str = LIB_PATH):
     lib.headloss_fp8_matmul.argtypes = [vp, i64, vp, i32, vp, i64, vp, i32, i64, i64, i64, vp, i64, i32,
                                         vp, i64, vp, vp]
     lib.headloss_fp8_matmul.restype = i32
+    lib.headloss_fp8_linear_workspace.argtypes = [i64, i64, i64]
+    lib.headloss_fp8_linear_workspace.restype = i64
+    lib.headloss_fp8_linear.argtypes = [vp, i64, i32, vp, i64, vp, i32, i64, i64, i64, vp, i64, i32, vp,
+                                        i64, vp, vp]
+    lib.headloss_fp8_linear.restype = i32
     lib.headloss_beam_workspace.argtypes = [i64, i32, i64, i32, i32]
     lib.headloss_beam_workspace.restype = i64
     lib.headloss_beam_select.argtypes = [vp, i64, i32, i64, i64, i32, vp, vp, i64, i32, i32, f32, f32,
@@ -395,6 +401,20 @@ def headloss_fp8_matmul(a, lda, a_scales, a_type, b, ldb, b_scales, b_type, M, N
         int(b_type), int(M), int(N), int(K), _ptr(out), int(ldo), int(out_dtype),
         _ptr(workspace), int(workspace_bytes), _ptr(err), _stream(stream)),
         "headloss_fp8_matmul")
+
+
+def headloss_fp8_linear_workspace(M, N, K) -> int:
+    return load_library().headloss_fp8_linear_workspace(int(M), int(N), int(K))
+
+
+def headloss_fp8_linear(x, ldx, dtype, b, ldb, b_scales, b_type, M, N, K, out, ldo, out_dtype, workspace,
+                        workspace_bytes, err, stream=None) -> None:
+    """out = x . b^T with x quantised on the way (include/headloss_fp8.h); raises HeadlossError
+    on a bad status."""
+    _check(load_library().headloss_fp8_linear(
+        _ptr(x), int(ldx), int(dtype), _ptr(b), int(ldb), _ptr(b_scales), int(b_type), int(M), int(N),
+        int(K), _ptr(out), int(ldo), int(out_dtype), _ptr(workspace), int(workspace_bytes), _ptr(err),
+        _stream(stream)), "headloss_fp8_linear")
 
 
 def headloss_beam_workspace(requests, beams, V, dtype, keep) -> int:
@@ -877,13 +897,17 @@ class Fp8Head:
         out = self._out("out", out, N, self.V, dtype)
         if N == 0:
             return out
-        pitch, blocks = -(-D // 16) * 16, -(-D // 128)
-        buf = self._empty(N * (pitch + 4 * blocks), dtype=self._u8, device=self.device)
-        q = buf.data_ptr()
-        scales = q + N * pitch
-        self._quantize(hidden, HEADLOSS_E4M3, q, pitch, scales, 1)
-        self._matmul(q, pitch, scales, HEADLOSS_E4M3, self.q.data_ptr(), self.ldq, self.scales.data_ptr(),
-                     self.type, N, self.V, D, out)
+        need = self._needs.get(N)
+        if need is None:
+            need = self._needs[N] = self._lib.headloss_fp8_linear_workspace(N, self.V, D)
+        work = self._empty(max(need, 0), dtype=self._u8, device=self.device)
+        status = self._lib.headloss_fp8_linear(
+            hidden.data_ptr(), hidden.stride(0) if N > 1 else D, self._codes[hidden.dtype], self.q.data_ptr(),
+            self.ldq, self.scales.data_ptr(), self.type, N, self.V, D, out.data_ptr(),
+            out.stride(0) if N > 1 else self.V, self._codes[dtype], work.data_ptr(), need, self.err.data_ptr(),
+            _raw_stream(self.index))
+        if status:
+            _check(status, "headloss_fp8_linear")
         return out
 
     def backward(self, grad, hidden, grad_hidden=None, grad_weight=None, weight_dtype=None, stream=None):

@@ -86,6 +86,23 @@ int headloss_fp8_matmul(const void* a, int64_t lda, const float* a_scales, int a
                         void* out, int64_t ldo, int out_dtype, void* workspace,
                         int64_t workspace_bytes, int* err, void* stream);
 
+/*
+ * headloss_fp8_linear_workspace -- bytes of workspace of headloss_fp8_linear; -1 for sizes that it
+ * refuses.  Needs a device.
+ */
+int64_t headloss_fp8_linear_workspace(int64_t M, int64_t N, int64_t K);
+
+/*
+ * headloss_fp8_linear -- out = x . b^T, x (M x K of `dtype`, row i at element i * ldx) quantised to e4m3 in
+ * block 1 on the way: headloss_fp8_quantize and headloss_fp8_matmul in one call, the product's loads of b
+ * beginning while x is quantised.  The same bits as the two calls.  Arguments, checks and errors as
+ * theirs; workspace at least headloss_fp8_linear_workspace(M, N, K) bytes (never 0 for M, N > 0).
+ */
+int headloss_fp8_linear(const void* x, int64_t ldx, int dtype, const void* b, int64_t ldb,
+                        const float* b_scales, int b_type, int64_t M, int64_t N, int64_t K, void* out,
+                        int64_t ldo, int out_dtype, void* workspace, int64_t workspace_bytes, int* err,
+                        void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -59,7 +59,26 @@ def test_matmul_refuses(lib, other, status):
     assert matmul(lib, **other) == status
 
 
+def linear(lib, **other):
+    a = dict(x=A, ldx=100, dtype=1, b=A, ldb=112, b_scales=A, b_type=0, M=3, N=200, K=100, out=A, ldo=200,
+             out_dtype=1, workspace=A, bytes=1 << 20, err=A, stream=None)
+    assert set(other) <= set(a)
+    a.update(other)
+    return lib.headloss_fp8_linear(*a.values())
+
+
+@pytest.mark.parametrize("other,status", [
+    (dict(M=0), OK), (dict(N=0, x=None, b=None, workspace=None), OK), (dict(M=-1), ARG), (dict(K=0), ARG),
+    (dict(K=1 << 31, ldx=1 << 31, ldb=1 << 31), ARG), (dict(ldb=96), ARG), (dict(ldo=199), ARG), (dict(b=None), ARG),
+    (dict(b_scales=None), ARG), (dict(out=None), ARG), (dict(err=None), ARG), (dict(workspace=None), ARG),
+    (dict(bytes=64), ARG), (dict(b_type=3), ARG), (dict(out_dtype=3), DTYPE), (dict(ldb=104), ALIGN),
+    (dict(workspace=A + 8), ALIGN), (dict(out=A + 1), ALIGN)])
+def test_linear_refuses(lib, other, status):
+    assert linear(lib, **other) == status
+
+
 def test_workspace_refuses(lib):
+    assert lib.headloss_fp8_linear_workspace(1, 1, 0) == -1
     assert lib.headloss_fp8_workspace(-1, 1, 1) == -1
     assert lib.headloss_fp8_workspace(1, 1, 0) == -1
 

@@ -104,11 +104,12 @@ __global__ void __launch_bounds__(W_THREADS, 1)
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // full: a stage has its tiles, and the accumulator its block goes to was read (an arrival a warp);
+    // empty: the block's MMAs are done, so its stage is free and its sums can be read. One wait and one
+    // commit a block: each costs the issuing warp some hundred cycles of the block's 768.
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + W_BAR_OFF);
     uint64_t* empty = full + W_STAGES;
-    uint64_t* tfull = empty + W_STAGES;  // [2] a block's sums are in the accumulator
-    uint64_t* tempty = tfull + 2;        // [2] the accumulator was read (an arrival a warp)
-    uint64_t* mma_done = tempty + 2;
+    uint64_t* mma_done = empty + W_STAGES;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = warp_index(), lane = threadIdx.x & 31;
@@ -116,12 +117,8 @@ __global__ void __launch_bounds__(W_THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < W_STAGES; ++s) {
-            mbar_init(su32(&full[s]), 1);
+            mbar_init(su32(&full[s]), 1 + W_EPI_WARPS);
             mbar_init(su32(&empty[s]), 1);
-        }
-        for (int a = 0; a < 2; ++a) {
-            mbar_init(su32(&tfull[a]), 1);
-            mbar_init(su32(&tempty[a]), W_EPI_WARPS);
         }
         mbar_init(su32(mma_done), 1);
         *abort = 0;
@@ -169,8 +166,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                     const uint32_t acc = it & 1u;
                     const uint32_t a = su32(smem + s * W_STAGE_BYTES);
                     const uint64_t da = smem_desc(a), db = smem_desc(a + WA_BYTES);
-                    if (!warp_wait(su32(&full[s]), (it / W_STAGES) & 1u, abort, p.err) ||
-                        !warp_wait(su32(&tempty[acc]), ((it >> 1) & 1u) ^ 1u, abort, p.err)) {
+                    if (!warp_wait(su32(&full[s]), (it / W_STAGES) & 1u, abort, p.err)) {
                         go = false;
                         break;
                     }
@@ -179,7 +175,6 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                     for (int k = 0; k < BK / 32; ++k)  // 32 bytes of K each: two units of the descriptor's address
                         warp_mma_f8(tmem + acc * WN, da + 2 * k, db + 2 * k, p.idesc, k != 0);
                     warp_mma_commit(su32(&empty[s]));
-                    warp_mma_commit(su32(&tfull[acc]));
                 }
             }
             if (it) {  // what was issued is done before TMEM is freed
@@ -194,6 +189,10 @@ __global__ void __launch_bounds__(W_THREADS, 1)
         unsigned char* stage = smem + W_OUT_OFF + (warp - 4) * W_OUT_BYTES;
         uint32_t it = 0;
         bool go = true;
+        if (lane == 0) {  // both accumulators are free
+            mbar_arrive(su32(&full[0]));
+            mbar_arrive(su32(&full[1]));
+        }
         for (uint32_t i = blockIdx.x; go && i < items; i += gridDim.x) {
             int m, n;
             tile_at(i / p.splits, p.MT, p.NT, m, n);
@@ -215,7 +214,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                     fb = __ldg(sb + kb + 1);
                 }
                 const int acc = int(it & 1u);
-                if (!wait_phase(su32(&tfull[acc]), (it >> 1) & 1u, abort, p.err)) {
+                if (!wait_phase(su32(&empty[it % W_STAGES]), (it / W_STAGES) & 1u, abort, p.err)) {
                     go = false;
                     break;
                 }
@@ -227,13 +226,16 @@ __global__ void __launch_bounds__(W_THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     tmem_wait32(v[c & 1]);
-                    if (c < 3) tmem_ld32(t + 32 * (c + 1), v[(c + 1) & 1]);
+                    if (c < 3) {
+                        tmem_ld32(t + 32 * (c + 1), v[(c + 1) & 1]);
+                    } else {  // all is read: the accumulator is free for the block after the next
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(su32(&full[(it + 2) % W_STAGES]));
+                    }
 #pragma unroll
                     for (int j = 0; j < 32; ++j) sum[32 * c + j] = fmaf(__uint_as_float(v[c & 1][j]), s, sum[32 * c + j]);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(su32(&tempty[acc]));
             }
             if (!go) break;
             // 128 bytes of 32 rows at a time through shared memory (128-byte swizzle)
@@ -319,7 +321,6 @@ __global__ void __launch_bounds__(256) join_kernel(const float* __restrict__ par
 constexpr int N_STAGES = 4;
 constexpr int N_EPI_WARPS = 4;
 constexpr int N_THREADS = 64 + 32 * N_EPI_WARPS;
-constexpr int N_ACCS = 4;           // accumulators: blocks of K between the MMAs and the scaled sums
 constexpr int NW_BYTES = 128 * BK;  // 128 rows of b, a K block
 
 template <int NT>
@@ -328,7 +329,7 @@ struct Narrow {
     static constexpr int SCALE_OFF = N_STAGES * STAGE;          // [warp][2][NT] products of scales
     static constexpr int BAR_OFF = SCALE_OFF + N_EPI_WARPS * 2 * NT * 4;
     static constexpr int SMEM = BAR_OFF + 256 + 1024;
-    static constexpr int TMEM = N_ACCS * NT;                    // 64, 128 or 256 columns
+    static constexpr int TMEM = N_STAGES * NT;                  // an accumulator a stage: 64, 128 or 256 columns
 };
 
 struct NarrowArgs {
@@ -356,9 +357,7 @@ __global__ void __launch_bounds__(N_THREADS)
     float* scale = reinterpret_cast<float*>(smem + L::SCALE_OFF);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
     uint64_t* empty = full + N_STAGES;
-    uint64_t* tfull = empty + N_STAGES;
-    uint64_t* tempty = tfull + N_ACCS;
-    uint64_t* mma_done = tempty + N_ACCS;
+    uint64_t* mma_done = empty + N_STAGES;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = warp_index(), lane = threadIdx.x & 31;
@@ -368,12 +367,8 @@ __global__ void __launch_bounds__(N_THREADS)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < N_STAGES; ++s) {
-            mbar_init(su32(&full[s]), 1);
+            mbar_init(su32(&full[s]), 1 + N_EPI_WARPS);
             mbar_init(su32(&empty[s]), 1);
-        }
-        for (int a = 0; a < N_ACCS; ++a) {
-            mbar_init(su32(&tfull[a]), 1);
-            mbar_init(su32(&tempty[a]), N_EPI_WARPS);
         }
         mbar_init(su32(mma_done), 1);
         *abort = 0;
@@ -412,16 +407,13 @@ __global__ void __launch_bounds__(N_THREADS)
         for (int kb = k0; kb < k1; ++kb) {
             const uint32_t it = uint32_t(kb - k0);
             const int s = int(it % N_STAGES);
-            const uint32_t acc = it % N_ACCS, w = su32(smem + s * L::STAGE);
+            const uint32_t w = su32(smem + s * L::STAGE);
             const uint64_t dw = smem_desc(w), dx = smem_desc(w + NW_BYTES);
-            if (!warp_wait(su32(&full[s]), (it / N_STAGES) & 1u, abort, p.err) ||
-                !warp_wait(su32(&tempty[acc]), ((it / N_ACCS) & 1u) ^ 1u, abort, p.err))
-                break;
+            if (!warp_wait(su32(&full[s]), (it / N_STAGES) & 1u, abort, p.err)) break;
             tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < BK / 32; ++k) warp_mma_f8(tmem + acc * NT, dw + 2 * k, dx + 2 * k, p.idesc, k != 0);
+            for (int k = 0; k < BK / 32; ++k) warp_mma_f8(tmem + uint32_t(s * NT), dw + 2 * k, dx + 2 * k, p.idesc, k != 0);
             warp_mma_commit(su32(&empty[s]));
-            warp_mma_commit(su32(&tfull[acc]));
             issued = true;
         }
         if (issued) {
@@ -445,22 +437,24 @@ __global__ void __launch_bounds__(N_THREADS)
             }
         };
         if (k0 < k1) fetch(k0);
+        if (lane == 0)  // every accumulator is free
+            for (int s = 0; s < N_STAGES; ++s) mbar_arrive(su32(&full[s]));
         for (int kb = k0; kb < k1; ++kb) {
-            const uint32_t it = uint32_t(kb - k0), acc = it % N_ACCS;
+            const uint32_t it = uint32_t(kb - k0), acc = it % N_STAGES;
             float* now = mine + (it & 1u) * NT;
 #pragma unroll
             for (int j = 0; j < PER; ++j)
                 if (lane + 32 * j < NT) now[lane + 32 * j] = next[j];
             if (kb + 1 < k1) fetch(kb + 1);
             __syncwarp();
-            if (!wait_phase(su32(&tfull[acc]), (it / N_ACCS) & 1u, abort, p.err)) break;
+            if (!wait_phase(su32(&empty[acc]), (it / N_STAGES) & 1u, abort, p.err)) break;
             tc_fence_after();
             const uint32_t at = tmem + (uint32_t(32 * q) << 16) + acc * NT;
             uint32_t v[NT];
             tmem_ld_all<NT>(at, v);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(su32(&tempty[acc]));
+            if (lane == 0) mbar_arrive(su32(&full[acc]));
 #pragma unroll
             for (int j = 0; j < NT; j += 4) {
                 const float4 s = *reinterpret_cast<const float4*>(now + j);

@@ -20,11 +20,19 @@ __device__ __forceinline__ void fence_mbar_init() {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// Up to 32 tries of the phase of `parity` (each waits a little by itself).
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+        "mov.u32 n, 0;\n"
+        "AGAIN:\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE;\n\t"
+        "add.u32 n, n, 1;\n\t"
+        "setp.lt.u32 q, n, 32;\n\t"
+        "@q bra AGAIN;\n"
+        "DONE:\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(bar), "r"(parity)
@@ -37,18 +45,14 @@ __device__ __forceinline__ uint64_t gtimer() {
     return t;
 }
 // Wait for the phase of `parity`.  False, without further waiting, once the kernel is giving
-// up; after WAIT_NS it gives up itself: bit 0 of *err, and the abort flag.  The clock is read
-// every 32nd try alone: reading it takes longer than most waits.
+// up; after WAIT_NS it gives up itself: bit 0 of *err, and the abort flag.
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* abort, int* err) {
-    uint64_t t0 = 0;
-    for (uint32_t i = 1;; ++i) {
-        if (mbar_try(bar, parity)) return true;
-        if (i & 31) continue;
+    if (mbar_try(bar, parity)) return true;
+    const uint64_t t0 = gtimer();
+    for (;;) {
         if (*abort) return false;
-        const uint64_t t = gtimer();
-        if (!t0) {
-            t0 = t;
-        } else if (t - t0 > WAIT_NS) {
+        if (mbar_try(bar, parity)) return true;
+        if (gtimer() - t0 > WAIT_NS) {
             *abort = 1;
             atomicOr(err, 1);
             return false;
@@ -57,17 +61,12 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
 }
 // The same for what was issued: not ended by the abort flag, bounded by time.
 __device__ __forceinline__ void drain_phase(uint32_t bar, uint32_t parity, int* err) {
-    uint64_t t0 = 0;
-    for (uint32_t i = 1; !mbar_try(bar, parity); ++i) {
-        if (i & 31) continue;
-        const uint64_t t = gtimer();
-        if (!t0) {
-            t0 = t;
-        } else if (t - t0 > WAIT_NS) {
+    const uint64_t t0 = gtimer();
+    while (!mbar_try(bar, parity))
+        if (gtimer() - t0 > WAIT_NS) {
             atomicOr(err, 1);
             return;
         }
-    }
 }
 // A converged warp's wait, with one answer for all lanes that the compiler knows to be uniform.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, int* err) {

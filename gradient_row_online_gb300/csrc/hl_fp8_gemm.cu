@@ -7,13 +7,11 @@
 // scale is applied exactly once, in fp32, and a sum over K never lives in the accumulator for more
 // than 128 products.
 //
-// wide_kernel (more than 64 rows of a): persistent, one CTA an SM, 128 x 256 tiles of out; per K
-// block the MMAs take 512 cycles at the full rate and the scaled sums 32768 FMAs, 256 cycles of the
-// FMA pipe.  With fewer tiles than half the SMs, K is split; the parts go to the workspace in fp32
-// and a second kernel adds them in order.
-// narrow_kernel (up to 64 rows of a): b's rows are the MMA's 128 rows and a's its 16, 32 or 64
-// columns, so that b streams through once at HBM's rate.  A cluster of up to 8 CTAs splits K
-// and joins its sums over DSMEM.
+// One CTA an SM walks the 128 x 256 tiles of out. Few rows of a take the same way: a's tile is then
+// 16, 32 or 64 rows of copies, the MMAs' other rows are left as they are and never read, and b, 256 rows
+// at a time, streams through at HBM's rate. (b as the MMA's 128 rows and a as its 16 to 64 columns is
+// slower: such an MMA takes the time of 128 columns and more, and moves half the bytes of b.) With fewer
+// tiles than half the SMs, K is split; the parts go to the workspace in fp32 and a second kernel adds them in order.
 // Every wait is bounded; one that gives up sets bit 0 of *err, and the kernel drains what it issued.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -83,6 +81,8 @@ struct WideArgs {
     int64_t mpad;           // rows between two parts of the workspace
     void* out;
     int64_t ldo;
+    int a_rows;             // of a's copies
+    int early;              // b was in place before the launch in front of this one began
     int tma_out;            // rows of out start on 16-byte boundaries
     int n_even;             // and end on them
     uint32_t idesc;
@@ -95,6 +95,13 @@ __device__ __forceinline__ void tile_at(uint32_t i, uint32_t MT, uint32_t NT, in
     const uint32_t w = i - g * per, wide = min(NT - g * GN, uint32_t(GN));
     m = int(w / wide);
     n = int(g * GN + w % wide);
+}
+
+// Blocks of K of a CTA's first piece of work that fit the ring.
+__device__ __forceinline__ uint32_t first_blocks(const WideArgs& p) {
+    const int sp = int(blockIdx.x % p.splits);
+    const int n = int(int64_t(p.KB) * (sp + 1) / p.splits) - int(int64_t(p.KB) * sp / p.splits);
+    return uint32_t(min(n, W_STAGES));
 }
 
 template <int OT>
@@ -128,11 +135,12 @@ __global__ void __launch_bounds__(W_THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    grid_wait();
+    if (warp != 2) grid_wait();
 
     if (warp < 4) {
         give_registers<W_FEW_REGS>();
         if (warp == 0) {  // copies
+            const uint32_t bytes = uint32_t(p.a_rows * BK + WB_BYTES), ahead = p.early ? first_blocks(p) : 0;
             uint32_t it = 0;
             bool go = true;
             for (uint32_t i = blockIdx.x; go && i < items; i += gridDim.x) {
@@ -142,15 +150,16 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                 const int k0 = int(int64_t(p.KB) * sp / p.splits), k1 = int(int64_t(p.KB) * (sp + 1) / p.splits);
                 for (int kb = k0; kb < k1; ++kb, ++it) {
                     const int s = int(it % W_STAGES);
-                    const uint32_t ph = (it / W_STAGES) & 1u;
-                    if (!warp_wait(su32(&empty[s]), ph ^ 1u, abort, p.err)) {
-                        go = false;
-                        break;
-                    }
                     const uint32_t a = su32(smem + s * W_STAGE_BYTES), bar = su32(&full[s]);
-                    warp_expect_tx(bar, W_STAGE_BYTES);
+                    if (it >= ahead) {
+                        if (!warp_wait(su32(&empty[s]), ((it / W_STAGES) & 1u) ^ 1u, abort, p.err)) {
+                            go = false;
+                            break;
+                        }
+                        warp_expect_tx(bar, bytes);
+                        warp_tma_load_2d(a + WA_BYTES, &map_b, kb * BK, n * WN, bar);
+                    }
                     warp_tma_load_2d(a, &map_a, kb * BK, m * WM, bar);
-                    warp_tma_load_2d(a + WA_BYTES, &map_b, kb * BK, n * WN, bar);
                 }
             }
             for (uint32_t j = it > W_STAGES ? it - W_STAGES : 0; j < it; ++j)  // what was issued has landed
@@ -182,6 +191,17 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                 drain_phase(su32(mma_done), 0u, p.err);
             }
         }
+        else if (warp == 2 && p.early) {  // the first stages' rows of b, before a's quantisation is done
+            int m, n;
+            tile_at(blockIdx.x / p.splits, p.MT, p.NT, m, n);
+            const int k0 = int(int64_t(p.KB) * int(blockIdx.x % p.splits) / p.splits);
+            const uint32_t ahead = first_blocks(p);
+            for (uint32_t s = 0; s < ahead; ++s) {
+                warp_expect_tx(su32(&full[s]), uint32_t(p.a_rows * BK + WB_BYTES));
+                warp_tma_load_2d(su32(smem + s * W_STAGE_BYTES) + WA_BYTES, &map_b, (k0 + int(s)) * BK, n * WN, su32(&full[s]));
+            }
+            grid_wait();
+        }
         __syncwarp();
     } else {  // scaled sums: warp w has TMEM lanes 32 (w % 4) .., columns 128 h ..
         take_registers<W_SUM_REGS>();
@@ -201,6 +221,14 @@ __global__ void __launch_bounds__(W_THREADS, 1)
             const int64_t row = int64_t(m) * WM + 32 * q + lane;
             const int nb = min(2 * n + h, p.NB - 1);
             const bool in = row < p.M;
+            if (int64_t(m) * WM + 32 * q >= p.M) {  // this warp has no rows of out
+                for (int kb = k0; go && kb < k1; ++kb, ++it) {
+                    go = wait_phase(su32(&empty[it % W_STAGES]), (it / W_STAGES) & 1u, abort, p.err);
+                    __syncwarp();
+                    if (go && lane == 0) mbar_arrive(su32(&full[(it + 2) % W_STAGES]));
+                }
+                continue;
+            }
             const float* sa = p.a_scales + (in ? row : 0);
             const float* sb = p.b_scales + int64_t(nb) * p.KB;
             float sum[128];
@@ -316,193 +344,6 @@ __global__ void __launch_bounds__(256) join_kernel(const float* __restrict__ par
     }
 }
 
-// ---------------------------------------------------------------- narrow ----
-
-constexpr int N_STAGES = 4;
-constexpr int N_EPI_WARPS = 4;
-constexpr int N_THREADS = 64 + 32 * N_EPI_WARPS;
-constexpr int NW_BYTES = 128 * BK;  // 128 rows of b, a K block
-
-template <int NT>
-struct Narrow {
-    static constexpr int STAGE = NW_BYTES + NT * BK;
-    static constexpr int SCALE_OFF = N_STAGES * STAGE;          // [warp][2][NT] products of scales
-    static constexpr int BAR_OFF = SCALE_OFF + N_EPI_WARPS * 2 * NT * 4;
-    static constexpr int SMEM = BAR_OFF + 256 + 1024;
-    static constexpr int TMEM = N_STAGES * NT;                  // an accumulator a stage: 64, 128 or 256 columns
-};
-
-struct NarrowArgs {
-    const float* a_scales;
-    const float* b_scales;
-    int M;
-    int64_t N;
-    int KB;
-    int splits;  // the cluster
-    int early;   // b is in place before the launch before this one began
-    void* out;
-    int64_t ldo;
-    uint32_t idesc;
-    int* err;
-};
-
-template <int NT, int OT>
-__global__ void __launch_bounds__(N_THREADS)
-    narrow_kernel(const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_a,
-                  const NarrowArgs p) {
-    using L = Narrow<NT>;
-    extern __shared__ __align__(1024) unsigned char smem_raw[];
-    unsigned char* smem = reinterpret_cast<unsigned char*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float* scale = reinterpret_cast<float*>(smem + L::SCALE_OFF);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
-    uint64_t* empty = full + N_STAGES;
-    uint64_t* mma_done = empty + N_STAGES;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
-    volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    const int warp = warp_index(), lane = threadIdx.x & 31;
-    const int S = p.splits, rank = S > 1 ? int(cluster_rank()) : 0;
-    const int tile = blockIdx.x / S;
-    const int k0 = int(int64_t(p.KB) * rank / S), k1 = int(int64_t(p.KB) * (rank + 1) / S);
-
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < N_STAGES; ++s) {
-            mbar_init(su32(&full[s]), 1 + N_EPI_WARPS);
-            mbar_init(su32(&empty[s]), 1);
-        }
-        mbar_init(su32(mma_done), 1);
-        *abort = 0;
-        fence_mbar_init();
-    }
-    if (warp == 1) tmem_alloc(su32(tmem_slot), L::TMEM);
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-
-    float sum[NT];
-    if (warp == 0) {
-        // the first stages' rows of b before the wait for a's quantisation
-        const int ahead = p.early ? min(N_STAGES, k1 - k0) : 0;
-        for (int s = 0; s < ahead; ++s) {
-            warp_expect_tx(su32(&full[s]), L::STAGE);
-            warp_tma_load_2d(su32(smem + s * L::STAGE), &map_b, (k0 + s) * BK, tile * 128, su32(&full[s]));
-        }
-        grid_wait();
-        uint32_t it = 0;
-        for (int kb = k0; kb < k1; ++kb, ++it) {
-            const int s = int(it % N_STAGES);
-            const uint32_t ph = (it / N_STAGES) & 1u;
-            if (!warp_wait(su32(&empty[s]), ph ^ 1u, abort, p.err) && int(it) >= ahead) break;
-            const uint32_t w = su32(smem + s * L::STAGE), bar = su32(&full[s]);
-            if (int(it) >= ahead) {
-                warp_expect_tx(bar, L::STAGE);
-                warp_tma_load_2d(w, &map_b, kb * BK, tile * 128, bar);
-            }
-            warp_tma_load_2d(w + NW_BYTES, &map_a, kb * BK, 0, bar);
-        }
-        for (uint32_t j = it > N_STAGES ? it - N_STAGES : 0; j < it; ++j)
-            drain_phase(su32(&full[j % N_STAGES]), (j / N_STAGES) & 1u, p.err);
-    } else if (warp == 1) {
-        bool issued = false;
-        for (int kb = k0; kb < k1; ++kb) {
-            const uint32_t it = uint32_t(kb - k0);
-            const int s = int(it % N_STAGES);
-            const uint32_t w = su32(smem + s * L::STAGE);
-            const uint64_t dw = smem_desc(w), dx = smem_desc(w + NW_BYTES);
-            if (!warp_wait(su32(&full[s]), (it / N_STAGES) & 1u, abort, p.err)) break;
-            tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < BK / 32; ++k) warp_mma_f8(tmem + uint32_t(s * NT), dw + 2 * k, dx + 2 * k, p.idesc, k != 0);
-            warp_mma_commit(su32(&empty[s]));
-            issued = true;
-        }
-        if (issued) {
-            warp_mma_commit(su32(mma_done));
-            drain_phase(su32(mma_done), 0u, p.err);
-        }
-    } else {  // a thread has one row of b, every row of a
-        grid_wait();
-        const int q = warp & 3;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) sum[j] = 0.f;
-        const float* sb = p.b_scales + int64_t(tile) * p.KB;
-        float* mine = scale + (warp - 2) * 2 * NT;  // this warp's products of scales, two blocks of K
-        constexpr int PER = NT < 32 ? 1 : NT / 32;
-        float next[PER];
-        auto fetch = [&](int kb) {
-#pragma unroll
-            for (int j = 0; j < PER; ++j) {
-                const int t = lane + 32 * j;
-                next[j] = t < NT && t < p.M ? __ldg(p.a_scales + int64_t(kb) * p.M + t) * __ldg(sb + kb) : 0.f;
-            }
-        };
-        if (k0 < k1) fetch(k0);
-        if (lane == 0)  // every accumulator is free
-            for (int s = 0; s < N_STAGES; ++s) mbar_arrive(su32(&full[s]));
-        for (int kb = k0; kb < k1; ++kb) {
-            const uint32_t it = uint32_t(kb - k0), acc = it % N_STAGES;
-            float* now = mine + (it & 1u) * NT;
-#pragma unroll
-            for (int j = 0; j < PER; ++j)
-                if (lane + 32 * j < NT) now[lane + 32 * j] = next[j];
-            if (kb + 1 < k1) fetch(kb + 1);
-            __syncwarp();
-            if (!wait_phase(su32(&empty[acc]), (it / N_STAGES) & 1u, abort, p.err)) break;
-            tc_fence_after();
-            const uint32_t at = tmem + (uint32_t(32 * q) << 16) + acc * NT;
-            uint32_t v[NT];
-            tmem_ld_all<NT>(at, v);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(su32(&full[acc]));
-#pragma unroll
-            for (int j = 0; j < NT; j += 4) {
-                const float4 s = *reinterpret_cast<const float4*>(now + j);
-                sum[j] = fmaf(__uint_as_float(v[j]), s.x, sum[j]);
-                sum[j + 1] = fmaf(__uint_as_float(v[j + 1]), s.y, sum[j + 1]);
-                sum[j + 2] = fmaf(__uint_as_float(v[j + 2]), s.z, sum[j + 2]);
-                sum[j + 3] = fmaf(__uint_as_float(v[j + 3]), s.w, sum[j + 3]);
-            }
-        }
-    }
-    const int v = (warp & 3) * 32 + lane;  // the tile's row of b (epilogue warps)
-    const int64_t col = int64_t(tile) * 128 + v;
-    if (S == 1) {
-        if (warp >= 2 && col < p.N)
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-                if (j < p.M) store1<OT>(p.out, j * p.ldo + col, sum[j]);
-    } else {
-        // each CTA of the cluster gets its share of a's rows from all of them: [source][row][128]
-        const int share = NT / S;
-        __syncthreads();
-        __syncwarp();
-        cluster_sync();  // no CTA's ring is in use any more
-        if (warp >= 2)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int peer = j / share;
-                const uint32_t at = su32(smem) + uint32_t(((rank * share + j - peer * share) * 128 + v) * 4);
-                st_peer(map_peer(at, uint32_t(peer)), sum[j]);
-            }
-        cluster_sync();
-        if (warp >= 2) {
-            const float* part = reinterpret_cast<const float*>(smem);
-            for (int j = 0; j < share; ++j) {
-                float t = 0.f;
-                for (int r = 0; r < S; ++r) t += part[(r * share + j) * 128 + v];
-                const int64_t row = rank * share + j;
-                if (row < p.M && col < p.N) store1<OT>(p.out, row * p.ldo + col, t);
-            }
-        }
-    }
-    __syncthreads();
-    if (warp == 1) {
-        tc_fence_after();
-        tmem_dealloc(tmem, L::TMEM);
-    }
-}
-
 // ------------------------------------------------------------------ host ----
 
 int quantize(const void* x, int64_t rows, int64_t cols, int64_t ld, int dtype, int type, void* q, int64_t ldq,
@@ -527,7 +368,6 @@ int make_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, int64_t
 }
 
 struct Plan {
-    int narrow;    // 0, or the MMA's columns
     int splits;
     int64_t mpad, ldw, bytes;
 };
@@ -536,13 +376,6 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int sms) {
     Plan r = {};
     const int64_t KB = (K + BK - 1) / BK;
     r.splits = 1;
-    if (M <= 64) {
-        r.narrow = M <= 16 ? 16 : M <= 32 ? 32 : 64;
-        const int64_t tiles = (N + 127) / 128;
-        // CTAs enough for three an SM, each with four blocks of K at least
-        while (r.splits < 8 && tiles * r.splits < 3 * sms && KB >= 8 * r.splits) r.splits *= 2;
-        return r;
-    }
     const int64_t tiles = ((M + WM - 1) / WM) * ((N + WN - 1) / WN);
     if (2 * tiles <= sms && KB >= 8) {
         int64_t s = sms / tiles;
@@ -570,7 +403,7 @@ int sm_count(int* sms) {
 
 template <int OT>
 int launch_wide(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo, const WideArgs& a, int sms,
-                bool early, cudaStream_t s) {
+                cudaStream_t s) {
     const void* fn = reinterpret_cast<const void*>(&wide_kernel<OT>);
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, W_SMEM) != cudaSuccess)
         return HEADLOSS_ERR_CUDA;
@@ -584,36 +417,8 @@ int launch_wide(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap&
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = early ? 1 : 0;
+    cfg.numAttrs = a.early ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, wide_kernel<OT>, ma, mb, mo, a) == cudaSuccess ? HEADLOSS_OK : HEADLOSS_ERR_CUDA;
-}
-
-template <int NT, int OT>
-int launch_narrow(const CUtensorMap& mb, const CUtensorMap& ma, const NarrowArgs& a, cudaStream_t s) {
-    const void* fn = reinterpret_cast<const void*>(&narrow_kernel<NT, OT>);
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Narrow<NT>::SMEM) != cudaSuccess)
-        return HEADLOSS_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned((a.N + 127) / 128 * a.splits));
-    cfg.blockDim = dim3(N_THREADS);
-    cfg.dynamicSmemBytes = Narrow<NT>::SMEM;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = unsigned(a.splits);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = a.early ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, narrow_kernel<NT, OT>, mb, ma, a) == cudaSuccess ? HEADLOSS_OK
-                                                                                    : HEADLOSS_ERR_CUDA;
-}
-template <int NT>
-int launch_narrow_as(int ot, const CUtensorMap& mb, const CUtensorMap& ma, const NarrowArgs& a, cudaStream_t s) {
-    return ot == HEADLOSS_FP32   ? launch_narrow<NT, HEADLOSS_FP32>(mb, ma, a, s)
-           : ot == HEADLOSS_BF16 ? launch_narrow<NT, HEADLOSS_BF16>(mb, ma, a, s)
-                                 : launch_narrow<NT, HEADLOSS_FP16>(mb, ma, a, s);
 }
 
 }  // namespace hl_fp8
@@ -652,25 +457,6 @@ int matmul(const void* a, int64_t lda, const float* a_scales, int a_type, const 
     const int KB = int((K + BK - 1) / BK);
     CUtensorMap ma, mb, mo;
     const auto U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-    if (plan.narrow) {
-        if (make_map(&mb, U8, b, N, K, ldb, 128, BK) || make_map(&ma, U8, a, M, K, lda, plan.narrow, BK))
-            return HEADLOSS_ERR_CUDA;
-        NarrowArgs n = {};
-        n.a_scales = a_scales;
-        n.b_scales = b_scales;
-        n.M = int(M);
-        n.N = N;
-        n.KB = KB;
-        n.splits = plan.splits;
-        n.early = early;
-        n.out = out;
-        n.ldo = ldo;
-        n.idesc = idesc_of(128, plan.narrow, b_type, a_type);
-        n.err = err;
-        return plan.narrow == 16   ? launch_narrow_as<16>(out_dtype, mb, ma, n, s)
-               : plan.narrow == 32 ? launch_narrow_as<32>(out_dtype, mb, ma, n, s)
-                                   : launch_narrow_as<64>(out_dtype, mb, ma, n, s);
-    }
     WideArgs w = {};
     w.a_scales = a_scales;
     w.b_scales = b_scales;
@@ -686,15 +472,17 @@ int matmul(const void* a, int64_t lda, const float* a_scales, int a_type, const 
     w.ldo = ldo;
     w.tma_out = !(bits(out) & 15) && !((ldo * size) & 15);
     w.n_even = !((N * size) & 15);
+    w.a_rows = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : WM;
+    w.early = early;
     w.idesc = idesc_of(WM, WN, a_type, b_type);
     w.err = err;
-    if (make_map(&ma, U8, a, M, K, lda, WM, BK) || make_map(&mb, U8, b, N, K, ldb, WN, BK))
+    if (make_map(&ma, U8, a, M, K, lda, w.a_rows, BK) || make_map(&mb, U8, b, N, K, ldb, WN, BK))
         return HEADLOSS_ERR_CUDA;
     if (plan.splits > 1) {
         w.tma_out = w.n_even = 1;
         if (make_map(&mo, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, workspace, plan.splits * plan.mpad, plan.ldw, plan.ldw * 4, 32, 32))
             return HEADLOSS_ERR_CUDA;
-        const int rc = launch_wide<HEADLOSS_FP32>(ma, mb, mo, w, sms, early, s);
+        const int rc = launch_wide<HEADLOSS_FP32>(ma, mb, mo, w, sms, s);
         if (rc != HEADLOSS_OK) return rc;
         const int64_t words = M * (plan.ldw / 4);
         const int grid = int((words + 255) / 256 < 8 * sms ? (words + 255) / 256 : 8 * sms);
@@ -715,9 +503,9 @@ int matmul(const void* a, int64_t lda, const float* a_scales, int a_type, const 
     } else {
         mo = ma;  // not used
     }
-    return out_dtype == HEADLOSS_FP32   ? launch_wide<HEADLOSS_FP32>(ma, mb, mo, w, sms, early, s)
-           : out_dtype == HEADLOSS_BF16 ? launch_wide<HEADLOSS_BF16>(ma, mb, mo, w, sms, early, s)
-                                        : launch_wide<HEADLOSS_FP16>(ma, mb, mo, w, sms, early, s);
+    return out_dtype == HEADLOSS_FP32   ? launch_wide<HEADLOSS_FP32>(ma, mb, mo, w, sms, s)
+           : out_dtype == HEADLOSS_BF16 ? launch_wide<HEADLOSS_BF16>(ma, mb, mo, w, sms, s)
+                                        : launch_wide<HEADLOSS_FP16>(ma, mb, mo, w, sms, s);
 }
 
 }  // namespace hl_fp8

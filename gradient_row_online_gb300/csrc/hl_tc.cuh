@@ -150,7 +150,7 @@ __device__ __forceinline__ void warp_mma_commit(uint32_t bar) {
         "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
         : "memory");
 }
-// 32 lanes x 32 (16) columns of fp32: thread t gets lane (base lane + t). The registers are not to be
+// 32 lanes x 32 columns of fp32: thread t gets lane (base lane + t). The registers are not to be
 // read before the wait, which names them for that reason.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
@@ -164,42 +164,6 @@ __device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
                  :
                  : "memory");
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                 : "r"(taddr)
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :
-                 : "memory");
-}
-
-// All of NT columns, waited for once.
-template <int NT>
-__device__ __forceinline__ void tmem_ld_all(uint32_t taddr, uint32_t (&r)[NT]);
-template <>
-__device__ __forceinline__ void tmem_ld_all<16>(uint32_t taddr, uint32_t (&r)[16]) {
-    tmem_ld16(taddr, r);
-    tmem_wait16(r);
-}
-template <>
-__device__ __forceinline__ void tmem_ld_all<32>(uint32_t taddr, uint32_t (&r)[32]) {
-    tmem_ld32(taddr, r);
-    tmem_wait32(r);
-}
-template <>
-__device__ __forceinline__ void tmem_ld_all<64>(uint32_t taddr, uint32_t (&r)[64]) {
-    uint32_t(&lo)[32] = *reinterpret_cast<uint32_t(*)[32]>(&r[0]);
-    uint32_t(&hi)[32] = *reinterpret_cast<uint32_t(*)[32]>(&r[32]);
-    tmem_ld32(taddr, lo);
-    tmem_ld32(taddr + 32, hi);
-    tmem_wait32(lo);
-    tmem_wait32(hi);
-}
-
 // A warpgroup's registers a thread, less or more than at launch; what is taken was given up
 // by another of the same block.
 template <int N>
@@ -212,23 +176,6 @@ __device__ __forceinline__ void take_registers() {
 }
 // The launch in front of this one has completed, where this one was let in before.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t map_peer(uint32_t addr, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ void st_peer(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
 
 inline PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
     static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {

@@ -1,10 +1,11 @@
 // hl_beam.cu -- headloss_beam_select (include/headloss_beam.h).
 //
-// slice_kernel: a row's 16-byte words are split into slices of up to 2048, a CTA each, which it holds
-// in registers (eight words a thread, all in flight at once): one read of the logits. The slice's
-// largest logit and a bound for its candidates come from the maxima of groups of threads: the
-// keep-th largest of them has at least `keep` logits at or above it, and hardly more. The sum of
-// exponentials follows in fp32; the few logits at the bound and above go to the workspace.
+// slice_kernel: a row is split into slices, a CTA each, as far as the rows alone do not fill the GPU. A
+// slice goes in batches of 2048 16-byte words through registers (eight a thread, all in flight at once):
+// one read of the logits. A bound for its candidates comes from the first batch's maxima of groups of
+// threads: the keep-th largest of them has at least `keep` logits at or above it, and hardly more.
+// The words at the bound and above are listed, and the list raises the bound as it grows; the
+// exponentials are added in fp32 on the way. The candidates go to the workspace.
 // merge_kernel: a CTA a request joins the beams' sums and takes the candidates of all slices in two
 // steps: fp32 scores with a bound of their error leave hardly more than `keep`, which are scored in
 // fp64 and ranked. So the order between beams does not hang on fp32 rounding of the scores.
@@ -137,20 +138,29 @@ struct Words {
         if (DT == HEADLOSS_BF16) return (__float_as_uint(v) >> 16) * 0x10001u;
         return uint32_t(__half_as_ushort(__float2half_rz(v))) * 0x10001u;
     }
-    // whether every magnitude of a word is at most `most` (a NaN is not)
-    static __device__ __forceinline__ bool within(const uint32_t (&w)[4], uint32_t most) {
+    // a value in both halves, rounded upwards (past the largest: infinity)
+    static __device__ __forceinline__ uint32_t packed_up(float v) {
+        if (DT == HEADLOSS_FP32) return __float_as_uint(v);
+        if (DT == HEADLOSS_BF16) return uint32_t(__bfloat16_as_ushort(__float2bfloat16_ru(v))) * 0x10001u;
+        return uint32_t(__half_as_ushort(__float2half_ru(v))) * 0x10001u;
+    }
+    // whether every magnitude of two words is at most `most` (a NaN may hide behind a number)
+    static __device__ __forceinline__ bool within(const uint32_t (&v)[4], const uint32_t (&w)[4], uint32_t most) {
         if (DT == HEADLOSS_FP32) {
-            const float m = __uint_as_float(most);
-            return fabsf(__uint_as_float(w[0])) <= m && fabsf(__uint_as_float(w[1])) <= m &&
-                   fabsf(__uint_as_float(w[2])) <= m && fabsf(__uint_as_float(w[3])) <= m;
+            float m = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) m = fmaxf(m, fmaxf(fabsf(__uint_as_float(v[k])), fabsf(__uint_as_float(w[k]))));
+            return m <= __uint_as_float(most);
         }
         if (DT == HEADLOSS_BF16) {
             using P = hl::Pack16<__nv_bfloat16>;
-            const uint32_t m = P::absmax2(P::absmax2(w[0], w[1]), P::absmax2(w[2], w[3])) & 0x7fff7fffu;
+            const uint32_t m = P::absmax2(P::absmax2(P::absmax2(v[0], v[1]), P::absmax2(v[2], v[3])),
+                                          P::absmax2(P::absmax2(w[0], w[1]), P::absmax2(w[2], w[3]))) & 0x7fff7fffu;
             return __hble2(*reinterpret_cast<const __nv_bfloat162*>(&m), *reinterpret_cast<const __nv_bfloat162*>(&most));
         }
         using P = hl::Pack16<__half>;
-        const uint32_t m = P::absmax2(P::absmax2(w[0], w[1]), P::absmax2(w[2], w[3])) & 0x7fff7fffu;
+        const uint32_t m = P::absmax2(P::absmax2(P::absmax2(v[0], v[1]), P::absmax2(v[2], v[3])),
+                                      P::absmax2(P::absmax2(w[0], w[1]), P::absmax2(w[2], w[3]))) & 0x7fff7fffu;
         return __hble2(*reinterpret_cast<const __half2*>(&m), *reinterpret_cast<const __half2*>(&most));
     }
     // whether a value (of two) is `least` or more, and not -inf
@@ -161,7 +171,7 @@ struct Words {
             return !__hblt2(*reinterpret_cast<const __nv_bfloat162*>(&t), *reinterpret_cast<const __nv_bfloat162*>(&least));
         return !__hblt2(*reinterpret_cast<const __half2*>(&t), *reinterpret_cast<const __half2*>(&least));
     }
-    static __device__ __forceinline__ void unpack(const uint32_t (&w)[4], hl::f2 (&x)[PER / 2]) {
+    static __device__ __forceinline__ void unpack(const uint32_t (&w)[4], hl::f2* x) {
         if (DT == HEADLOSS_FP32) {
             x[0] = hl::pk(__uint_as_float(w[0]), __uint_as_float(w[1]));
             x[1] = hl::pk(__uint_as_float(w[2]), __uint_as_float(w[3]));
@@ -204,16 +214,20 @@ __device__ __forceinline__ hl::f2 mass_near(const hl::f2 (&x)[N], hl::f2 minus_z
     return s;
 }
 
-constexpr int HITS = 256;  // words with a candidate that a slice lists
+constexpr int HITS = ST;      // words with a candidate that a slice lists
+constexpr int MANY = 48;      // so many are thinned out before their logits are looked at
+constexpr float FAR = 64.f;   // octaves above a thread's shift at which it is raised
+constexpr int RING = 2 * SLICE_WORDS * 16;
 
 template <int DT, bool CAP>
-__global__ void __launch_bounds__(ST, 4) slice_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(ST, 3) slice_kernel(const __grid_constant__ Args a) {
     using W = Words<DT>;
+    extern __shared__ __align__(16) uint4 ring[];  // two batches
     __shared__ __align__(16) uint4 hit[HITS];
     __shared__ int hit_at[HITS];  // the word's place, and whether its sum went through mass_any
-    __shared__ float tops[ST];
-    __shared__ float part[ST / 32];
-    __shared__ int hits, count, found[ST / 32];
+    __shared__ __align__(16) float tops[ST];
+    __shared__ float part[ST / 32], shift[ST / 32];
+    __shared__ int more_hits[3], count, found[ST / 32];
     __shared__ float bound_at;
     asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -227,35 +241,31 @@ __global__ void __launch_bounds__(ST, 4) slice_kernel(const __grid_constant__ Ar
     const int off = int(reinterpret_cast<uintptr_t>(base) & 15) / W::SIZE;  // elements of the first word before the row
     const int words = (off + a.V + W::PER - 1) / W::PER;
     const int j0 = int(int64_t(words) * slice / a.slices), j1 = int(int64_t(words) * (slice + 1) / a.slices);
-    if (tid == 0) hits = count = 0;
+    if (tid == 0) more_hits[0] = more_hits[1] = more_hits[2] = count = 0;
+    int hits = 0;  // listed words
 
-    uint32_t w[WORDS][4], wt[WORDS];
-    const bool inside = j0 * W::PER >= off && j1 * W::PER - off <= a.V;  // no word is shared with a neighbour
-    const char* at = base + (int64_t(j0 + tid) * W::PER - off) * W::SIZE;
-#pragma unroll
-    for (int i = 0; i < WORDS; ++i) {
-        const int j = j0 + i * ST + tid;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) w[i][k] = W::NONE;
-        if (j < j1) {
-            const int lo = j * W::PER - off;
-            if (inside || (lo >= 0 && lo + W::PER <= a.V)) {
-                const uint4 u = __ldg(reinterpret_cast<const uint4*>(at + i * ST * 16));
-                w[i][0] = u.x, w[i][1] = u.y, w[i][2] = u.z, w[i][3] = u.w;
-            } else {
-                W::edge(base, lo, a.V, w[i]);
-            }
+    // the n-th largest of the threads' values, for all threads
+    auto nth = [&](float mine, int n) {
+        tops[tid] = mine;
+        __syncthreads();
+        int rank = 0;
+        for (int k = 0; k < ST; k += 4) {
+            const float4 u = *reinterpret_cast<const float4*>(&tops[k]);
+            rank += (u.x > mine || (u.x == mine && k < tid)) + (u.y > mine || (u.y == mine && k + 1 < tid)) +
+                    (u.z > mine || (u.z == mine && k + 2 < tid)) + (u.w > mine || (u.w == mine && k + 3 < tid));
         }
-    }
-    uint32_t all = W::NONE;
-#pragma unroll
-    for (int i = 0; i < WORDS; ++i) {  // (a NaN loses every comparison)
-        wt[i] = W::top2(W::top2(w[i][0], w[i][1]), W::top2(W::top2(w[i][2], w[i][3]), W::NONE));
-        all = W::top2(all, wt[i]);
-    }
-    const float mine = W::top_of(all);
-    float top, bound;
-    if (a.keep <= 16) {  // the maxima of 32 groups of eight threads, sorted by every warp
+        if (rank == n - 1) bound_at = mine;
+        __syncthreads();
+        return bound_at;
+    };
+    // A logit that `keep` of this batch's are not below: the keep-th largest of the maxima of 32 groups of
+    // eight threads, sorted by every warp, or of the threads'. And the largest.
+    auto batch_bound = [&](float mine, float& largest) {
+        if (a.keep > 16) {
+            const float r = nth(mine, a.keep);
+            largest = nth(mine, 1);
+            return r;
+        }
         float v = mine;
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -270,69 +280,225 @@ __global__ void __launch_bounds__(ST, 4) slice_kernel(const __grid_constant__ Ar
                 const bool larger = ((lane & o) == 0) == ((lane & k) == 0);  // falling where the k bit is clear
                 v = larger ? fmaxf(v, u) : fminf(v, u);
             }
-        top = __shfl_sync(0xffffffffu, v, 0);
-        bound = __shfl_sync(0xffffffffu, v, a.keep - 1);
-    } else {  // the threads' maxima, ranked
-        tops[tid] = mine;
-        __syncthreads();
-        int rank = 0;
-        top = NEG;
-        for (int k = 0; k < ST; ++k) {
-            const float u = tops[k];
-            top = fmaxf(top, u);
-            rank += u > mine || (u == mine && k < tid);
+        largest = __shfl_sync(0xffffffffu, v, 0);
+        return __shfl_sync(0xffffffffu, v, a.keep - 1);
+    };
+
+    float top = NEG, bound = NEG;  // of this thread; of the CTA
+    // What a thread takes off its exponents: the first batch's largest, raised where one lies far above.
+    float zt = NEG;
+    uint32_t far2 = 0;
+    hl::f2 s2 = 0ull;
+    bool crowded = false;
+    const hl::f2 K2 = hl::pk1(a.K);
+    const uint32_t near2 = CAP ? W::packed(a.near) : 0u;
+    // at this logit (not below the bound) a shift is raised; none is where the cap keeps all within range
+    auto far_of = [&](float x) { return W::packed_up(CAP && 2.f * a.cap_K < FAR ? INFINITY : x + FAR / a.K); };
+    auto z_of = [&](float x) { return CAP ? a.cap_K * tanhf(x * a.inv_cap) : x * a.K; };
+    // Each thread copies and reads its own words, so that its own wait is all the copies need.
+    auto fetch = [&](int jb, int stage) {
+        const int je = min(j1, jb + SLICE_WORDS);
+        const bool inside = jb * W::PER >= off && je * W::PER - off <= a.V;  // no word is shared with a neighbour
+        const char* at = base + (int64_t(jb + tid) * W::PER - off) * W::SIZE;
+        const uint32_t own = uint32_t(__cvta_generic_to_shared(&ring[stage * WORDS * ST + tid]));
+        if (inside && jb + SLICE_WORDS == je) {
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(own + i * ST * 16), "l"(at + i * ST * 16)
+                             : "memory");
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            return;
         }
-        if (rank == a.keep - 1) bound_at = mine;
+#pragma unroll 1
+        for (int i = 0; i < WORDS; ++i) {
+            const int j = jb + i * ST + tid;
+            if (j < je) {
+                const int lo = j * W::PER - off;
+                uint4* to = &ring[(stage * WORDS + i) * ST + tid];
+                if (inside || (lo >= 0 && lo + W::PER <= a.V)) {
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(uint32_t(__cvta_generic_to_shared(to))),
+                                 "l"(at + i * ST * 16)
+                                 : "memory");
+                } else {
+                    uint32_t w[4] = {W::NONE, W::NONE, W::NONE, W::NONE};
+                    W::edge(base, lo, a.V, w);
+                    *to = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            } else if (j < je + 2 * ST) {
+                ring[(stage * WORDS + i) * ST + tid] = make_uint4(W::NONE, W::NONE, W::NONE, W::NONE);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if (j0 < j1) fetch(j0, 0);
+    int stage = 0, turn = 0;
+#pragma unroll 1
+    for (int jb = j0; jb < j1 && !crowded; jb += SLICE_WORDS, stage ^= 1) {
+        const int je = min(j1, jb + SLICE_WORDS);
+        if (je < j1) {
+            fetch(je, stage ^ 1);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+        }
+        const int pairs = (je - jb + 2 * ST - 1) / (2 * ST);  // of words a thread
+        auto word = [&](int i, uint32_t (&w)[4]) {
+            const uint4 u = ring[(stage * WORDS + i) * ST + tid];
+            w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+        };
+        // (a NaN loses every comparison; of a word of NaNs alone it stays, and reaches any bound)
+        auto word_top = [&](const uint32_t (&w)[4]) { return W::top2(W::top2(w[0], w[1]), W::top2(w[2], w[3])); };
+        if (!(zt > NEG)) {  // nothing was allowed so far
+            uint32_t t = W::NONE;
+#pragma unroll 2
+            for (int i = 0; i < 2 * pairs; ++i) {
+                uint32_t w[4];
+                word(i, w);
+                t = W::top2(t, word_top(w));
+            }
+            float largest;
+            bound = batch_bound(W::top_of(t), largest);
+            __syncthreads();
+            if (!(largest > NEG)) continue;
+            zt = z_of(largest);
+            if (!(zt > NEG)) zt = -3e38f;  // (the sum is taken again below)
+            far2 = far_of(largest);
+        }
+        // three counters in turn: one barrier a batch stands between a counter's pushes, reads and reset
+        int* pushed = &more_hits[turn];
+        turn = turn == 2 ? 0 : turn + 1;
+        uint32_t bound2 = W::packed(bound), all = W::NONE;  // (exact: the bound is a logit)
+#pragma unroll 2
+        for (int i = 0; i < 2 * pairs; i += 2) {
+            uint32_t w[2][4];
+            word(i, w[0]);
+            word(i + 1, w[1]);
+            const uint32_t t0 = word_top(w[0]), t1 = word_top(w[1]), t = W::top2(t0, t1);
+            all = W::top2(all, t);
+            int any = 0;
+            if (CAP) any = !__all_sync(0xffffffffu, W::within(w[0], w[1], near2));
+            // the words with a candidate go to a list, so that the code for them exists once
+            if (W::reaches(t, bound2)) {
+                const float x = W::top_of(t);
+                if (W::reaches(t, far2) && x > NEG) {  // (not a NaN)
+                    const float z = z_of(x);
+                    s2 = hl::mul2(s2, hl::pk1(hl::ex2f(zt - z)));
+                    zt = z;
+                    far2 = far_of(x);
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    if (W::reaches(k ? t1 : t0, bound2)) {
+                        const int p = hits + atomicAdd(pushed, 1);
+                        if (p < HITS) {
+                            hit[p] = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+                            hit_at[p] = (jb + (i + k) * ST + tid) * 2 | any;
+                        }
+                    }
+            }
+            hl::f2 x[W::PER];
+            W::unpack(w[0], x);
+            W::unpack(w[1], x + W::PER / 2);
+            if (CAP && any) {
+                float s = 0.f;
+#pragma unroll
+                for (int e = 0; e < W::PER; ++e) {
+                    float lo, hi;
+                    hl::upk(x[e], lo, hi);
+                    s += mass_any(lo, zt, a) + mass_any(hi, zt, a);
+                }
+                s2 = hl::add2(s2, hl::pk(s, 0.f));
+            } else if (CAP) {
+                s2 = hl::add2(s2, mass_near(x, hl::pk1(-zt), a));
+            } else {
+                const hl::f2 minus_zt = hl::pk1(-zt);
+#pragma unroll
+                for (int e = 0; e < W::PER; ++e) s2 = hl::add2(s2, hl::ex2p(hl::fma2(x[e], K2, minus_zt)));
+            }
+        }
+        top = fmaxf(top, W::top_of(all));
         __syncthreads();
-        bound = bound_at;
+        int listed = hits + *pushed;
+        if (tid == 0) more_hits[turn == 2 ? 0 : turn + 1] = 0;
+        if (listed > HITS) {  // more than fit (a row that rises): once more with this batch's own bound
+            float largest;
+            bound = fmaxf(bound, batch_bound(W::top_of(all), largest));
+            __syncthreads();
+            if (tid == 0) *pushed = 0;
+            __syncthreads();
+            bound2 = W::packed(bound);
+#pragma unroll 1
+            for (int i = 0; i < 2 * pairs; ++i) {
+                uint32_t w[4];
+                word(i, w);
+                if (W::reaches(word_top(w), bound2)) {
+                    const int p = hits + atomicAdd(pushed, 1);
+                    if (p < HITS) {
+                        hit[p] = make_uint4(w[0], w[1], w[2], w[3]);
+                        hit_at[p] = (jb + i * ST + tid) * 2 | 1;
+                    }
+                }
+            }
+            __syncthreads();
+            listed = hits + *pushed;
+            crowded = listed > HITS;
+            __syncthreads();
+        }
+        hits = listed;
+        // The list thinned out, before it is full and at the end: the keep-th largest of its words' maxima is
+        // a bound too.
+        if (hits > (je < j1 ? HITS / 2 : MANY) && hits > a.keep && !crowded) {
+            uint4 h = make_uint4(W::NONE, W::NONE, W::NONE, W::NONE);
+            int h_at = 0;
+            const int e = (tid & 7) * 32 + tid / 8;  // the groups of eight threads share the list evenly
+            if (e < hits) h = hit[e], h_at = hit_at[e];
+            const float u = W::top_of(W::top2(W::top2(h.x, h.y), W::top2(W::top2(h.z, h.w), W::NONE)));
+            if (tid == 0) count = 0;
+            float largest;
+            bound = fmaxf(bound, batch_bound(u, largest));
+            __syncthreads();
+            if (u >= bound && u > NEG) {
+                const int p = atomicAdd(&count, 1);
+                hit[p] = h;
+                hit_at[p] = h_at;
+            }
+            __syncthreads();
+            hits = count;
+            __syncthreads();
+            if (tid == 0) count = 0;
+        }
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    // the slice's largest logit, and its sum: of each warp and its shift
+    float sum = hl::hsum(s2), zw = zt;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) zw = fmaxf(zw, __shfl_xor_sync(0xffffffffu, zw, o));
+    sum = zt > NEG ? sum * hl::ex2f(zt - zw) : 0.f;  // (each thread's is its own)
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    }
+    if (lane == 0) part[warp] = sum, shift[warp] = zw, tops[warp] = top;
+    __syncthreads();
+    top = NEG;
+#pragma unroll
+    for (int k = 0; k < ST / 32; ++k) top = fmaxf(top, tops[k]);
     if (top == NEG) {  // nothing is allowed here
         if (tid == 0) *head = Head{NEG, 0.f, 0, 0};
         return;
     }
-    // The words with a candidate go to shared memory, so that the code for them exists once.
-    uint32_t through_any = 0;  // of this thread's words
-    float sum;
-    hl::f2 s2 = 0ull;
-    // what is taken off the exponents: of the largest logit, rounded
-    const float zt = CAP ? a.cap_K * tanhf(top * a.inv_cap) : top * a.K;
-    const hl::f2 minus_zt = hl::pk1(-zt), K2 = hl::pk1(a.K);
-    const uint32_t near2 = CAP ? W::packed(a.near) : 0u, bound2 = W::packed(bound);  // (exact: the bound is a logit)
+    zt = CAP ? a.cap_K * tanhf(top * a.inv_cap) : top * a.K;
+    sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < WORDS; ++i) {
-        hl::f2 x[W::PER / 2];
-        W::unpack(w[i], x);
-        if (CAP && !__all_sync(0xffffffffu, W::within(w[i], near2))) {
-            float s = 0.f;
-#pragma unroll
-            for (int e = 0; e < W::PER / 2; ++e) {
-                float lo, hi;
-                hl::upk(x[e], lo, hi);
-                s += mass_any(lo, zt, a) + mass_any(hi, zt, a);
-            }
-            s2 = hl::add2(s2, hl::pk(s, 0.f));
-            through_any |= 1u << i;
-        } else if (CAP) {
-            s2 = hl::add2(s2, mass_near(x, minus_zt, a));
-        } else {
-#pragma unroll
-            for (int e = 0; e < W::PER / 2; ++e) s2 = hl::add2(s2, hl::ex2p(hl::fma2(x[e], K2, minus_zt)));
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < WORDS; ++i)
-        if (W::reaches(wt[i], bound2)) {
-            const int p = atomicAdd(&hits, 1);
-            if (p < HITS) {
-                hit[p] = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
-                hit_at[p] = (j0 + i * ST + tid) * 2 | int(through_any >> i & 1u);
-            }
-        }
-    sum = hl::hsum(s2);
-    __syncthreads();
-    const bool crowded = hits > HITS;
+    for (int k = 0; k < ST / 32; ++k)
+        if (shift[k] > NEG) sum += part[k] * hl::ex2f(shift[k] - zt);
+    // 2^(top K - zt) is taken off again: zt was rounded
+    if (!CAP) sum *= hl::ex2f(-fmaf(top, a.K, -zt));
+    float more = 0.f;
     if (!crowded) {
-        for (int k = tid; k < hits * W::PER; k += ST) {
+        const int n = hits;
+        for (int k = tid; k < n * W::PER; k += ST) {
             const int h = k / W::PER, e = k % W::PER;
             const float x = W::value(reinterpret_cast<const char*>(&hit[h]), e);
             if (x >= bound && x > NEG) {
@@ -342,25 +508,39 @@ __global__ void __launch_bounds__(ST, 4) slice_kernel(const __grid_constant__ Ar
                     // the candidates have most of the mass: theirs enters more exactly, relative to the
                     // largest logit's own z
                     const hl::f2 one[1] = {hl::pk1(x)};
-                    const float had = hit_at[h] & 1 ? mass_any(x, zt, a) : hl::lo_of(mass_near(one, minus_zt, a));
-                    sum += exp2f(fall(x, top, a.cap, a.inv_cap) * a.K) - had;
+                    const float went = hit_at[h] & 1 ? mass_any(x, zt, a) : hl::lo_of(mass_near(one, hl::pk1(-zt), a));
+                    more += exp2f(fall(x, top, a.cap, a.inv_cap) * a.K) - went;
                 }
             }
         }
     }
+    if (CAP) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) part[warp] = sum;
+        for (int o = 16; o; o >>= 1) more += __shfl_xor_sync(0xffffffffu, more, o);
+        __syncthreads();
+        if (lane == 0) part[warp] = more;
+    }
     __syncthreads();
-    sum = 0.f;
+    if (CAP) {
 #pragma unroll
-    for (int k = 0; k < ST / 32; ++k) sum += part[k];
-    // 2^(top K - zt) is taken off again: zt was rounded
-    if (!CAP) sum *= hl::ex2f(-fmaf(top, a.K, -zt));
+        for (int k = 0; k < ST / 32; ++k) sum += part[k];
+    }
     int n = count;
     const int e0 = max(0, j0 * W::PER - off), e1 = min(a.V, j1 * W::PER - off);
-    if (!(sum > 0.5f && sum < INFINITY)) {  // a NaN, an infinity, zt beyond fp32: from memory, one by one
+    if (crowded || !(sum > 0.5f && sum < INFINITY)) {  // not all was summed; a NaN, an infinity, zt beyond fp32
         float s = 0.f;
+#pragma unroll 1
+        for (int e = e0 + tid; e < e1; e += ST) {
+            const float x = W::value(base, e);
+            if (x > NEG) top = fmaxf(top, x);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        __syncthreads();
+        if (lane == 0) tops[warp] = top;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < ST / 32; ++k) top = fmaxf(top, tops[k]);
 #pragma unroll 1
         for (int e = e0 + tid; e < e1; e += ST) {
             const float x = W::value(base, e);
@@ -475,26 +655,32 @@ __global__ void __launch_bounds__(MT) merge_kernel(const Args a) {
             for (int k = lane; k < S; k += 32) top = fmaxf(top, heads[b * S + k].top);
 #pragma unroll
             for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            double total = 0.0;
+            float total = 0.f;
             if (top > NEG)
                 for (int k = lane; k < S; k += 32) {
                     const Head h = heads[b * S + k];
-                    if (h.top > NEG) total += double(h.sum * exp2f(fall(h.top, top, a.cap, a.inv_cap) * a.K));
+                    if (h.top > NEG) total += h.sum * exp2f(fall(h.top, top, a.cap, a.inv_cap) * a.K);
                 }
 #pragma unroll
             for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
             if (lane == 0) {
                 kind[b] = top > NEG;
                 top_of[b] = top;
-                log_mass[b] = log(total);
-                log_of[b] = float(log_mass[b]);
-                if (a.cap > 0.f) tanh_top[b] = tanh(double(top) / a.cap);
+                log_of[b] = total;
             }
         } else if (lane == 0) {
             kind[b] = live ? 2 : 0;
         }
         if (lane == 0) before_of[b] = double(s);
     }
+    __syncthreads();
+    // fp64 takes as long for one lane as for a warp: a lane a beam
+    if (tid < B && kind[tid] == 1) {
+        log_mass[tid] = log(double(log_of[tid]));
+        log_of[tid] = float(log_mass[tid]);
+    }
+    if (a.cap > 0.f && tid >= MAX_BEAMS && tid < MAX_BEAMS + B && kind[tid - MAX_BEAMS] == 1)
+        tanh_top[tid - MAX_BEAMS] = tanh(double(top_of[tid - MAX_BEAMS]) / a.cap);
     __syncthreads();
 
     // An entry's score in fp64, and in fp32 with a bound of its error.
@@ -693,6 +879,8 @@ __global__ void __launch_bounds__(MT) merge_kernel(const Args a) {
 
 // ------------------------------------------------------------------ host ----
 
+constexpr int64_t FILL = 900;  // CTAs: about three an SM, twice
+
 struct Plan {
     int slices, cap_list;
     int64_t heads, bytes;
@@ -701,7 +889,10 @@ Plan plan_of(int64_t requests, int beams, int64_t V, int dtype, int keep) {
     Plan p;
     const int per = dtype == HEADLOSS_FP32 ? 4 : 8;
     const int64_t words = (V + per - 1 + per - 1) / per;  // of a row that starts anywhere in a word
-    p.slices = int((words + SLICE_WORDS - 1) / SLICE_WORDS);
+    // batches of a row on CTAs of their own until those would fill three a SM twice
+    const int64_t batches = (words + SLICE_WORDS - 1) / SLICE_WORDS, rows = requests * beams > 0 ? requests * beams : 1;
+    const int64_t most = (FILL + rows - 1) / rows;
+    p.slices = int(batches < most ? batches : most);
     p.cap_list = keep <= 16 ? 64 : 4 * keep;
     const int64_t n = requests * beams * p.slices;
     p.heads = n * int64_t(sizeof(Head));
@@ -713,10 +904,16 @@ bool sizes_ok(int64_t requests, int beams, int64_t V, int keep) {
            keep <= MAX_KEEP && V >= 1 && V < (int64_t(1) << 31) - 4096 && requests * beams <= INT32_MAX;
 }
 
+template <int DT, bool CAP>
+bool launch_slices(const Args& a, unsigned grid, cudaStream_t s) {
+    if (cudaFuncSetAttribute(slice_kernel<DT, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, RING) != cudaSuccess)
+        return false;
+    slice_kernel<DT, CAP><<<grid, ST, RING, s>>>(a);
+    return cudaGetLastError() == cudaSuccess;
+}
 template <int DT>
-void launch(const Args& a, unsigned grid, cudaStream_t s) {
-    if (a.cap > 0.f) slice_kernel<DT, true><<<grid, ST, 0, s>>>(a);
-    else slice_kernel<DT, false><<<grid, ST, 0, s>>>(a);
+bool launch(const Args& a, unsigned grid, cudaStream_t s) {
+    return a.cap > 0.f ? launch_slices<DT, true>(a, grid, s) : launch_slices<DT, false>(a, grid, s);
 }
 
 }  // namespace hl_beam
@@ -787,10 +984,10 @@ extern "C" int headloss_beam_select(const void* logits, int64_t requests, int be
     a.tokens = tokens;
     a.out_ended = out_ended;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (dtype == HEADLOSS_FP32) launch<HEADLOSS_FP32>(a, unsigned(grid), s);
-    else if (dtype == HEADLOSS_BF16) launch<HEADLOSS_BF16>(a, unsigned(grid), s);
-    else launch<HEADLOSS_FP16>(a, unsigned(grid), s);
-    if (cudaGetLastError() != cudaSuccess) return HEADLOSS_ERR_CUDA;
+    const bool ok = dtype == HEADLOSS_FP32   ? launch<HEADLOSS_FP32>(a, unsigned(grid), s)
+                    : dtype == HEADLOSS_BF16 ? launch<HEADLOSS_BF16>(a, unsigned(grid), s)
+                                             : launch<HEADLOSS_FP16>(a, unsigned(grid), s);
+    if (!ok) return HEADLOSS_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(requests));
     cfg.blockDim = dim3(MT);

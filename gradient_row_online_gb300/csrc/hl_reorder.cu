@@ -125,6 +125,15 @@ __global__ void __launch_bounds__(T, 512 / T) reorder_kernel(const Args a) {
     }
 }
 
+inline int64_t gcd(int64_t a, int64_t b) {
+    while (b) {
+        const int64_t t = a % b;
+        a = b;
+        b = t;
+    }
+    return a;
+}
+
 template <int BT, int U, int T>
 int launch(Args a, int64_t lines, int64_t most_words, int sms, int smem, cudaStream_t s) {
     const int64_t chunks = (most_words + U * T - 1) / (U * T);
@@ -134,9 +143,13 @@ int launch(Args a, int64_t lines, int64_t most_words, int sms, int smem, cudaStr
     if (shares > chunks) shares = chunks;
     a.shares = uint32_t(shares);
     a.units = uint32_t(lines * shares);
+    // Requests differ in their moves and ranges, and follow one another in the units: with a grid that shares
+    // no divisor with their number every CTA meets all of them.
+    int64_t ctas = a.units < grid ? a.units : grid;
+    while (ctas < a.units && gcd(ctas, a.requests * shares) > 1) --ctas;
     if (smem && cudaFuncSetAttribute(reorder_kernel<BT, U, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return HEADLOSS_ERR_CUDA;
-    reorder_kernel<BT, U, T><<<unsigned(a.units < grid ? a.units : grid), T, smem, s>>>(a);
+    reorder_kernel<BT, U, T><<<unsigned(ctas), T, smem, s>>>(a);
     return cudaGetLastError() == cudaSuccess ? HEADLOSS_OK : HEADLOSS_ERR_CUDA;
 }
 
@@ -238,7 +251,7 @@ extern "C" int headloss_reorder(headloss_reorder_t h, const int32_t* parents, in
     // few words: one place a thread, on more CTAs
     const bool few = lines * ((h->most + 1023) / 1024) < 4 * sms;
     if (h->beams > 4)
-        return few ? launch<8, 1, 256>(a, lines, h->most, sms, 0, s) : launch<8, 2, 256>(a, lines, h->most, sms, 0, s);
+        return few ? launch<8, 1, 128>(a, lines, h->most, sms, 0, s) : launch<8, 2, 256>(a, lines, h->most, sms, 0, s);
     return few ? launch<4, 1, 256>(a, lines, h->most, sms, 0, s) : launch<4, 4, 256>(a, lines, h->most, sms, 0, s);
 }
 

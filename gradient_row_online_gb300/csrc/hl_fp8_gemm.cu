@@ -234,13 +234,19 @@ __global__ void __launch_bounds__(W_THREADS, 1)
             float sum[128];
 #pragma unroll
             for (int j = 0; j < 128; ++j) sum[j] = 0.f;
-            float fa = in ? __ldg(sa + int64_t(k0) * p.M) : 0.f, fb = __ldg(sb + k0);
+            // scales four blocks ahead: a load takes about as long as a block
+            float fa[4], fb[4];
+            auto fetch = [&](int kb, float& x, float& y) {
+                x = in && kb < k1 ? __ldg(sa + int64_t(kb) * p.M) : 0.f;
+                y = kb < k1 ? __ldg(sb + kb) : 0.f;
+            };
+#pragma unroll
+            for (int j = 0; j < 4; ++j) fetch(k0 + j, fa[j], fb[j]);
             for (int kb = k0; kb < k1; ++kb, ++it) {
-                const float s = fa * fb;
-                if (kb + 1 < k1) {
-                    fa = in ? __ldg(sa + int64_t(kb + 1) * p.M) : 0.f;
-                    fb = __ldg(sb + kb + 1);
-                }
+                const float s = fa[0] * fb[0];
+#pragma unroll
+                for (int j = 0; j < 3; ++j) fa[j] = fa[j + 1], fb[j] = fb[j + 1];
+                fetch(kb + 4, fa[3], fb[3]);
                 const int acc = int(it & 1u);
                 if (!wait_phase(su32(&empty[it % W_STAGES]), (it / W_STAGES) & 1u, abort, p.err)) {
                     go = false;

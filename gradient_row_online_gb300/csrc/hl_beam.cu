@@ -226,7 +226,9 @@ __global__ void __launch_bounds__(ST, 3) slice_kernel(const __grid_constant__ Ar
     __shared__ __align__(16) uint4 hit[HITS];
     __shared__ int hit_at[HITS];  // the word's place, and whether its sum went through mass_any
     __shared__ __align__(16) float tops[ST];
+    __shared__ uint32_t group[32];
     __shared__ float part[ST / 32], shift[ST / 32];
+    __shared__ long long extra[ST / 32];
     __shared__ int more_hits[3], count, found[ST / 32];
     __shared__ float bound_at;
     asm volatile("griddepcontrol.launch_dependents;");
@@ -258,6 +260,19 @@ __global__ void __launch_bounds__(ST, 3) slice_kernel(const __grid_constant__ Ar
         __syncthreads();
         return bound_at;
     };
+    // the keep-th largest and the largest of 32 values, a lane each (keep <= 32)
+    auto sorted = [&](float v, float& largest) {
+#pragma unroll
+        for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+            for (int o = k >> 1; o; o >>= 1) {
+                const float u = __shfl_xor_sync(0xffffffffu, v, o);
+                const bool larger = ((lane & o) == 0) == ((lane & k) == 0);  // falling where the k bit is clear
+                v = larger ? fmaxf(v, u) : fminf(v, u);
+            }
+        largest = __shfl_sync(0xffffffffu, v, 0);
+        return __shfl_sync(0xffffffffu, v, a.keep - 1);
+    };
     // A logit that `keep` of this batch's are not below: the keep-th largest of the maxima of 32 groups of
     // eight threads, sorted by every warp, or of the threads'. And the largest.
     auto batch_bound = [&](float mine, float& largest) {
@@ -271,17 +286,19 @@ __global__ void __launch_bounds__(ST, 3) slice_kernel(const __grid_constant__ Ar
         for (int o = 1; o < 8; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
         if ((lane & 7) == 0) tops[tid >> 3] = v;
         __syncthreads();
-        v = tops[lane];
-#pragma unroll
-        for (int k = 2; k <= 32; k <<= 1)
-#pragma unroll
-            for (int o = k >> 1; o; o >>= 1) {
-                const float u = __shfl_xor_sync(0xffffffffu, v, o);
-                const bool larger = ((lane & o) == 0) == ((lane & k) == 0);  // falling where the k bit is clear
-                v = larger ? fmaxf(v, u) : fminf(v, u);
-            }
-        largest = __shfl_sync(0xffffffffu, v, 0);
-        return __shfl_sync(0xffffffffu, v, a.keep - 1);
+        return sorted(tops[lane], largest);
+    };
+    // The same of a list in any order, a word a thread: the groups go by the words' places, so that the
+    // bound, and with it what enters the sum once more, is the same in every run.
+    auto list_bound = [&](float mine, int place) {
+        if (a.keep > 16) return nth(mine, a.keep);
+        if (tid < 32) group[tid] = 0u;
+        __syncthreads();
+        if (mine > NEG) atomicMax(&group[place & 31], key_of(mine));
+        __syncthreads();
+        const uint32_t k = group[lane];
+        float largest;
+        return sorted(k == 0u ? NEG : __uint_as_float(k >> 31 ? k & 0x7fffffffu : ~k), largest);
     };
 
     float top = NEG, bound = NEG;  // of this thread; of the CTA
@@ -450,13 +467,10 @@ __global__ void __launch_bounds__(ST, 3) slice_kernel(const __grid_constant__ Ar
         if (hits > (je < j1 ? HITS / 2 : MANY) && hits > a.keep && !crowded) {
             uint4 h = make_uint4(W::NONE, W::NONE, W::NONE, W::NONE);
             int h_at = 0;
-            const int e = (tid & 7) * 32 + tid / 8;  // the groups of eight threads share the list evenly
-            if (e < hits) h = hit[e], h_at = hit_at[e];
+            if (tid < hits) h = hit[tid], h_at = hit_at[tid];
             const float u = W::top_of(W::top2(W::top2(h.x, h.y), W::top2(W::top2(h.z, h.w), W::NONE)));
             if (tid == 0) count = 0;
-            float largest;
-            bound = fmaxf(bound, batch_bound(u, largest));
-            __syncthreads();
+            bound = fmaxf(bound, list_bound(u, h_at >> 1));
             if (u >= bound && u > NEG) {
                 const int p = atomicAdd(&count, 1);
                 hit[p] = h;
@@ -495,7 +509,7 @@ __global__ void __launch_bounds__(ST, 3) slice_kernel(const __grid_constant__ Ar
         if (shift[k] > NEG) sum += part[k] * hl::ex2f(shift[k] - zt);
     // 2^(top K - zt) is taken off again: zt was rounded
     if (!CAP) sum *= hl::ex2f(-fmaf(top, a.K, -zt));
-    float more = 0.f;
+    long long more = 0;  // in units of 2^-40: the list's order is not the same in every run, so it must not matter
     if (!crowded) {
         const int n = hits;
         for (int k = tid; k < n * W::PER; k += ST) {
@@ -509,7 +523,7 @@ __global__ void __launch_bounds__(ST, 3) slice_kernel(const __grid_constant__ Ar
                     // largest logit's own z
                     const hl::f2 one[1] = {hl::pk1(x)};
                     const float went = hit_at[h] & 1 ? mass_any(x, zt, a) : hl::lo_of(mass_near(one, hl::pk1(-zt), a));
-                    more += exp2f(fall(x, top, a.cap, a.inv_cap) * a.K) - went;
+                    more += __float2ll_rn((exp2f(fall(x, top, a.cap, a.inv_cap) * a.K) - went) * 0x1p40f);
                 }
             }
         }
@@ -517,13 +531,14 @@ __global__ void __launch_bounds__(ST, 3) slice_kernel(const __grid_constant__ Ar
     if (CAP) {
 #pragma unroll
         for (int o = 16; o; o >>= 1) more += __shfl_xor_sync(0xffffffffu, more, o);
-        __syncthreads();
-        if (lane == 0) part[warp] = more;
+        if (lane == 0) extra[warp] = more;
     }
     __syncthreads();
     if (CAP) {
+        more = 0;
 #pragma unroll
-        for (int k = 0; k < ST / 32; ++k) sum += part[k];
+        for (int k = 0; k < ST / 32; ++k) more += extra[k];
+        sum += float(more) * 0x1p-40f;
     }
     int n = count;
     const int e0 = max(0, j0 * W::PER - off), e1 = min(a.V, j1 * W::PER - off);

@@ -9,6 +9,12 @@
 namespace hl_tc {
 
 constexpr unsigned long long WAIT_NS = 2000000000ull;
+#ifdef HL_FAULT_INJECT  // test builds alone: another limit
+static __device__ unsigned long long injected_wait_ns = WAIT_NS;
+__device__ __forceinline__ unsigned long long wait_limit() { return injected_wait_ns; }
+#else
+__device__ __forceinline__ unsigned long long wait_limit() { return WAIT_NS; }
+#endif
 
 __device__ __forceinline__ uint32_t su32(const void* p) { return uint32_t(__cvta_generic_to_shared(p)); }
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
@@ -52,7 +58,7 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
     for (;;) {
         if (*abort) return false;
         if (mbar_try(bar, parity)) return true;
-        if (gtimer() - t0 > WAIT_NS) {
+        if (gtimer() - t0 > wait_limit()) {
             *abort = 1;
             atomicOr(err, 1);
             return false;
@@ -63,7 +69,7 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
 __device__ __forceinline__ void drain_phase(uint32_t bar, uint32_t parity, int* err) {
     const uint64_t t0 = gtimer();
     while (!mbar_try(bar, parity))
-        if (gtimer() - t0 > WAIT_NS) {
+        if (gtimer() - t0 > wait_limit()) {
             atomicOr(err, 1);
             return;
         }

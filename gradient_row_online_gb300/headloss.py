@@ -755,7 +755,8 @@ class Fp8Head:
 
     `weight` (V x D, unit column stride) is quantised once, in 128 x 128 blocks of e4m3;
     `set_weight` does so again after an optimiser's step, into the same buffers (order it
-    with calls on other streams).  `grads` is the 8-bit type of the loss's gradient, "e4m3"
+    with calls on other streams; a checkpoint's codes are left, the first time, for buffers of
+    the head's own).  `grads` is the 8-bit type of the loss's gradient, "e4m3"
     or "e5m2".  A call's own buffers are made on the stream it runs on."""
 
     _TYPES = {"e4m3": HEADLOSS_E4M3, "e5m2": HEADLOSS_E5M2}
@@ -786,7 +787,7 @@ class Fp8Head:
         self.type = types[q.dtype]
         with _on(self.index, None):
             codes = q.view(torch.uint8)
-            self.scales = scales.contiguous()
+            self.scales, self.held = scales.contiguous(), True
             if codes.is_contiguous() and D % 16 == 0 and codes.data_ptr() % 16 == 0:
                 self.q, self.ldq = codes, D
             else:
@@ -804,6 +805,7 @@ class Fp8Head:
             raise ValueError('grads: "e4m3" or "e5m2" is wanted')
         self._lib = load_library()
         self.V, self.D, self.train, self.type = V, D, bool(train), HEADLOSS_E4M3
+        self.held = False  # a checkpoint's own memory, which is not written to
         self.grads = self._TYPES[grads]
         self.index, self.device = like.get_device(), like.device
         self.weight_dtype = torch.bfloat16
@@ -875,8 +877,9 @@ class Fp8Head:
         self._matrix("weight", weight, self.index)
         if tuple(weight.shape) != (self.V, self.D):
             raise ValueError(f"weight: {self.V} x {self.D} is wanted")
-        if self.type != HEADLOSS_E4M3:
-            raise ValueError("set_weight: the head holds a checkpoint's e5m2 codes")
+        if self.held:
+            self._make()
+            self.type, self.held = HEADLOSS_E4M3, False
         t, self.weight_dtype = self.train, weight.dtype
         self._quantize(weight, HEADLOSS_E4M3, self.q.data_ptr(), self.ldq, self.scales.data_ptr(), 128,
                        self.qt.data_ptr() if t else None, self.ldqt if t else 0,
@@ -1036,7 +1039,7 @@ class StateReorder:
     `axis` the dimension of the positions (a cache's): a call's `begin` and `end` (int32, one a
     request) then name the positions to take, say those behind a prompt that the beams share.
     Called with parents (requests x beams int32, as the selection gives them); returns the
-    reordered tensors."""
+    reordered tensors.  The object is kept as long as a graph that holds one of its calls."""
 
     def __init__(self, states, beams: int, outs=None, axis=None):
         import torch

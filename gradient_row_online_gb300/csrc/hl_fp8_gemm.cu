@@ -8,7 +8,7 @@
 // than 128 products.
 //
 // One CTA an SM walks the 128 x 256 tiles of out. Few rows of a take the same way: a's tile is then
-// 16, 32 or 64 rows of copies, the MMAs' other rows are left as they are and never read, and b, 256 rows
+// 32 or 64 rows of copies, the MMAs' other rows are whatever follows and their sums never read, and b, 256 rows
 // at a time, streams through at HBM's rate. (b as the MMA's 128 rows and a as its 16 to 64 columns is
 // slower: such an MMA takes the time of 128 columns and more, and moves half the bytes of b.) With fewer
 // tiles than half the SMs, K is split; the parts go to the workspace in fp32 and a second kernel adds them in order.
@@ -56,9 +56,7 @@ __device__ __forceinline__ void store1(void* out, int64_t i, float v) {
 // ------------------------------------------------------------------ wide ----
 
 constexpr int WM = 128, WN = 256;
-constexpr int W_STAGES = 4;
-constexpr int WA_BYTES = WM * BK, WB_BYTES = WN * BK;      // 16 KB, 32 KB
-constexpr int W_STAGE_BYTES = WA_BYTES + WB_BYTES;
+constexpr int WB_BYTES = WN * BK;                           // 32 KB
 constexpr int W_EPI_WARPS = 8;                              // 2 for each TMEM lane quadrant
 constexpr int W_THREADS = 128 + 32 * W_EPI_WARPS;
 // Launched with 168 registers a thread (64512 a CTA); the warpgroup of the copies and MMAs
@@ -66,10 +64,19 @@ constexpr int W_THREADS = 128 + 32 * W_EPI_WARPS;
 constexpr int W_LAUNCH_REGS = 168, W_FEW_REGS = 40, W_SUM_REGS = 224;
 static_assert(128 * W_FEW_REGS + 32 * W_EPI_WARPS * W_SUM_REGS <= W_THREADS * W_LAUNCH_REGS, "registers");
 constexpr int W_OUT_BYTES = 32 * 128;                       // 32 rows x 128 bytes of one warp
-constexpr int W_OUT_OFF = W_STAGES * W_STAGE_BYTES;
-constexpr int W_BAR_OFF = W_OUT_OFF + W_EPI_WARPS * W_OUT_BYTES;
-constexpr int W_SMEM = W_BAR_OFF + 256 + 1024;
-static_assert(W_SMEM <= 232448, "shared memory");
+// By the rows of a's copies: few rows leave shared memory for more stages, that is for more bytes of b in
+// flight (128 KB an SM give 5.4 TB/s, 160 KB and 192 KB what HBM does), and fewer warps have rows to write out.
+template <int A_ROWS>
+struct Wide {
+    static constexpr int STAGES = A_ROWS == 32 ? 6 : A_ROWS == 64 ? 5 : 4;
+    static constexpr int A_BYTES = A_ROWS * BK;
+    static constexpr int STAGE_BYTES = A_BYTES + WB_BYTES;
+    static constexpr int OUT_OFF = STAGES * STAGE_BYTES;
+    static constexpr int OUT_WARPS = 2 * A_ROWS / 32;
+    static constexpr int BAR_OFF = OUT_OFF + OUT_WARPS * W_OUT_BYTES;
+    static constexpr int SMEM = BAR_OFF + 256 + 1024;
+    static_assert(SMEM <= 232448 && STAGE_BYTES >= WM * BK, "shared memory; the MMAs read 128 rows from a's first");
+};
 constexpr int GN = 16;                                      // column tiles a group of the tile order
 
 struct WideArgs {
@@ -81,7 +88,6 @@ struct WideArgs {
     int64_t mpad;           // rows between two parts of the workspace
     void* out;
     int64_t ldo;
-    int a_rows;             // of a's copies
     int early;              // b was in place before the launch in front of this one began
     int tma_out;            // rows of out start on 16-byte boundaries
     int n_even;             // and end on them
@@ -98,36 +104,39 @@ __device__ __forceinline__ void tile_at(uint32_t i, uint32_t MT, uint32_t NT, in
 }
 
 // Blocks of K of a CTA's first piece of work that fit the ring.
+template <int STAGES>
 __device__ __forceinline__ uint32_t first_blocks(const WideArgs& p) {
     const int sp = int(blockIdx.x % p.splits);
     const int n = int(int64_t(p.KB) * (sp + 1) / p.splits) - int(int64_t(p.KB) * sp / p.splits);
-    return uint32_t(min(n, W_STAGES));
+    return uint32_t(min(n, STAGES));
 }
 
 #ifdef HL_FAULT_INJECT  // test builds alone: the first CTA leaves out a's copy of this block
 static __device__ int injected_drop = -1;
 #endif
 
-template <int OT>
+template <int OT, int A_ROWS>
 __global__ void __launch_bounds__(W_THREADS, 1)
     wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                 const __grid_constant__ CUtensorMap map_o, const WideArgs p) {
+    using L = Wide<A_ROWS>;
+    constexpr int STAGES = L::STAGES;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     // full: a stage has its tiles, and the accumulator its block goes to was read (an arrival a warp);
     // empty: the block's MMAs are done, so its stage is free and its sums can be read. One wait and one
     // commit a block: each costs the issuing warp some hundred cycles of the block's 768.
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + W_BAR_OFF);
-    uint64_t* empty = full + W_STAGES;
-    uint64_t* mma_done = empty + W_STAGES;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
+    uint64_t* empty = full + STAGES;
+    uint64_t* mma_done = empty + STAGES;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = warp_index(), lane = threadIdx.x & 31;
     const uint32_t items = uint32_t(p.MT) * p.NT * p.splits;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < W_STAGES; ++s) {
+        for (int s = 0; s < STAGES; ++s) {
             mbar_init(su32(&full[s]), 1 + W_EPI_WARPS);
             mbar_init(su32(&empty[s]), 1);
         }
@@ -144,7 +153,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
     if (warp < 4) {
         give_registers<W_FEW_REGS>();
         if (warp == 0) {  // copies
-            const uint32_t bytes = uint32_t(p.a_rows * BK + WB_BYTES), ahead = p.early ? first_blocks(p) : 0;
+            const uint32_t ahead = p.early ? first_blocks<STAGES>(p) : 0;
             uint32_t it = 0;
             bool go = true;
             for (uint32_t i = blockIdx.x; go && i < items; i += gridDim.x) {
@@ -153,15 +162,15 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                 const int sp = int(i % p.splits);
                 const int k0 = int(int64_t(p.KB) * sp / p.splits), k1 = int(int64_t(p.KB) * (sp + 1) / p.splits);
                 for (int kb = k0; kb < k1; ++kb, ++it) {
-                    const int s = int(it % W_STAGES);
-                    const uint32_t a = su32(smem + s * W_STAGE_BYTES), bar = su32(&full[s]);
+                    const int s = int(it % STAGES);
+                    const uint32_t a = su32(smem + s * L::STAGE_BYTES), bar = su32(&full[s]);
                     if (it >= ahead) {
-                        if (!warp_wait(su32(&empty[s]), ((it / W_STAGES) & 1u) ^ 1u, abort, p.err)) {
+                        if (!warp_wait(su32(&empty[s]), ((it / STAGES) & 1u) ^ 1u, abort, p.err)) {
                             go = false;
                             break;
                         }
-                        warp_expect_tx(bar, bytes);
-                        warp_tma_load_2d(a + WA_BYTES, &map_b, kb * BK, n * WN, bar);
+                        warp_expect_tx(bar, L::STAGE_BYTES);
+                        warp_tma_load_2d(a + L::A_BYTES, &map_b, kb * BK, n * WN, bar);
                     }
 #ifdef HL_FAULT_INJECT
                     if (blockIdx.x == 0 && int(it) == injected_drop) continue;
@@ -169,8 +178,8 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                     warp_tma_load_2d(a, &map_a, kb * BK, m * WM, bar);
                 }
             }
-            for (uint32_t j = it > W_STAGES ? it - W_STAGES : 0; j < it; ++j)  // what was issued has landed
-                drain_phase(su32(&full[j % W_STAGES]), (j / W_STAGES) & 1u, p.err);
+            for (uint32_t j = it > STAGES ? it - STAGES : 0; j < it; ++j)  // what was issued has landed
+                drain_phase(su32(&full[j % STAGES]), (j / STAGES) & 1u, p.err);
         } else if (warp == 1) {  // MMAs
             uint32_t it = 0;
             bool go = true;
@@ -178,11 +187,11 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                 const int sp = int(i % p.splits);
                 const int k0 = int(int64_t(p.KB) * sp / p.splits), k1 = int(int64_t(p.KB) * (sp + 1) / p.splits);
                 for (int kb = k0; kb < k1; ++kb, ++it) {
-                    const int s = int(it % W_STAGES);
+                    const int s = int(it % STAGES);
                     const uint32_t acc = it & 1u;
-                    const uint32_t a = su32(smem + s * W_STAGE_BYTES);
-                    const uint64_t da = smem_desc(a), db = smem_desc(a + WA_BYTES);
-                    if (!warp_wait(su32(&full[s]), (it / W_STAGES) & 1u, abort, p.err)) {
+                    const uint32_t a = su32(smem + s * L::STAGE_BYTES);
+                    const uint64_t da = smem_desc(a), db = smem_desc(a + L::A_BYTES);
+                    if (!warp_wait(su32(&full[s]), (it / STAGES) & 1u, abort, p.err)) {
                         go = false;
                         break;
                     }
@@ -202,10 +211,10 @@ __global__ void __launch_bounds__(W_THREADS, 1)
             int m, n;
             tile_at(blockIdx.x / p.splits, p.MT, p.NT, m, n);
             const int k0 = int(int64_t(p.KB) * int(blockIdx.x % p.splits) / p.splits);
-            const uint32_t ahead = first_blocks(p);
+            const uint32_t ahead = first_blocks<STAGES>(p);
             for (uint32_t s = 0; s < ahead; ++s) {
-                warp_expect_tx(su32(&full[s]), uint32_t(p.a_rows * BK + WB_BYTES));
-                warp_tma_load_2d(su32(smem + s * W_STAGE_BYTES) + WA_BYTES, &map_b, (k0 + int(s)) * BK, n * WN, su32(&full[s]));
+                warp_expect_tx(su32(&full[s]), L::STAGE_BYTES);
+                warp_tma_load_2d(su32(smem + s * L::STAGE_BYTES) + L::A_BYTES, &map_b, (k0 + int(s)) * BK, n * WN, su32(&full[s]));
             }
             grid_wait();
         }
@@ -213,7 +222,8 @@ __global__ void __launch_bounds__(W_THREADS, 1)
     } else {  // scaled sums: warp w has TMEM lanes 32 (w % 4) .., columns 128 h ..
         take_registers<W_SUM_REGS>();
         const int q = warp & 3, h = (warp - 4) >> 2;
-        unsigned char* stage = smem + W_OUT_OFF + (warp - 4) * W_OUT_BYTES;
+        // (a warp without rows has no place to stage them, and writes none)
+        unsigned char* stage = smem + L::OUT_OFF + (h * (A_ROWS / 32) + q) * W_OUT_BYTES;
         uint32_t it = 0;
         bool go = true;
         if (lane == 0) {  // both accumulators are free
@@ -230,9 +240,9 @@ __global__ void __launch_bounds__(W_THREADS, 1)
             const bool in = row < p.M;
             if (int64_t(m) * WM + 32 * q >= p.M) {  // this warp has no rows of out
                 for (int kb = k0; go && kb < k1; ++kb, ++it) {
-                    go = wait_phase(su32(&empty[it % W_STAGES]), (it / W_STAGES) & 1u, abort, p.err);
+                    go = wait_phase(su32(&empty[it % STAGES]), (it / STAGES) & 1u, abort, p.err);
                     __syncwarp();
-                    if (go && lane == 0) mbar_arrive(su32(&full[(it + 2) % W_STAGES]));
+                    if (go && lane == 0) mbar_arrive(su32(&full[(it + 2) % STAGES]));
                 }
                 continue;
             }
@@ -255,7 +265,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                 for (int j = 0; j < 3; ++j) fa[j] = fa[j + 1], fb[j] = fb[j + 1];
                 fetch(kb + 4, fa[3], fb[3]);
                 const int acc = int(it & 1u);
-                if (!wait_phase(su32(&empty[it % W_STAGES]), (it / W_STAGES) & 1u, abort, p.err)) {
+                if (!wait_phase(su32(&empty[it % STAGES]), (it / STAGES) & 1u, abort, p.err)) {
                     go = false;
                     break;
                 }
@@ -272,7 +282,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                     } else {  // all is read: the accumulator is free for the block after the next
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(su32(&full[(it + 2) % W_STAGES]));
+                        if (lane == 0) mbar_arrive(su32(&full[(it + 2) % STAGES]));
                     }
 #pragma unroll
                     for (int j = 0; j < 32; ++j) sum[32 * c + j] = fmaf(__uint_as_float(v[c & 1][j]), s, sum[32 * c + j]);
@@ -423,24 +433,33 @@ int sm_count(int* sms) {
            cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
 }
 
-template <int OT>
-int launch_wide(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo, const WideArgs& a, int sms,
+template <int OT, int A_ROWS>
+int launch_rows(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo, const WideArgs& a, int sms,
                 cudaStream_t s) {
-    const void* fn = reinterpret_cast<const void*>(&wide_kernel<OT>);
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, W_SMEM) != cudaSuccess)
+    const auto fn = wide_kernel<OT, A_ROWS>;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Wide<A_ROWS>::SMEM) != cudaSuccess)
         return HEADLOSS_ERR_CUDA;
     const int64_t items = int64_t(a.MT) * a.NT * a.splits;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(items < sms ? items : sms));
     cfg.blockDim = dim3(W_THREADS);
-    cfg.dynamicSmemBytes = W_SMEM;
+    cfg.dynamicSmemBytes = Wide<A_ROWS>::SMEM;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.early ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, wide_kernel<OT>, ma, mb, mo, a) == cudaSuccess ? HEADLOSS_OK : HEADLOSS_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, fn, ma, mb, mo, a) == cudaSuccess ? HEADLOSS_OK : HEADLOSS_ERR_CUDA;
+}
+int rows_of_copies(int64_t M) { return M <= 32 ? 32 : M <= 64 ? 64 : WM; }
+template <int OT>
+int launch_wide(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo, const WideArgs& a, int sms,
+                cudaStream_t s) {
+    const int rows = rows_of_copies(a.M);
+    return rows == 32   ? launch_rows<OT, 32>(ma, mb, mo, a, sms, s)
+           : rows == 64 ? launch_rows<OT, 64>(ma, mb, mo, a, sms, s)
+                        : launch_rows<OT, WM>(ma, mb, mo, a, sms, s);
 }
 
 }  // namespace hl_fp8
@@ -504,11 +523,10 @@ int matmul(const void* a, int64_t lda, const float* a_scales, int a_type, const 
     w.ldo = ldo;
     w.tma_out = !(bits(out) & 15) && !((ldo * size) & 15);
     w.n_even = !((N * size) & 15);
-    w.a_rows = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : WM;
     w.early = early;
     w.idesc = idesc_of(WM, WN, a_type, b_type);
     w.err = err;
-    if (make_map(&ma, U8, a, M, K, lda, w.a_rows, BK) || make_map(&mb, U8, b, N, K, ldb, WN, BK))
+    if (make_map(&ma, U8, a, M, K, lda, rows_of_copies(M), BK) || make_map(&mb, U8, b, N, K, ldb, WN, BK))
         return HEADLOSS_ERR_CUDA;
     if (plan.splits > 1) {
         w.tma_out = w.n_even = 1;

@@ -28,8 +28,7 @@ struct Item {
     int64_t row_stride, outer_stride, position_stride;
     int64_t run_words;    // words of a position
     int64_t positions;
-    int32_t word;         // bytes
-    int32_t linear;       // positions follow one another without a gap
+    int64_t linear;       // positions follow one another without a gap
 };
 
 struct Args {
@@ -37,12 +36,21 @@ struct Args {
     const uint32_t* lines;  // [n] lines of one request before state i
     int n, beams;
     uint32_t requests, units, shares;
+    uint32_t outer;         // lines of every state where they have the same number, else 0
     const int32_t *parents, *begin, *end;
 };
 
-template <typename W, int BT, int U, int T>
+// U16 places of 16-byte words at once, and of smaller ones as many as make 16 words.
+template <typename W, int BT, int U16>
+__host__ __device__ constexpr int places() {
+    return sizeof(W) == 16 || BT == 0 ? U16 : 16 / (BT > 0 ? BT : 1);
+}
+template <typename W, int BT, int U16, int T>
 __device__ __forceinline__ void move(const Item& it, const char* src, char* dst, const int32_t* __restrict__ parents,
-                                     int B, int64_t k0, int64_t words, int64_t step, int64_t first, W* column) {
+                                     int B, uint32_t share, uint32_t shares, int64_t words, int64_t first, W* column) {
+    constexpr int U = places<W, BT, U16>();
+    const int64_t k0 = int64_t(share) * (BT > 0 ? U * T : T), step = int64_t(shares) * (BT > 0 ? U * T : T);
+    if (k0 >= words) return;
     const bool inplace = it.src == it.dst;
     auto parent = [&](int b) {
         const int p = __ldg(parents + b);
@@ -63,6 +71,7 @@ __device__ __forceinline__ void move(const Item& it, const char* src, char* dst,
             if (b < B && !(inplace && p == b)) moves |= 1u << b;
         }
         if (!moves) return;
+#pragma unroll 1
         for (int64_t k = k0 + threadIdx.x; k < words; k += step) {
             W v[U][BT > 0 ? BT : 1];
             int64_t at[U];
@@ -93,13 +102,14 @@ __device__ __forceinline__ void move(const Item& it, const char* src, char* dst,
     }
 }
 
-template <int BT, int U, int T>
+template <typename W, int BT, int U, int T>
 __global__ void __launch_bounds__(T, 512 / T) reorder_kernel(const Args a) {
     extern __shared__ __align__(16) unsigned char columns[];
     for (uint32_t unit = blockIdx.x; unit < a.units; unit += gridDim.x) {
         const uint32_t share = unit % a.shares, line = unit / a.shares;
         const uint32_t q = line / a.requests, r = line - q * a.requests;
-        int lo = 0, hi = a.n - 1;  // the state: the last one whose lines begin at or before q
+        // the state: the last one whose lines begin at or before q
+        int lo = a.outer ? int(q / a.outer) : 0, hi = a.outer ? lo : a.n - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) / 2;
             if (__ldg(a.lines + mid) <= q) lo = mid;
@@ -111,17 +121,12 @@ __global__ void __launch_bounds__(T, 512 / T) reorder_kernel(const Args a) {
             first = max(__ldg(a.begin + r), 0);
             last = min(int64_t(__ldg(a.end + r)), it.positions);
         }
-        const int64_t words = (last - first) * it.run_words, k0 = int64_t(share) * (U * T);
-        if (k0 >= words) continue;
-        const int64_t at = int64_t(r) * a.beams * it.row_stride + int64_t(q - __ldg(a.lines + lo)) * it.outer_stride;
-        const int64_t step = int64_t(a.shares) * (U * T);
-        const int32_t* parents = a.parents + int64_t(r) * a.beams;
-        switch (it.word) {
-            case 16: move<uint4, BT, U, T>(it, it.src + at, it.dst + at, parents, a.beams, k0, words, step, first, reinterpret_cast<uint4*>(columns)); break;
-            case 4: move<uint32_t, BT, U, T>(it, it.src + at, it.dst + at, parents, a.beams, k0, words, step, first, reinterpret_cast<uint32_t*>(columns)); break;
-            case 2: move<uint16_t, BT, U, T>(it, it.src + at, it.dst + at, parents, a.beams, k0, words, step, first, reinterpret_cast<uint16_t*>(columns)); break;
-            default: move<uint8_t, BT, U, T>(it, it.src + at, it.dst + at, parents, a.beams, k0, words, step, first, columns); break;
-        }
+        const int64_t words = (last - first) * it.run_words;
+        if (words <= 0) continue;
+        const int64_t at = int64_t(r) * a.beams * it.row_stride +
+                           int64_t(q - (a.outer ? uint32_t(lo) * a.outer : __ldg(a.lines + lo))) * it.outer_stride;
+        move<W, BT, U, T>(it, it.src + at, it.dst + at, a.parents + int64_t(r) * a.beams, a.beams, share, a.shares,
+                          words, first, reinterpret_cast<W*>(columns));
     }
 }
 
@@ -134,9 +139,20 @@ inline int64_t gcd(int64_t a, int64_t b) {
     return a;
 }
 
-template <int BT, int U, int T>
-int launch(Args a, int64_t lines, int64_t most_words, int sms, int smem, cudaStream_t s) {
-    const int64_t chunks = (most_words + U * T - 1) / (U * T);
+// The states whose words have one size.
+struct Group {
+    const Item* items;
+    const uint32_t* lines;
+    int n;
+    int64_t total;   // lines of one request
+    int64_t most;    // words of the longest
+    int64_t outer;   // lines of every state where they have the same number, else -1
+};
+
+template <typename W, int BT, int U, int T>
+int launch(Args a, const Group& g, int sms, int smem, cudaStream_t s) {
+    constexpr int chunk = places<W, BT, U>() * T;
+    const int64_t chunks = (g.most + chunk - 1) / chunk, lines = g.total * a.requests;
     const int64_t grid = int64_t(sms) * (1024 / T);
     // shares enough for four units a CTA, so that lines of different lengths even out
     int64_t shares = (4 * grid + lines - 1) / lines;
@@ -147,10 +163,21 @@ int launch(Args a, int64_t lines, int64_t most_words, int sms, int smem, cudaStr
     // no divisor with their number every CTA meets all of them.
     int64_t ctas = a.units < grid ? a.units : grid;
     while (ctas < a.units && gcd(ctas, a.requests * shares) > 1) --ctas;
-    if (smem && cudaFuncSetAttribute(reorder_kernel<BT, U, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    if (smem && cudaFuncSetAttribute(reorder_kernel<W, BT, U, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return HEADLOSS_ERR_CUDA;
-    reorder_kernel<BT, U, T><<<unsigned(ctas), T, smem, s>>>(a);
+    reorder_kernel<W, BT, U, T><<<unsigned(ctas), T, smem, s>>>(a);
     return cudaGetLastError() == cudaSuccess ? HEADLOSS_OK : HEADLOSS_ERR_CUDA;
+}
+
+// Sixteen words of a thread in flight (of 16 bytes: 256 bytes, four places of four beams), fewer places where
+// a line has too few words for that on every SM; more than 16 beams go through shared memory.
+template <typename W>
+int launch_words(const Args& a, const Group& g, int sms, cudaStream_t s) {
+    if (a.beams > 16) return launch<W, 0, 1, 128>(a, g, sms, a.beams * 128 * int(sizeof(W)), s);
+    if (a.beams > 8) return launch<W, 16, 1, 256>(a, g, sms, 0, s);
+    const bool few = g.total * a.requests * ((g.most + 1023) / 1024) < 4 * sms;
+    if (a.beams > 4) return few ? launch<W, 8, 1, 128>(a, g, sms, 0, s) : launch<W, 8, 2, 256>(a, g, sms, 0, s);
+    return few ? launch<W, 4, 1, 256>(a, g, sms, 0, s) : launch<W, 4, 4, 256>(a, g, sms, 0, s);
 }
 
 }  // namespace hl_reorder
@@ -158,9 +185,8 @@ int launch(Args a, int64_t lines, int64_t most_words, int sms, int smem, cudaStr
 struct headloss_reorder_s {
     hl_reorder::Item* items;
     uint32_t* lines;
-    int n, beams, sms;
-    int64_t total;  // lines of one request
-    int64_t most;   // words of the longest
+    int beams, sms;
+    hl_reorder::Group groups[4];  // words of 16, 4, 2 and 1 bytes
 };
 
 extern "C" int headloss_reorder_create(const headloss_state* states, int n, int beams, headloss_reorder_t* out) {
@@ -170,39 +196,46 @@ extern "C" int headloss_reorder_create(const headloss_state* states, int n, int 
     uint32_t* lines = new (std::nothrow) uint32_t[n];
     headloss_reorder_s* h = new (std::nothrow) headloss_reorder_s();
     int rc = items && lines && h ? HEADLOSS_OK : HEADLOSS_ERR_CUDA;
-    int64_t total = 0, most = 0;
     int used = 0;
-    for (int i = 0; rc == HEADLOSS_OK && i < n; ++i) {
-        const headloss_state& s = states[i];
-        if (!s.state || !s.out || s.outer < 0 || s.positions < 0 || s.run_bytes < 0 || s.row_stride < 0 ||
-            s.outer_stride < 0 || s.position_stride < 0) {
-            rc = HEADLOSS_ERR_ARG;
-            break;
+    const int sizes[4] = {16, 4, 2, 1};
+    for (int t = 0; t < 4; ++t) {
+        const int from = used;
+        Group group = {};
+        for (int i = 0; rc == HEADLOSS_OK && i < n; ++i) {
+            const headloss_state& s = states[i];
+            if (!s.state || !s.out || s.outer < 0 || s.positions < 0 || s.run_bytes < 0 || s.row_stride < 0 ||
+                s.outer_stride < 0 || s.position_stride < 0) {
+                rc = HEADLOSS_ERR_ARG;
+                break;
+            }
+            if (!s.outer || !s.positions || !s.run_bytes) continue;  // holds nothing
+            const int64_t outer_stride = s.outer > 1 ? s.outer_stride : 0;
+            const int64_t position_stride = s.positions > 1 ? s.position_stride : s.run_bytes;
+            const uint64_t bits = uint64_t(reinterpret_cast<uintptr_t>(s.state) | reinterpret_cast<uintptr_t>(s.out)) |
+                                  uint64_t(s.row_stride | outer_stride | position_stride | s.run_bytes);
+            if ((bits & 1 ? 1 : bits & 2 ? 2 : bits & 12 ? 4 : 16) != sizes[t]) continue;
+            Item& it = items[used];
+            it.src = static_cast<const char*>(s.state);
+            it.dst = static_cast<char*>(s.out);
+            it.row_stride = s.row_stride;
+            it.outer_stride = outer_stride;
+            it.position_stride = position_stride;
+            it.run_words = s.run_bytes / sizes[t];
+            it.positions = s.positions;
+            it.linear = position_stride == s.run_bytes;
+            lines[used] = uint32_t(group.total);
+            group.outer = used == from || group.outer == s.outer ? s.outer : -1;
+            ++used;
+            if (s.outer > INT32_MAX || (group.total += s.outer) > INT32_MAX || s.positions > INT64_MAX / s.run_bytes)
+                rc = HEADLOSS_ERR_ARG;
+            else if (it.positions * it.run_words > group.most)
+                group.most = it.positions * it.run_words;
         }
-        if (!s.outer || !s.positions || !s.run_bytes) continue;  // holds nothing
-        Item& it = items[used];
-        it.src = static_cast<const char*>(s.state);
-        it.dst = static_cast<char*>(s.out);
-        it.row_stride = s.row_stride;
-        it.outer_stride = s.outer > 1 ? s.outer_stride : 0;
-        it.position_stride = s.positions > 1 ? s.position_stride : s.run_bytes;
-        const uint64_t bits = uint64_t(reinterpret_cast<uintptr_t>(s.state) | reinterpret_cast<uintptr_t>(s.out)) |
-                              uint64_t(it.row_stride | it.outer_stride | it.position_stride | s.run_bytes);
-        it.word = bits & 1 ? 1 : bits & 2 ? 2 : bits & 12 ? 4 : 16;
-        it.run_words = s.run_bytes / it.word;
-        it.positions = s.positions;
-        it.linear = it.position_stride == s.run_bytes;
-        lines[used++] = uint32_t(total);
-        if (s.outer > INT32_MAX || (total += s.outer) > INT32_MAX || s.positions > INT64_MAX / s.run_bytes)
-            rc = HEADLOSS_ERR_ARG;
-        else if (it.positions * it.run_words > most)
-            most = it.positions * it.run_words;
+        group.n = used - from;
+        if (h) h->groups[t] = group;
     }
     if (rc == HEADLOSS_OK) {
-        h->n = used;
         h->beams = beams;
-        h->total = total;
-        h->most = most;
         int dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
@@ -212,6 +245,12 @@ extern "C" int headloss_reorder_create(const headloss_state* states, int n, int 
             cudaMemcpy(h->lines, lines, used * sizeof(uint32_t), cudaMemcpyHostToDevice) != cudaSuccess) {
             cudaGetLastError();
             rc = HEADLOSS_ERR_CUDA;
+        }
+        int from = 0;
+        for (int t = 0; t < 4; ++t) {
+            h->groups[t].items = h->items + from;
+            h->groups[t].lines = h->lines + from;
+            from += h->groups[t].n;
         }
     }
     delete[] items;
@@ -232,27 +271,29 @@ extern "C" int headloss_reorder(headloss_reorder_t h, const int32_t* parents, in
     if (!parents || !begin != !end) return HEADLOSS_ERR_ARG;
     if ((reinterpret_cast<uintptr_t>(parents) | reinterpret_cast<uintptr_t>(begin) | reinterpret_cast<uintptr_t>(end)) & 3)
         return HEADLOSS_ERR_ALIGN;
-    const int64_t lines = h->total * requests;
-    if (lines == 0) return HEADLOSS_OK;
-    if (lines > INT32_MAX) return HEADLOSS_ERR_ARG;
+    for (const Group& g : h->groups)
+        if (g.total * requests > INT32_MAX) return HEADLOSS_ERR_ARG;
     Args a = {};
-    a.items = h->items;
-    a.lines = h->lines;
-    a.n = h->n;
     a.beams = h->beams;
     a.requests = uint32_t(requests);
     a.parents = parents;
     a.begin = begin;
     a.end = end;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int sms = h->sms;
-    if (h->beams > 16) return launch<0, 1, 128>(a, lines, h->most, sms, h->beams * 128 * 16, s);
-    if (h->beams > 8) return launch<16, 1, 256>(a, lines, h->most, sms, 0, s);
-    // few words: one place a thread, on more CTAs
-    const bool few = lines * ((h->most + 1023) / 1024) < 4 * sms;
-    if (h->beams > 4)
-        return few ? launch<8, 1, 128>(a, lines, h->most, sms, 0, s) : launch<8, 2, 256>(a, lines, h->most, sms, 0, s);
-    return few ? launch<4, 1, 256>(a, lines, h->most, sms, 0, s) : launch<4, 4, 256>(a, lines, h->most, sms, 0, s);
+    for (int t = 0; t < 4; ++t) {
+        const Group& g = h->groups[t];
+        if (!g.n) continue;
+        a.items = g.items;
+        a.lines = g.lines;
+        a.n = g.n;
+        a.outer = g.outer > 0 ? uint32_t(g.outer) : 0;
+        const int rc = t == 0   ? launch_words<uint4>(a, g, h->sms, s)
+                       : t == 1 ? launch_words<uint32_t>(a, g, h->sms, s)
+                       : t == 2 ? launch_words<uint16_t>(a, g, h->sms, s)
+                                : launch_words<uint8_t>(a, g, h->sms, s);
+        if (rc != HEADLOSS_OK) return rc;
+    }
+    return HEADLOSS_OK;
 }
 
 extern "C" void headloss_reorder_destroy(headloss_reorder_t h) {

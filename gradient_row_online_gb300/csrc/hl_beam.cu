@@ -53,6 +53,7 @@ struct Args {
     float cap, inv_cap;
     float scale, K;       // logits_scale, logits_scale * log2(e)
     float cap_K, near;    // cap * K; the magnitudes that `poly` covers
+    float far;            // FAR octaves in logits
     hl::f2 poly[6];       // z K = x poly(x^2), each coefficient twice
     int slices, cap_list; // slices a row, candidates a slice
     Head* heads;
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(ST, 3) slice_kernel(const __grid_constant__ Ar
     const hl::f2 K2 = hl::pk1(a.K);
     const uint32_t near2 = CAP ? W::packed(a.near) : 0u;
     // at this logit (not below the bound) a shift is raised; none is where the cap keeps all within range
-    auto far_of = [&](float x) { return W::packed_up(CAP && 2.f * a.cap_K < FAR ? INFINITY : x + FAR / a.K); };
+    auto far_of = [&](float x) { return W::packed_up(CAP && 2.f * a.cap_K < FAR ? INFINITY : x + a.far); };
     auto z_of = [&](float x) { return CAP ? a.cap_K * tanhf(x * a.inv_cap) : x * a.K; };
     // Each thread copies and reads its own words, so that its own wait is all the copies need.
     auto fetch = [&](int jb, int stage) {
@@ -980,6 +981,7 @@ extern "C" int headloss_beam_select(const void* logits, int64_t requests, int be
     a.scale = logits_scale;
     a.K = K;
     a.cap_K = softcap * K;
+    a.far = FAR / K;
     // a cap whose powers leave fp32's range takes the other way to tanh throughout
     const bool fits = softcap > 1e-3f && softcap < 1e6f && K < 1e6f && K > 1e-6f;
     a.near = fits ? HL_TANH_B_Y0 * softcap : -1.f;

@@ -10,8 +10,16 @@
 // One CTA an SM walks the 128 x 256 tiles of out. Few rows of a take the same way: a's tile is then
 // 32 or 64 rows of copies, the MMAs' other rows are whatever follows and their sums never read, and b, 256 rows
 // at a time, streams through at HBM's rate. (b as the MMA's 128 rows and a as its 16 to 64 columns is
-// slower: such an MMA takes the time of 128 columns and more, and moves half the bytes of b.) With fewer
-// tiles than half the SMs, K is split; the parts go to the workspace in fp32 and a second kernel adds them in order.
+// slower: such an MMA takes the time of 128 columns and more, and moves half the bytes of b: 48 x 128256 took 115
+// us.) The tiles of the last round, which are fewer than SMs, have their K split where that takes less time; the
+// parts go to the workspace in fp32 and a second kernel adds them in order.
+//
+// What bounds it, at many rows: shared memory moves 96 KB a block of K (48 written by the copies, 48 read by the
+// MMAs), 768 cycles at 128 bytes a cycle, and reading the accumulator back takes another 256 of TMEM's: 1024, of
+// which the MMAs' own 512 are half. Measured 1050 cycles, 2.2 PFLOP/s (8192 x 32000 x 4096 0.96 ms); with K summed
+// in TMEM throughout, which the scales do not allow, 0.74 ms. Tiles of 256 x 256 on pairs of CTAs
+// (cta_group::2) move 64 KB a block, but with two accumulators the way over to the other CTA and back, some
+// 1300 cycles, is not hidden: 1.30 ms.
 // Every wait is bounded; one that gives up sets bit 0 of *err, and the kernel drains what it issued.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -64,11 +72,11 @@ constexpr int W_THREADS = 128 + 32 * W_EPI_WARPS;
 constexpr int W_LAUNCH_REGS = 168, W_FEW_REGS = 40, W_SUM_REGS = 224;
 static_assert(128 * W_FEW_REGS + 32 * W_EPI_WARPS * W_SUM_REGS <= W_THREADS * W_LAUNCH_REGS, "registers");
 constexpr int W_OUT_BYTES = 32 * 128;                       // 32 rows x 128 bytes of one warp
-// By the rows of a's copies: few rows leave shared memory for more stages, that is for more bytes of b in
-// flight (128 KB an SM give 5.4 TB/s, 160 KB and 192 KB what HBM does), and fewer warps have rows to write out.
+// By the rows of a's copies. Up to 64 rows leave shared memory for five stages, that is for 160 KB of b in flight,
+// and fewer warps have rows to write out (16 x 128256: 119 us with copies of 128 rows, 92 with 64, 94 with 32).
 template <int A_ROWS>
 struct Wide {
-    static constexpr int STAGES = A_ROWS == 32 ? 6 : A_ROWS == 64 ? 5 : 4;
+    static constexpr int STAGES = A_ROWS == 64 ? 5 : 4;
     static constexpr int A_BYTES = A_ROWS * BK;
     static constexpr int STAGE_BYTES = A_BYTES + WB_BYTES;
     static constexpr int OUT_OFF = STAGES * STAGE_BYTES;
@@ -84,8 +92,9 @@ struct WideArgs {
     const float* b_scales;  // [NB][KB]
     int64_t M, N;
     int KB, NB, MT, NT;
-    int splits;
-    int64_t mpad;           // rows between two parts of the workspace
+    uint32_t whole;         // tiles that one CTA sums over all of K; the others, fewer than SMs,
+    int splits;             // in as many parts of K
+    float* parts;           // [part][column half][32 rows][128 columns][row]
     void* out;
     int64_t ldo;
     int early;              // b was in place before the launch in front of this one began
@@ -103,12 +112,19 @@ __device__ __forceinline__ void tile_at(uint32_t i, uint32_t MT, uint32_t NT, in
     n = int(g * GN + w % wide);
 }
 
-// Blocks of K of a CTA's first piece of work that fit the ring.
-template <int STAGES>
-__device__ __forceinline__ uint32_t first_blocks(const WideArgs& p) {
-    const int sp = int(blockIdx.x % p.splits);
-    const int n = int(int64_t(p.KB) * (sp + 1) / p.splits) - int(int64_t(p.KB) * sp / p.splits);
-    return uint32_t(min(n, STAGES));
+// Piece i of the work: a tile, blocks k0 .. k1 - 1 of K, and the part that it is (-1: the whole sum).
+struct Piece {
+    uint32_t tile;
+    int k0, k1, part;
+};
+__device__ __forceinline__ Piece piece_at(const WideArgs& p, uint32_t i) {
+    if (i < p.whole) return {i, 0, p.KB, -1};
+    const uint32_t j = i - p.whole, t = j / uint32_t(p.splits), sp = j - t * uint32_t(p.splits);
+    return {p.whole + t, int(uint64_t(p.KB) * sp / uint32_t(p.splits)), int(uint64_t(p.KB) * (sp + 1) / uint32_t(p.splits)),
+            p.splits > 1 ? int(j) : -1};
+}
+__device__ __forceinline__ uint32_t pieces(const WideArgs& p) {
+    return p.whole + (uint32_t(p.MT) * p.NT - p.whole) * uint32_t(p.splits);
 }
 
 #ifdef HL_FAULT_INJECT  // test builds alone: the first CTA leaves out a's copy of this block
@@ -133,7 +149,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = warp_index(), lane = threadIdx.x & 31;
-    const uint32_t items = uint32_t(p.MT) * p.NT * p.splits;
+    const uint32_t items = pieces(p);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -153,15 +169,15 @@ __global__ void __launch_bounds__(W_THREADS, 1)
     if (warp < 4) {
         give_registers<W_FEW_REGS>();
         if (warp == 0) {  // copies
-            const uint32_t ahead = p.early ? first_blocks<STAGES>(p) : 0;
+            const Piece w0 = piece_at(p, blockIdx.x);
+            const uint32_t ahead = p.early ? uint32_t(min(w0.k1 - w0.k0, STAGES)) : 0;
             uint32_t it = 0;
             bool go = true;
             for (uint32_t i = blockIdx.x; go && i < items; i += gridDim.x) {
+                const Piece w = piece_at(p, i);
                 int m, n;
-                tile_at(i / p.splits, p.MT, p.NT, m, n);
-                const int sp = int(i % p.splits);
-                const int k0 = int(int64_t(p.KB) * sp / p.splits), k1 = int(int64_t(p.KB) * (sp + 1) / p.splits);
-                for (int kb = k0; kb < k1; ++kb, ++it) {
+                tile_at(w.tile, p.MT, p.NT, m, n);
+                for (int kb = w.k0; kb < w.k1; ++kb, ++it) {
                     const int s = int(it % STAGES);
                     const uint32_t a = su32(smem + s * L::STAGE_BYTES), bar = su32(&full[s]);
                     if (it >= ahead) {
@@ -184,9 +200,8 @@ __global__ void __launch_bounds__(W_THREADS, 1)
             uint32_t it = 0;
             bool go = true;
             for (uint32_t i = blockIdx.x; go && i < items; i += gridDim.x) {
-                const int sp = int(i % p.splits);
-                const int k0 = int(int64_t(p.KB) * sp / p.splits), k1 = int(int64_t(p.KB) * (sp + 1) / p.splits);
-                for (int kb = k0; kb < k1; ++kb, ++it) {
+                const Piece w = piece_at(p, i);
+                for (int kb = w.k0; kb < w.k1; ++kb, ++it) {
                     const int s = int(it % STAGES);
                     const uint32_t acc = it & 1u;
                     const uint32_t a = su32(smem + s * L::STAGE_BYTES);
@@ -208,13 +223,13 @@ __global__ void __launch_bounds__(W_THREADS, 1)
             }
         }
         else if (warp == 2 && p.early) {  // the first stages' rows of b, before a's quantisation is done
+            const Piece w = piece_at(p, blockIdx.x);
             int m, n;
-            tile_at(blockIdx.x / p.splits, p.MT, p.NT, m, n);
-            const int k0 = int(int64_t(p.KB) * int(blockIdx.x % p.splits) / p.splits);
-            const uint32_t ahead = first_blocks<STAGES>(p);
+            tile_at(w.tile, p.MT, p.NT, m, n);
+            const uint32_t ahead = uint32_t(min(w.k1 - w.k0, STAGES));
             for (uint32_t s = 0; s < ahead; ++s) {
                 warp_expect_tx(su32(&full[s]), L::STAGE_BYTES);
-                warp_tma_load_2d(su32(smem + s * L::STAGE_BYTES) + L::A_BYTES, &map_b, (k0 + int(s)) * BK, n * WN, su32(&full[s]));
+                warp_tma_load_2d(su32(smem + s * L::STAGE_BYTES) + L::A_BYTES, &map_b, (w.k0 + int(s)) * BK, n * WN, su32(&full[s]));
             }
             grid_wait();
         }
@@ -231,10 +246,10 @@ __global__ void __launch_bounds__(W_THREADS, 1)
             mbar_arrive(su32(&full[1]));
         }
         for (uint32_t i = blockIdx.x; go && i < items; i += gridDim.x) {
+            const Piece w = piece_at(p, i);
+            const int k0 = w.k0, k1 = w.k1;
             int m, n;
-            tile_at(i / p.splits, p.MT, p.NT, m, n);
-            const int sp = int(i % p.splits);
-            const int k0 = int(int64_t(p.KB) * sp / p.splits), k1 = int(int64_t(p.KB) * (sp + 1) / p.splits);
+            tile_at(w.tile, p.MT, p.NT, m, n);
             const int64_t row = int64_t(m) * WM + 32 * q + lane;
             const int nb = min(2 * n + h, p.NB - 1);
             const bool in = row < p.M;
@@ -289,9 +304,14 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                 }
             }
             if (!go) break;
+            if (w.part >= 0) {
+                float* to = p.parts + ((int64_t(w.part) * 2 + h) * 4 + q) * 4096 + lane;
+#pragma unroll
+                for (int j = 0; j < 128; ++j) to[j * 32] = sum[j];
+                continue;
+            }
             // 128 bytes of 32 rows at a time through shared memory (128-byte swizzle)
             constexpr int COLS = OT == HEADLOSS_FP32 ? 32 : 64;
-            const int64_t base = p.splits > 1 ? sp * p.mpad : 0;  // rows before this part's
             const int64_t r0 = int64_t(m) * WM + 32 * q, n0 = int64_t(n) * WN + 128 * h;
 #pragma unroll
             for (int g = 0; g < 128 / COLS; ++g) {
@@ -299,17 +319,17 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                 __syncwarp();
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
-                    uint4 w;
+                    uint4 u;
                     if (OT == HEADLOSS_FP32) {
                         const float* f = sum + 32 * g + 4 * c;
-                        w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                        u = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
                                        __float_as_uint(f[3]));
                     } else {
                         const float* f = sum + 64 * g + 8 * c;
-                        w = make_uint4(round2<OT>(f[0], f[1]), round2<OT>(f[2], f[3]), round2<OT>(f[4], f[5]),
+                        u = make_uint4(round2<OT>(f[0], f[1]), round2<OT>(f[2], f[3]), round2<OT>(f[4], f[5]),
                                        round2<OT>(f[6], f[7]));
                     }
-                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) * 16)) = w;
+                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) * 16)) = u;
                 }
                 const int64_t c0 = n0 + g * COLS;
                 // a store that TMA clips at N would still write whole 16-byte units
@@ -317,7 +337,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                     fence_async_shared();
                     __syncwarp();
                     if (lane == 0 && r0 < p.M && c0 < p.N) {
-                        tma_store_2d(&map_o, int(c0), int(base + r0), su32(stage));
+                        tma_store_2d(&map_o, int(c0), int(r0), su32(stage));
                         bulk_commit();
                     }
                 } else {
@@ -348,22 +368,30 @@ __global__ void __launch_bounds__(W_THREADS, 1)
     }
 }
 
-// The parts of a split K, added in their order.
+// The parts of the tiles whose K was split, added in their order: a CTA 32 rows x 32 columns.
 template <int OT>
-__global__ void __launch_bounds__(256) join_kernel(const float* __restrict__ parts, int splits, int64_t mpad,
-                                                   int64_t ldw, int64_t M, int64_t N, void* out, int64_t ldo) {
-    const int64_t words = ldw / 4, total = M * words;
-    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
-        const int64_t row = i / words, col = (i - row * words) * 4;
-        float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int s = 0; s < splits; ++s) {
-            const float4 u = *reinterpret_cast<const float4*>(parts + (s * mpad + row) * ldw + col);
-            t.x += u.x, t.y += u.y, t.z += u.z, t.w += u.w;
-        }
-        const float f[4] = {t.x, t.y, t.z, t.w};
+__global__ void __launch_bounds__(256) join_kernel(const WideArgs p) {
+    __shared__ float sums[32][33];
+    const int piece = blockIdx.x & 31, q = piece & 3, h = piece >> 2 & 1, j0 = (piece >> 3) * 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t t = blockIdx.x >> 5;
+    int m, n;
+    tile_at(p.whole + t, p.MT, p.NT, m, n);
+    const int64_t r0 = int64_t(m) * WM + 32 * q, c0 = int64_t(n) * WN + 128 * h + j0;
+    if (r0 >= p.M || c0 >= p.N) return;
+    const float* from = p.parts + ((int64_t(t) * p.splits * 2 + h) * 4 + q) * 4096 + (j0 + warp * 4) * 32 + lane;
+    float x[4] = {};
+#pragma unroll 8
+    for (int sp = 0; sp < p.splits; ++sp)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (col + j < N) store1<OT>(out, row * ldo + col + j, f[j]);
+        for (int j = 0; j < 4; ++j) x[j] += from[int64_t(sp) * 8 * 4096 + j * 32];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sums[lane][warp * 4 + j] = x[j];
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int64_t row = r0 + warp * 4 + r;
+        if (row < p.M && c0 + lane < p.N) store1<OT>(p.out, row * p.ldo + c0 + lane, sums[warp * 4 + r][lane]);
     }
 }
 
@@ -391,33 +419,33 @@ int make_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, int64_t
 }
 
 struct Plan {
+    int64_t whole;
     int splits;
-    int64_t mpad, ldw, bytes;
+    int64_t bytes;
 };
 
+// The tiles go over the SMs in rounds; those of the last, incomplete round have their K in as many parts as take
+// the least time: a block of K some 0.58 us, with few rows what its 32 KB of b take (0.4 us alone, HBM's rate
+// together), and for parts a second launch (4 us) and their sums written and read (5 bytes a picosecond). Measured,
+// whole and in parts: 4096 x 4096 x 128256 2155 and 1927 us, 512 x 4096 x 128256 534 and 311, 1 x 4096 x 32000 114
+// and 32, 200 x 1000 x 5003 26 and 12.
 Plan plan_of(int64_t M, int64_t N, int64_t K, int sms) {
-    Plan r = {};
-    const int64_t KB = (K + BK - 1) / BK;
-    r.splits = 1;
-    const int64_t tiles = ((M + WM - 1) / WM) * ((N + WN - 1) / WN);
-    // K in as many parts as take the least time: rounds of tiles on all SMs, each block of K some 0.58 us, and
-    // for parts a second launch (4 us) and their fp32 sums written and read (5 bytes a picosecond). Measured at 4096 x
-    // 4096 x 128256: 2.28 ms whole (3.4 rounds that count as four), 2.1 ms in parts.
-    const int64_t mpad = (M + 31) / 32 * 32, ldw = (N + 3) / 4 * 4;
-    double least = 0.58 * double((tiles + sms - 1) / sms) * double(KB);
-    for (int64_t s = 2; s <= 16 && s <= KB / 4; ++s) {
-        const double t = 0.58 * double((tiles * s + sms - 1) / sms) * double((KB + s - 1) / s) + 4.0 +
-                         double(s * mpad * ldw) * 8 / 5e6;
-        if (t < least) {
+    const int64_t KB = (K + BK - 1) / BK, tiles = ((M + WM - 1) / WM) * ((N + WN - 1) / WN), rest = tiles % sms;
+    Plan r = {tiles - rest, 1, 0};
+    double least = 0;
+    for (int64_t s = 1; rest && s <= 16 && (s == 1 || s <= KB / 4); ++s) {
+        const int64_t at_once = rest * s < sms ? rest * s : sms, rounds = (rest * s + sms - 1) / sms;
+        const double together = double(at_once) * WN * BK / 6.5e6;
+        const double block = M > 64 ? 0.58 : together > 0.4 ? together : 0.4;
+        const double t = block * double(rounds) * double((KB + s - 1) / s) +
+                         (s > 1 ? 4.0 + double(rest * s * (M < WM ? M : WM) * WN) * 8 / 5e6 : 0.0);
+        if (s == 1 || t < least) {
             least = t;
             r.splits = int(s);
         }
     }
-    if (r.splits > 1) {
-        r.mpad = mpad;
-        r.ldw = ldw;
-        r.bytes = r.splits * mpad * ldw * 4;
-    }
+    if (r.splits > 1) r.bytes = rest * r.splits * int64_t(WM) * WN * 4;
+    else r.whole = tiles;
     return r;
 }
 
@@ -439,7 +467,7 @@ int launch_rows(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap&
     const auto fn = wide_kernel<OT, A_ROWS>;
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Wide<A_ROWS>::SMEM) != cudaSuccess)
         return HEADLOSS_ERR_CUDA;
-    const int64_t items = int64_t(a.MT) * a.NT * a.splits;
+    const int64_t rest = int64_t(a.MT) * a.NT - a.whole, items = a.whole + rest * a.splits;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(items < sms ? items : sms));
     cfg.blockDim = dim3(W_THREADS);
@@ -450,16 +478,19 @@ int launch_rows(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap&
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.early ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, fn, ma, mb, mo, a) == cudaSuccess ? HEADLOSS_OK : HEADLOSS_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, fn, ma, mb, mo, a) != cudaSuccess) return HEADLOSS_ERR_CUDA;
+    if (a.splits > 1) {
+        join_kernel<OT><<<unsigned(rest * 32), 256, 0, s>>>(a);
+        if (cudaGetLastError() != cudaSuccess) return HEADLOSS_ERR_CUDA;
+    }
+    return HEADLOSS_OK;
 }
-int rows_of_copies(int64_t M) { return M <= 32 ? 32 : M <= 64 ? 64 : WM; }
+int rows_of_copies(int64_t M) { return M <= 64 ? 64 : WM; }
 template <int OT>
 int launch_wide(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo, const WideArgs& a, int sms,
                 cudaStream_t s) {
-    const int rows = rows_of_copies(a.M);
-    return rows == 32   ? launch_rows<OT, 32>(ma, mb, mo, a, sms, s)
-           : rows == 64 ? launch_rows<OT, 64>(ma, mb, mo, a, sms, s)
-                        : launch_rows<OT, WM>(ma, mb, mo, a, sms, s);
+    return rows_of_copies(a.M) == 64 ? launch_rows<OT, 64>(ma, mb, mo, a, sms, s)
+                                     : launch_rows<OT, WM>(ma, mb, mo, a, sms, s);
 }
 
 }  // namespace hl_fp8
@@ -517,8 +548,9 @@ int matmul(const void* a, int64_t lda, const float* a_scales, int a_type, const 
     w.NB = int((N + 127) / 128);
     w.MT = int((M + WM - 1) / WM);
     w.NT = int((N + WN - 1) / WN);
+    w.whole = uint32_t(plan.whole);
     w.splits = plan.splits;
-    w.mpad = plan.mpad;
+    w.parts = static_cast<float*>(workspace);
     w.out = out;
     w.ldo = ldo;
     w.tma_out = !(bits(out) & 15) && !((ldo * size) & 15);
@@ -528,23 +560,6 @@ int matmul(const void* a, int64_t lda, const float* a_scales, int a_type, const 
     w.err = err;
     if (make_map(&ma, U8, a, M, K, lda, rows_of_copies(M), BK) || make_map(&mb, U8, b, N, K, ldb, WN, BK))
         return HEADLOSS_ERR_CUDA;
-    if (plan.splits > 1) {
-        w.tma_out = w.n_even = 1;
-        if (make_map(&mo, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, workspace, plan.splits * plan.mpad, plan.ldw, plan.ldw * 4, 32, 32))
-            return HEADLOSS_ERR_CUDA;
-        const int rc = launch_wide<HEADLOSS_FP32>(ma, mb, mo, w, sms, s);
-        if (rc != HEADLOSS_OK) return rc;
-        const int64_t words = M * (plan.ldw / 4);
-        const int grid = int((words + 255) / 256 < 8 * sms ? (words + 255) / 256 : 8 * sms);
-        const float* parts = static_cast<const float*>(workspace);
-        if (out_dtype == HEADLOSS_FP32)
-            join_kernel<HEADLOSS_FP32><<<grid, 256, 0, s>>>(parts, plan.splits, plan.mpad, plan.ldw, M, N, out, ldo);
-        else if (out_dtype == HEADLOSS_BF16)
-            join_kernel<HEADLOSS_BF16><<<grid, 256, 0, s>>>(parts, plan.splits, plan.mpad, plan.ldw, M, N, out, ldo);
-        else
-            join_kernel<HEADLOSS_FP16><<<grid, 256, 0, s>>>(parts, plan.splits, plan.mpad, plan.ldw, M, N, out, ldo);
-        return cudaGetLastError() == cudaSuccess ? HEADLOSS_OK : HEADLOSS_ERR_CUDA;
-    }
     if (w.tma_out) {
         const auto type = out_dtype == HEADLOSS_FP32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                           : out_dtype == HEADLOSS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16

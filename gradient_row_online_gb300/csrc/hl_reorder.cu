@@ -4,8 +4,12 @@
 // A thread has words (16 bytes where the layout allows) at the same place of all beams of a
 // request: it reads the parents' before it writes, so that any map of parents is right in place
 // without a copy or a barrier, and a row that is its own parent costs nothing there. The words of
-// all beams, and of up to four places, are in flight together. HBM bound: a parent that several
-// beams share is read from HBM once.
+// all beams, and of several places, are in flight together. HBM bound: a parent that several
+// beams share is read from HBM once. Measured, GPU time, means over twelve draws of parents and ranges: 16 caches
+// of 16 x 4 beams x 8 x 2048 x 128 bf16 in place, up to a quarter of the positions, 64 us, 71% of the measured copy
+// rate over the bytes that move (64 to 80% in single draws: a third of the beams move, so most of a thread's
+// places have no load in flight); 32 caches of one request 8.5 us, of which a launch that moves nothing
+// takes 6.2.
 //
 // A unit of work is a line (a state, an outer index, a request) or one of C interleaved shares of it;
 // its CTA finds the positions to take from begin and end, so that a short range of a long cache costs
@@ -153,9 +157,14 @@ template <typename W, int BT, int U, int T>
 int launch(Args a, const Group& g, int sms, int smem, cudaStream_t s) {
     constexpr int chunk = places<W, BT, U>() * T;
     const int64_t chunks = (g.most + chunk - 1) / chunk, lines = g.total * a.requests;
-    const int64_t grid = int64_t(sms) * (1024 / T);
-    // shares enough for four units a CTA, so that lines of different lengths even out
+    // The CTAs that are resident at once: a second wave of fewer ends later (the mean of 16 caches of 16 x 4 beams
+    // over twelve draws of parents and ranges 69 us, and 64; through shared memory, where twice as many
+    // fit, the other way round: 216 us of 32 beams, and 198).
+    const int64_t grid = int64_t(sms) * ((BT ? 512 : 1024) / T);
+    // shares enough for four units a CTA, so that lines of different lengths even out, and for eight where a
+    // unit still has 4096 words (the same caches 66 and 64 us; 32 caches of one request, 8192 words a line, 8.5 and 11)
     int64_t shares = (4 * grid + lines - 1) / lines;
+    if (g.most / (2 * shares) >= 4096) shares *= 2;
     if (shares > chunks) shares = chunks;
     a.shares = uint32_t(shares);
     a.units = uint32_t(lines * shares);
@@ -169,15 +178,15 @@ int launch(Args a, const Group& g, int sms, int smem, cudaStream_t s) {
     return cudaGetLastError() == cudaSuccess ? HEADLOSS_OK : HEADLOSS_ERR_CUDA;
 }
 
-// Sixteen words of a thread in flight (of 16 bytes: 256 bytes, four places of four beams), fewer places where
-// a line has too few words for that on every SM; more than 16 beams go through shared memory.
+// Twelve to sixteen words of a thread in flight (three places of four beams: a fourth costs spilled registers), fewer
+// places where a line has too few words for that on every SM; more than 16 beams go through shared memory.
 template <typename W>
 int launch_words(const Args& a, const Group& g, int sms, cudaStream_t s) {
     if (a.beams > 16) return launch<W, 0, 1, 128>(a, g, sms, a.beams * 128 * int(sizeof(W)), s);
     if (a.beams > 8) return launch<W, 16, 1, 256>(a, g, sms, 0, s);
     const bool few = g.total * a.requests * ((g.most + 1023) / 1024) < 4 * sms;
     if (a.beams > 4) return few ? launch<W, 8, 1, 128>(a, g, sms, 0, s) : launch<W, 8, 2, 256>(a, g, sms, 0, s);
-    return few ? launch<W, 4, 1, 256>(a, g, sms, 0, s) : launch<W, 4, 4, 256>(a, g, sms, 0, s);
+    return few ? launch<W, 4, 1, 256>(a, g, sms, 0, s) : launch<W, 4, 3, 256>(a, g, sms, 0, s);
 }
 
 }  // namespace hl_reorder

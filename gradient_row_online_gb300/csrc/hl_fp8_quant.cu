@@ -9,7 +9,8 @@
 // the same: they are made once and turned 8 x 8 by byte permutes. The transpose's codes leave through
 // a 16 KB tile in shared memory whose 8-byte units are placed by XOR, so that both its writes and its
 // reads touch every bank once and global stores are whole 128-byte rows.
-// HBM bound: each input element is read once, each code written once.
+// HBM bound: each input element is read once, each code written once. Measured, both outputs, bf16: 4096 x 128256 in
+// blocks of 1 and 1 359 us, 5.9 TB/s; 128256 x 4096 in blocks of 128 and 128 308 us, 6.8 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

@@ -240,3 +240,42 @@ def test_captured_and_replayed():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("N", [1, 7, 64, 130, 392])
+@pytest.mark.parametrize("extra", [0, 1, 8])
+def test_out_that_starts_anywhere(dtype, N, extra):
+    """The bits do not depend on where rows of out start, and what lies beside them stays."""
+    g = torch.Generator().manual_seed(N)
+    head = pkg.Fp8Head(torch.randn(N, 200, generator=g).cuda())
+    x = torch.randn(37, 200, generator=g).to(dtype).cuda()
+    want = head.logits(x)
+    for o in range(8):
+        buf = torch.full((39, N + 8 + extra), 7.0, dtype=dtype, device="cuda")
+        assert torch.equal(head.logits(x, out=buf[1:38, o:o + N]), want)
+        buf[1:38, o:o + N] = 7.0
+        assert (buf == 7.0).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 1000, 256), (3, 257, 130), (70, 513, 1000), (200, 2049, 77), (1, 4096, 32000)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_linear_is_the_two_calls(M, N, K, dtype):
+    g = torch.Generator().manual_seed(M + N + K)
+    x = torch.randn(M, K, generator=g).to(dtype).cuda()
+    code, ld = hl.dtype_code(dtype), -(-K // 16) * 16
+    bq, bs, _, _ = run_quantise(torch.randn(N, K, generator=g).cuda(), "e4m3", 128, 128)
+    b = torch.zeros(N, ld, dtype=torch.uint8)
+    b[:, :K] = bq.view(torch.uint8)
+    b, bs = b.cuda(), bs.cuda()
+    a, sa = torch.empty(M, ld, dtype=torch.uint8, device="cuda"), torch.empty(-(-K // 128), M, device="cuda")
+    out = torch.empty(2, M, N, dtype=dtype, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    hl.headloss_fp8_quantize(x, M, K, K, code, CODE["e4m3"], a, ld, sa, 1, None, 0, None, 0)
+    need = hl.headloss_fp8_workspace(M, N, K)
+    work = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+    hl.headloss_fp8_matmul(a, ld, sa, CODE["e4m3"], b, ld, bs, CODE["e4m3"], M, N, K, out[0], N, code, work, need, err)
+    need = hl.headloss_fp8_linear_workspace(M, N, K)
+    work = torch.empty(need, dtype=torch.uint8, device="cuda")
+    hl.headloss_fp8_linear(x, K, code, b, ld, bs, CODE["e4m3"], M, N, K, out[1], N, code, work, need, err)
+    assert int(err) == 0 and torch.equal(out[0], out[1])

@@ -18,8 +18,8 @@
 // MMAs), 768 cycles at 128 bytes a cycle, and reading the accumulator back takes another 256 of TMEM's: 1024, of
 // which the MMAs' own 512 are half. Measured some 1070 cycles, 2.2 PFLOP/s (8192 x 32000 x 4096 0.98 ms); with K summed
 // in TMEM throughout, which the scales do not allow, 0.74 ms. Tiles of 256 x 256 on pairs of CTAs
-// (cta_group::2) move 64 KB a block, but with two accumulators the way over to the other CTA and back, some
-// 1300 cycles, is not hidden: 1.30 ms.
+// (cta_group::2) move 64 KB a block, but with two accumulators the way over to the other CTA and back is not
+// hidden (840 cycles from an accumulator's release to the next MMAs on it): 1.30 ms.
 // Every wait is bounded; one that gives up sets bit 0 of *err, and the kernel drains what it issued.
 #include <cuda.h>
 #include <cudaTypedefs.h>

@@ -851,6 +851,10 @@ __global__ void __launch_bounds__(MT) merge_kernel(const Args a) {
             }
             if (tid == 0) kept[k] = list[0];
             __syncthreads();
+            if (kept[k].key == NO_KEY) {  // the others score -inf: fewer candidates than `keep`
+                m = k;
+                break;
+            }
         }
     }
     __syncthreads();

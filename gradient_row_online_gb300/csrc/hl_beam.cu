@@ -69,12 +69,13 @@ struct Args {
     uint8_t* out_ended;
 };
 
+// Bits in the order of the values (0 and -0 the same).
 __device__ __forceinline__ uint32_t key_of(float x) {
-    const uint32_t b = __float_as_uint(x);
+    const uint32_t b = __float_as_uint(x + 0.f);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 __device__ __forceinline__ uint64_t key_of(double x) {
-    const uint64_t b = uint64_t(__double_as_longlong(x));
+    const uint64_t b = uint64_t(__double_as_longlong(x + 0.0));
     return b >> 63 ? ~b : b | (uint64_t(1) << 63);
 }
 

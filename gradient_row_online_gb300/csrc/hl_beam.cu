@@ -59,6 +59,7 @@ struct Args {
     float scale, K;       // logits_scale, logits_scale * log2(e)
     float cap_K, near;    // cap * K; the magnitudes that `poly` covers
     float far;            // FAR octaves in logits
+    int precise;          // a cap whose exponentials are taken from differences of logits alone
     hl::f2 poly[6];       // z K = x poly(x^2), each coefficient twice
     int slices, cap_list; // slices a row, candidates a slice
     Head* heads;
@@ -79,14 +80,16 @@ __device__ __forceinline__ uint64_t key_of(double x) {
     return b >> 63 ? ~b : b | (uint64_t(1) << 63);
 }
 
-// z(x) - z(top), top >= x: exact without a cap; with one through tanh of the difference,
-// -c tanh(b - y) (1 - tanh b tanh y), whose error is relative to the difference
+// z(x) - z(top), top >= x: exact without a cap. With one, for y = x / c, b = top / c and E = e^-2|.|,
+// tanh y - tanh b = 2 F (e^-2(b - y) - 1) / ((1 + E_y) (1 + E_b)), F the larger E where the signs are equal, else 1: no
+// cancellation, and an error (2^-19 up to 8 caps) that is relative to the difference.
+template <bool CAP>
 __device__ __forceinline__ float fall(float x, float top, float cap, float inv_cap) {
     if (x == top) return 0.f;
-    if (cap == 0.f) return x - top;
-    const float y = x * inv_cap, b = top * inv_cap;
-    if (isinf(b)) return cap * (tanhf(y) - tanhf(b));
-    return -cap * tanhf(b - y) * (1.f - tanhf(b) * tanhf(y));
+    if (!CAP) return x - top;
+    const float y = x * inv_cap, b = top * inv_cap, ey = expf(-2.f * fabsf(y)), eb = expf(-2.f * fabsf(b));
+    const float f = y < 0.f && b >= 0.f ? 1.f : fmaxf(ey, eb);
+    return cap * __fdividef(2.f * f * expm1f(-2.f * ((top - x) * inv_cap)), (1.f + ey) * (1.f + eb));
 }
 template <int DT>
 struct Words {
@@ -218,6 +221,7 @@ __device__ __forceinline__ hl::f2 mass_near(const hl::f2 (&x)[N], hl::f2 minus_z
 constexpr int HITS = ST;      // words with a candidate that a slice lists
 constexpr int MANY = 48;      // so many are thinned out before their logits are looked at
 constexpr float FAR = 64.f;   // octaves above a thread's shift at which it is raised
+constexpr double PRECISE = 1024.0;  // cap * scale above which the slice is read again for its sum
 constexpr int RING = 2 * SLICE_WORDS * 16;
 
 template <int DT, bool CAP>
@@ -524,7 +528,7 @@ __global__ void __launch_bounds__(ST, 3) slice_kernel(const __grid_constant__ Ar
                     // largest logit's own z
                     const hl::f2 one[1] = {hl::pk1(x)};
                     const float went = hit_at[h] & 1 ? mass_any(x, zt, a) : hl::lo_of(mass_near(one, hl::pk1(-zt), a));
-                    more += __float2ll_rn((exp2f(fall(x, top, a.cap, a.inv_cap) * a.K) - went) * 0x1p40f);
+                    more += __float2ll_rn((exp2f(fall<CAP>(x, top, a.cap, a.inv_cap) * a.K) - went) * 0x1p40f);
                 }
             }
         }
@@ -543,7 +547,8 @@ __global__ void __launch_bounds__(ST, 3) slice_kernel(const __grid_constant__ Ar
     }
     int n = count;
     const int e0 = max(0, j0 * W::PER - off), e1 = min(a.V, j1 * W::PER - off);
-    if (crowded || !(sum > 0.5f && sum < INFINITY)) {  // not all was summed; a NaN, an infinity, zt beyond fp32
+    // not all was summed; a NaN, an infinity, zt beyond fp32; a cap that the passes above are too coarse for
+    if (crowded || (CAP && a.precise) || !(sum > 0.5f && sum < INFINITY)) {
         float s = 0.f;
 #pragma unroll 1
         for (int e = e0 + tid; e < e1; e += ST) {
@@ -560,7 +565,7 @@ __global__ void __launch_bounds__(ST, 3) slice_kernel(const __grid_constant__ Ar
 #pragma unroll 1
         for (int e = e0 + tid; e < e1; e += ST) {
             const float x = W::value(base, e);
-            if (x > NEG) s += exp2f(fall(x, top, a.cap, a.inv_cap) * a.K);
+            if (x > NEG) s += exp2f(fall<CAP>(x, top, a.cap, a.inv_cap) * a.K);
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -675,7 +680,11 @@ __global__ void __launch_bounds__(MT) merge_kernel(const Args a) {
             if (top > NEG)
                 for (int k = lane; k < S; k += 32) {
                     const Head h = heads[b * S + k];
-                    if (h.top > NEG) total += h.sum * exp2f(fall(h.top, top, a.cap, a.inv_cap) * a.K);
+                    if (h.top > NEG) {
+                        const float d = a.cap > 0.f ? fall<true>(h.top, top, a.cap, a.inv_cap)
+                                                    : fall<false>(h.top, top, 0.f, 0.f);
+                        total += h.sum * exp2f(d * a.K);
+                    }
                 }
 #pragma unroll
             for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -986,16 +995,21 @@ extern "C" int headloss_beam_select(const void* logits, int64_t requests, int be
     a.K = K;
     a.cap_K = softcap * K;
     a.far = FAR / K;
-    // a cap whose powers leave fp32's range takes the other way to tanh throughout
-    const bool fits = softcap > 1e-3f && softcap < 1e6f && K < 1e6f && K > 1e-6f;
-    a.near = fits ? HL_TANH_B_Y0 * softcap : -1.f;
+    // Both fast ways to tanh are off by a share of the cap, up to 2^-21 of cap * scale in an exponent (a score of rows
+    // whose logits lie at a third of the cap: 2e-6 at a cap of 30, 3e-5 at 1000, 5e-3 at 1e5). Above PRECISE a slice is
+    // read again and its sum taken from differences: 2048 x 151936 bf16 3.3 ms, and 0.20.
+    a.precise = double(softcap) * double(logits_scale) > PRECISE;
+    // a cap whose powers leave fp32's normal range takes the other way to tanh throughout
     const double C[6] = {HL_TANH_B_C0, HL_TANH_B_C1, HL_TANH_B_C2, HL_TANH_B_C3, HL_TANH_B_C4, HL_TANH_B_C5};
+    bool fits = softcap > 0.f;
     for (int i = 0; fits && i < 6; ++i) {
         const float c = float(C[i] * double(K) / pow(double(softcap), 2 * i));
         uint32_t u;
         memcpy(&u, &c, 4);
         a.poly[i] = uint64_t(u) << 32 | u;
+        fits = isnormal(c);
     }
+    a.near = fits ? HL_TANH_B_Y0 * softcap : -1.f;
     a.slices = p.slices;
     a.cap_list = p.cap_list;
     a.heads = static_cast<Head*>(workspace);

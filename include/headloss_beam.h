@@ -25,10 +25,12 @@ int64_t headloss_beam_workspace(int64_t requests, int beams, int64_t V, int dtyp
  * A beam b with the running score s_b continues with token j at the score
  *   s_b + log p_b(j),  p_b the softmax of logits_scale * z,  z = c tanh(x / c) (softcap c; c = 0: z = x)
  * of its row x of logits.  A NaN counts as -inf; a token at -inf is no candidate, nor is any of a beam whose
- * score is -inf (or NaN): a first step has the scores 0, -inf, -inf, ...  A row with an infinity has its
- * mass on its infinities.  A beam that has ended has one candidate: itself, with token eos at the score
- * s_b; its row is not read.  Candidates are ordered by score, as fp64 evaluates it from the row's sum of
- * exponentials (which is held in fp32); equal scores by beam, then by falling logit, then by token.
+ * score is -inf (or NaN): a first step has the scores 0, -inf, -inf, ...  Without a softcap a row with an
+ * infinity has its mass on its infinities.  A beam that has ended has one candidate: itself, with token eos at
+ * the score s_b; its row is not read.  Candidates are ordered by score, as fp64 evaluates it from the row's sum
+ * of exponentials (which is held in fp32); equal scores by beam, then by falling logit, then by token.
+ * Under a softcap the sum is off by a share of 2^-21 softcap * logits_scale at most where that product is up to
+ * 1024, and of 2^-19 log V above, beside the roundings of its additions.
  *
  * logits:       requests * beams rows of V values of `dtype` (enum headloss_dtype), device; row i starts at
  *               element i * ld (ld >= V).  The base is aligned to the element; rows need no more.

@@ -450,16 +450,21 @@ __global__ void __launch_bounds__(ST, 3) slice_kernel(const __grid_constant__ Ar
             __syncthreads();
             bound2 = W::packed(bound);
 #pragma unroll 1
-            for (int i = 0; i < 2 * pairs; ++i) {
-                uint32_t w[4];
-                word(i, w);
-                if (W::reaches(word_top(w), bound2)) {
-                    const int p = hits + atomicAdd(pushed, 1);
-                    if (p < HITS) {
-                        hit[p] = make_uint4(w[0], w[1], w[2], w[3]);
-                        hit_at[p] = (jb + i * ST + tid) * 2 | 1;
+            for (int i = 0; i < 2 * pairs; i += 2) {
+                uint32_t w[2][4];
+                word(i, w[0]);
+                word(i + 1, w[1]);
+                int any = 0;  // as above: which way their masses were taken
+                if (CAP) any = !__all_sync(0xffffffffu, W::within(w[0], w[1], near2));
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    if (W::reaches(word_top(w[k]), bound2)) {
+                        const int p = hits + atomicAdd(pushed, 1);
+                        if (p < HITS) {
+                            hit[p] = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+                            hit_at[p] = (jb + (i + k) * ST + tid) * 2 | any;
+                        }
                     }
-                }
             }
             __syncthreads();
             listed = hits + *pushed;

@@ -304,8 +304,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
             const bool in = row < p.M;
             if (int64_t(m) * WM + 32 * q >= p.M) {  // this warp has no rows of out
                 for (int kb = k0; go && kb < k1; ++kb, ++it) {
-                    go = wait_phase(su32(&empty[it % STAGES]), (it / STAGES) & 1u, abort, p.err);
-                    __syncwarp();
+                    go = warp_wait(su32(&empty[it % STAGES]), (it / STAGES) & 1u, abort, p.err);
                     if (go && lane == 0) mbar_arrive(su32(&full[(it + 2) % STAGES]));
                 }
                 continue;
@@ -329,10 +328,11 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                 for (int j = 0; j < 3; ++j) fa[j] = fa[j + 1], fb[j] = fb[j + 1];
                 fetch(kb + 4, fa[3], fb[3]);
                 const int acc = int(it & 1u);
-                if (!wait_phase(su32(&empty[it % STAGES]), (it / STAGES) & 1u, abort, p.err)) {
-                    go = false;
-                    break;
-                }
+                // Lanes may answer differently where the limit runs out as the phase completes. They go on together
+                // all the same, and ask one another where they meet: a vote here delays every block (8192 x
+                // 32000 x 4096 in 987 us, and 900).
+                const bool there = wait_phase(su32(&empty[it % STAGES]), (it / STAGES) & 1u, abort, p.err);
+                __syncwarp();
                 tc_fence_after();
                 const uint32_t t = tmem + (uint32_t(32 * q) << 16) + uint32_t(acc * WN + 128 * h);
                 // the next 32 columns are on their way while these are added
@@ -345,12 +345,13 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                         tmem_ld32(t + 32 * (c + 1), v[(c + 1) & 1]);
                     } else {  // all is read: the accumulator is free for the block after the next
                         tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(su32(&full[(it + 2) % STAGES]));
+                        go = __all_sync(0xffffffffu, there);
+                        if (go && lane == 0) mbar_arrive(su32(&full[(it + 2) % STAGES]));
                     }
 #pragma unroll
                     for (int j = 0; j < 32; ++j) sum[32 * c + j] = fmaf(__uint_as_float(v[c & 1][j]), s, sum[32 * c + j]);
                 }
+                if (!go) break;
             }
             if (!go) break;
             if (w.part >= 0) {

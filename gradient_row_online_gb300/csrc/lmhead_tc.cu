@@ -346,7 +346,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             int m, n;
             tile_of(i, MT, NT, m, n);
             const int acc = j & 1;
-            if (!wait_phase(su32(&tfull[acc]), uint32_t(j >> 1) & 1u, abort, err)) break;
+            // one answer for the warp: its lanes give up by clocks of their own, and read TMEM together
+            if (!__all_sync(0xffffffffu, wait_phase(su32(&tfull[acc]), uint32_t(j >> 1) & 1u, abort, err)))
+                break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t tbase = tmem + (uint32_t(32 * q) << 16) + uint32_t(acc * BN);
             float mx = -INFINITY, ssum = 0.f, esum = 0.f, ax = 0.f, tsum = 0.f;

@@ -28,3 +28,12 @@ def test_the_8_bit_products_warps_wait_together():
         end = text.index("__all_sync(0xffffffffu, there)", at)
         between = text[text.index(";", at):end]
         assert not re.search(r"there|break|return|continue|go\b(?! = $)", between)
+
+
+def test_the_bf16_products_epilogue_waits_together():
+    text = source("lmhead_tc.cu")
+    kernel = text[text.index("lmhead_gemm_kernel("):]
+    single = kernel[kernel.index("if (lane == 0) {"):kernel.index("const int q = warp & 3;")]  # the roles of one lane
+    whole = kernel[kernel.index("const int q = warp & 3;"):]
+    assert single.count("wait_phase(") == 3
+    assert whole.count("wait_phase(") == len(re.findall(r"__all_sync\(0xffffffffu, wait_phase\(", whole)) == 1

@@ -17,10 +17,12 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <new>
 
 #include "headloss.h"
 #include "headloss_beam.h"
+#include "hl_reorder_plan.h"
 
 namespace hl_reorder {
 
@@ -196,28 +198,44 @@ struct headloss_reorder_s {
     uint32_t* lines;
     int beams, sms;
     hl_reorder::Group groups[4];  // words of 16, 4, 2 and 1 bytes
+    headloss_state* states;       // on the host
+    int n;
+    std::atomic<int64_t> apart;   // so many rows are known to share no memory
 };
 
 extern "C" int headloss_reorder_create(const headloss_state* states, int n, int beams, headloss_reorder_t* out) {
     using namespace hl_reorder;
     if (!states || !out || n < 1 || n > (1 << 20) || beams < 1 || beams > MAX_BEAMS) return HEADLOSS_ERR_ARG;
+    int live = 0;  // states that hold anything
+    for (int i = 0; i < n; ++i) {
+        const headloss_state& s = states[i];
+        if (!s.state || !s.out || s.outer < 0 || s.positions < 0 || s.run_bytes < 0 || s.row_stride < 0 ||
+            s.outer_stride < 0 || s.position_stride < 0)
+            return HEADLOSS_ERR_ARG;
+        if (!s.outer || !s.positions || !s.run_bytes) continue;
+        if (s.outer > INT32_MAX || s.positions > INT64_MAX / s.run_bytes) return HEADLOSS_ERR_ARG;
+        ++live;
+    }
     Item* items = new (std::nothrow) Item[n];
     uint32_t* lines = new (std::nothrow) uint32_t[n];
     headloss_reorder_s* h = new (std::nothrow) headloss_reorder_s();
-    int rc = items && lines && h ? HEADLOSS_OK : HEADLOSS_ERR_CUDA;
+    headloss_state* held = new (std::nothrow) headloss_state[live > 0 ? live : 1];
+    if (h) h->states = new (std::nothrow) headloss_state[live > 0 ? live : 1];
+    int rc = items && lines && h && held && h->states ? HEADLOSS_OK : HEADLOSS_ERR_CUDA;
+    if (rc == HEADLOSS_OK) {
+        live = 0;
+        for (int i = 0; i < n; ++i)
+            if (states[i].outer && states[i].positions && states[i].run_bytes) held[live++] = states[i];
+        h->n = without_repeats(held, live, h->states);
+        if (h->n < 0) rc = HEADLOSS_ERR_CUDA;
+    }
     int used = 0;
     const int sizes[4] = {16, 4, 2, 1};
-    for (int t = 0; t < 4; ++t) {
+    for (int t = 0; t < 4 && rc == HEADLOSS_OK; ++t) {
         const int from = used;
         Group group = {};
-        for (int i = 0; rc == HEADLOSS_OK && i < n; ++i) {
-            const headloss_state& s = states[i];
-            if (!s.state || !s.out || s.outer < 0 || s.positions < 0 || s.run_bytes < 0 || s.row_stride < 0 ||
-                s.outer_stride < 0 || s.position_stride < 0) {
-                rc = HEADLOSS_ERR_ARG;
-                break;
-            }
-            if (!s.outer || !s.positions || !s.run_bytes) continue;  // holds nothing
+        for (int i = 0; i < h->n; ++i) {
+            const headloss_state& s = h->states[i];
             const int64_t outer_stride = s.outer > 1 ? s.outer_stride : 0;
             const int64_t position_stride = s.positions > 1 ? s.position_stride : s.run_bytes;
             const uint64_t bits = uint64_t(reinterpret_cast<uintptr_t>(s.state) | reinterpret_cast<uintptr_t>(s.out)) |
@@ -235,13 +253,15 @@ extern "C" int headloss_reorder_create(const headloss_state* states, int n, int 
             lines[used] = uint32_t(group.total);
             group.outer = used == from || group.outer == s.outer ? s.outer : -1;
             ++used;
-            if (s.outer > INT32_MAX || (group.total += s.outer) > INT32_MAX || s.positions > INT64_MAX / s.run_bytes)
+            group.total += s.outer;
+            if (group.total > INT32_MAX) {
                 rc = HEADLOSS_ERR_ARG;
-            else if (it.positions * it.run_words > group.most)
-                group.most = it.positions * it.run_words;
+                break;
+            }
+            if (it.positions * it.run_words > group.most) group.most = it.positions * it.run_words;
         }
         group.n = used - from;
-        if (h) h->groups[t] = group;
+        h->groups[t] = group;
     }
     if (rc == HEADLOSS_OK) {
         h->beams = beams;
@@ -264,6 +284,7 @@ extern "C" int headloss_reorder_create(const headloss_state* states, int n, int 
     }
     delete[] items;
     delete[] lines;
+    delete[] held;
     if (rc != HEADLOSS_OK) {
         headloss_reorder_destroy(h);
         return rc;
@@ -282,6 +303,11 @@ extern "C" int headloss_reorder(headloss_reorder_t h, const int32_t* parents, in
         return HEADLOSS_ERR_ALIGN;
     for (const Group& g : h->groups)
         if (g.total * requests > INT32_MAX) return HEADLOSS_ERR_ARG;
+    const int64_t rows = requests * h->beams;
+    if (rows > h->apart.load(std::memory_order_relaxed)) {
+        if (conflict(h->states, h->n, rows)) return HEADLOSS_ERR_ARG;
+        h->apart.store(rows, std::memory_order_relaxed);  // (another call's smaller number is right, too)
+    }
     Args a = {};
     a.beams = h->beams;
     a.requests = uint32_t(requests);
@@ -309,5 +335,6 @@ extern "C" void headloss_reorder_destroy(headloss_reorder_t h) {
     if (!h) return;
     if (h->items) cudaFree(h->items);
     if (h->lines) cudaFree(h->lines);
+    delete[] h->states;
     delete h;
 }

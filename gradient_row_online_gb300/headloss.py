@@ -1035,7 +1035,8 @@ class StateReorder:
     """headloss_reorder on torch tensors: the beams take their parents' states, in place or into
     `outs` (buffers of the same layout).  The tensors are held.
 
-    `states` are tensors of requests * beams rows (or more: those behind stay as they are).  With
+    `states` are tensors of requests * beams rows (or more: those behind stay as they are); one that is
+    listed twice is moved once, and a call refuses those that share memory in other ways.  With
     `axis` the dimension of the positions (a cache's): a call's `begin` and `end` (int32, one a
     request) then name the positions to take, say those behind a prompt that the beams share.
     Called with parents (requests x beams int32, as the selection gives them); returns the

@@ -78,8 +78,9 @@ typedef struct headloss_reorder_s* headloss_reorder_t;
 /*
  * headloss_reorder_create -- takes n states (1 .. 2^20) of beams, and copies the list to the current
  * device (synchronously).  `states` is in HOST memory.
+ * A state that is listed more than once, with the same out and layout, is moved once.
  * Errors: ERR_ARG (n out of range, beams not in 1 .. 64, a NULL pointer, outer, positions or run_bytes < 0, a
- * negative stride, 2^31 outer indices or more; that state and out overlap without being the same is not checked), ERR_CUDA.
+ * negative stride, 2^31 outer indices or more), ERR_CUDA.
  */
 int headloss_reorder_create(const headloss_state* states, int n, int beams, headloss_reorder_t* out);
 
@@ -94,7 +95,10 @@ int headloss_reorder_create(const headloss_state* states, int n, int beams, head
  * Asynchronous on `stream`, no allocation.  requests == 0 is valid; rows from requests * beams on stay as
  * they were.  In place, a row that is its own parent is neither read nor written.
  * Errors (nothing enqueued): ERR_ARG (NULL handle, parents NULL, one of begin and end NULL, requests < 0 or
- * requests * beams or requests times the handle's outer indices >= 2^31), ERR_ALIGN (an array not 4-byte aligned), ERR_CUDA.
+ * requests * beams or requests times the handle's outer indices >= 2^31; memory that these rows of one state's out
+ * take and another state or out, or the state itself where out is not the same, holds too, whatever begin and end:
+ * checked on the first call with so many requests; layouts that interleave beyond what a short search resolves
+ * count as such), ERR_ALIGN (an array not 4-byte aligned), ERR_CUDA.
  */
 int headloss_reorder(headloss_reorder_t h, const int32_t* parents, int64_t requests, const int32_t* begin,
                      const int32_t* end, void* stream);

@@ -163,11 +163,7 @@ int launch(Args a, const Group& g, int sms, int smem, cudaStream_t s) {
     // over twelve draws of parents and ranges 69 us, and 64; through shared memory, where twice as many
     // fit, the other way round: 216 us of 32 beams, and 198).
     const int64_t grid = int64_t(sms) * ((BT ? 512 : 1024) / T);
-    // shares enough for four units a CTA, so that lines of different lengths even out, and for eight where a
-    // unit still has 4096 words (the same caches 66 and 64 us; 32 caches of one request, 8192 words a line, 8.5 and 11)
-    int64_t shares = (4 * grid + lines - 1) / lines;
-    if (g.most / (2 * shares) >= 4096) shares *= 2;
-    if (shares > chunks) shares = chunks;
+    const int64_t shares = shares_of(lines, g.most, chunks, grid);
     a.shares = uint32_t(shares);
     a.units = uint32_t(lines * shares);
     // Requests differ in their moves and ranges, and follow one another in the units: with a grid that shares

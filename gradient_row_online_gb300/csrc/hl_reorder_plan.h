@@ -1,4 +1,5 @@
-// hl_reorder_plan.h -- what headloss_reorder decides on the host: whether its states share memory.
+// hl_reorder_plan.h -- what headloss_reorder decides on the host: whether its states share memory, and how many
+// units of work a line is.
 #pragma once
 #include <stdint.h>
 
@@ -145,6 +146,16 @@ inline int without_repeats(const headloss_state* from, int n, headloss_state* to
     delete[] order;
     delete[] again;
     return m;
+}
+
+// The shares of a line, of lines (below 2^31) whose longest has `most` words in `chunks` of a CTA's: enough for four
+// units a CTA, so that lines of different lengths even out, and for eight where a unit still has 4096 words (16 caches of
+// 16 x 4 beams 66 and 64 us; 32 caches of one request, 8192 words a line, 8.5 and 11). The units, and a step of the
+// grid past the last of them, are counted in 32 bits.
+inline int64_t shares_of(int64_t lines, int64_t most, int64_t chunks, int64_t grid) {
+    int64_t shares = (4 * grid + lines - 1) / lines;
+    if (most / (2 * shares) >= 4096 && 2 * shares * lines <= INT32_MAX) shares *= 2;
+    return shares < chunks ? shares : chunks;
 }
 
 }  // namespace hl_reorder

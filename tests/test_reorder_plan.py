@@ -1,5 +1,5 @@
 """What the reordering decides on the host, compiled by itself: no GPU. Whether states share memory, against their bytes
-counted one by one; which states are the same."""
+counted one by one; which states are the same; how many units of work there are."""
 import ctypes
 import itertools
 import os
@@ -16,6 +16,7 @@ DRIVER = """
 #include "hl_reorder_plan.h"
 extern "C" int overlap(const headloss_state* s, int n, int64_t rows) { return hl_reorder::conflict(s, n, rows); }
 extern "C" int distinct(const headloss_state* s, int n, headloss_state* to) { return hl_reorder::without_repeats(s, n, to); }
+extern "C" int64_t shares(int64_t lines, int64_t most, int64_t chunks, int64_t grid) { return hl_reorder::shares_of(lines, most, chunks, grid); }
 """
 
 
@@ -30,6 +31,7 @@ def plan(tmp_path_factory):
     lib = ctypes.CDLL(str(lib))
     lib.overlap.argtypes = [ctypes.POINTER(hlb.headloss_state), ctypes.c_int, ctypes.c_int64]
     lib.distinct.argtypes = [ctypes.POINTER(hlb.headloss_state), ctypes.c_int, ctypes.POINTER(hlb.headloss_state)]
+    lib.shares.argtypes, lib.shares.restype = [ctypes.c_int64] * 4, ctypes.c_int64
     return lib
 
 
@@ -127,3 +129,13 @@ def test_states_that_are_the_same(plan):
     got = [tuple(getattr(e, f) for f, _ in hlb.headloss_state._fields_) for e in to[:n]]
     assert got == [s[3], s[0], s[1], s[2]]  # (a stride that nothing is stepped by makes no difference)
     assert plan.distinct(table(s[0]), 0, to) == 0
+
+
+@pytest.mark.parametrize("grid", [1, 148, 152, 304, 608, 1216])
+def test_units_are_counted_in_32_bits(plan, grid):
+    for lines in (1, 7, 600, grid, 4 * grid, 1 << 20, (1 << 30) - 1, 1 << 30, (1 << 30) + 1, (1 << 31) - 600, (1 << 31) - 1):
+        for most in (1, 4096, 8191, 8192, 1 << 20, 1 << 40):
+            for chunk in (128, 768, 4096):
+                shares = plan.shares(lines, most, -(-most // chunk), grid)
+                assert 1 <= shares <= -(-most // chunk)
+                assert lines * shares + grid < 1 << 32, (lines, most, chunk)  # where a CTA's last step leads

@@ -1065,6 +1065,7 @@ class StateReorder:
         self._i32 = torch.int32
         self._call = load_library().headloss_reorder
         live = [e for e, t in zip(table, states) if t.numel()]
+        self._moves = bool(live)
         if live:
             with _on(self.index, None):
                 self.h = headloss_reorder_create((headloss_state * len(live))(*live), len(live), self.beams)
@@ -1116,7 +1117,9 @@ class StateReorder:
             if a is not None and (a.dtype is not self._i32 or a.dim() != 1 or a.numel() != R or
                                   a.get_device() != self.index or not a.is_contiguous()):
                 raise ValueError(f"{name}: a contiguous int32 tensor of {R} on {self.device} is wanted")
-        if self.h:
+        if self._moves:
+            if not self.h:
+                raise ValueError("a reordering that is not closed is wanted")
             status = self._call(self.h, parents.data_ptr(), R, begin.data_ptr() if begin is not None else None,
                                 end.data_ptr() if end is not None else None, _raw_stream(self.index))
             if status:

@@ -176,15 +176,17 @@ int launch(Args a, const Group& g, int sms, int smem, cudaStream_t s) {
     return cudaGetLastError() == cudaSuccess ? HEADLOSS_OK : HEADLOSS_ERR_CUDA;
 }
 
-// Twelve to sixteen words of a thread in flight (three places of four beams: a fourth costs spilled registers), fewer
-// places where a line has too few words for that on every SM; more than 16 beams go through shared memory.
+// Twelve to sixteen words of a thread in flight, in 128 registers: three places of four beams' 16-byte words (a fourth
+// spills; two places of five to eight beams spill 88 bytes, the smaller words of up to four beams 20), fewer places
+// where a line has too few words for that on every SM; more than 16 beams go through shared memory.
 template <typename W>
 int launch_words(const Args& a, const Group& g, int sms, cudaStream_t s) {
+    constexpr int FULL = sizeof(W) == 16 ? 3 : 1;  // (of smaller words `places` takes as many as make 16)
     if (a.beams > 16) return launch<W, 0, 1, 128>(a, g, sms, a.beams * 128 * int(sizeof(W)), s);
     if (a.beams > 8) return launch<W, 16, 1, 256>(a, g, sms, 0, s);
     const bool few = g.total * a.requests * ((g.most + 1023) / 1024) < 4 * sms;
     if (a.beams > 4) return few ? launch<W, 8, 1, 128>(a, g, sms, 0, s) : launch<W, 8, 2, 256>(a, g, sms, 0, s);
-    return few ? launch<W, 4, 1, 256>(a, g, sms, 0, s) : launch<W, 4, 3, 256>(a, g, sms, 0, s);
+    return few ? launch<W, 4, 1, 256>(a, g, sms, 0, s) : launch<W, 4, FULL, 256>(a, g, sms, 0, s);
 }
 
 }  // namespace hl_reorder

@@ -10,10 +10,12 @@
 // steps: fp32 scores with a bound of their error leave hardly more than `keep`, which are scored in
 // fp64 and ranked. So the order between beams does not hang on fp32 rounding of the scores.
 //
-// What bounds it: 2048 bf16 rows of 151936 under a softcap take 202 us in slice_kernel, at 39% of HBM's rate and 62%
-// of the issue slots (15 instructions a logit, the capped exponentials among them). Whole slices held in
-// registers took 252 us, slices in batches through registers 297. Up to some tens of rows the two launches
-// and their chains of steps count: 4 x 32000 14 us, of which the merge is 11; a merge of 256 x 8 beams is 21.
+// What bounds it: 2048 bf16 rows of 151936 under a softcap take 197 us in slice_kernel, at 40% of HBM's rate and 62%
+// of the issue slots (15 instructions a logit, the capped exponentials among them), and 13 in merge_kernel (each by
+// itself; a call 200 to 210). Whole slices held in registers took 252 us, slices in batches through registers 297. Up to
+// some tens of rows the two launches and their chains of steps count: 4 x 32000 14 us, of which the merge is 11.
+// A slice whose candidates are too many for its list, or come with few threads, is bisected by reading it again: 64 rows
+// of 32000 equal logits 770 us, and of 128 or 256 allowed tokens in a run 690 (of 16, 64, 384 and more 15).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

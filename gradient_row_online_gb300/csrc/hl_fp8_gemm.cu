@@ -8,16 +8,16 @@
 // than 128 products.
 //
 // One CTA an SM walks the 128 x 256 tiles of out. Few rows of a take the same way: a's tile is then
-// 32 or 64 rows of copies, the MMAs' other rows are whatever follows and their sums never read, and b, 256 rows
+// 64 rows of copies, the MMAs' other rows are whatever follows and their sums never read, and b, 256 rows
 // at a time, streams through at HBM's rate. (b as the MMA's 128 rows and a as its 16 to 64 columns is
 // slower: such an MMA takes the time of 128 columns and more, and moves half the bytes of b: 48 x 128256 took 115
 // us.) The tiles of the last round, which are fewer than SMs, have their K split where that takes less time; the
 // parts go to the workspace in fp32 and a second kernel adds them in order.
 //
 // What bounds it, at many rows: shared memory moves 96 KB a block of K (48 written by the copies, 48 read by the
-// MMAs), 768 cycles at 128 bytes a cycle, and reading the accumulator back takes another 256 of TMEM's: 1024, of
-// which the MMAs' own 512 are half. Measured some 1070 cycles, 2.2 PFLOP/s (8192 x 32000 x 4096 0.98 ms); with K summed
-// in TMEM throughout, which the scales do not allow, 0.74 ms. Tiles of 256 x 256 on pairs of CTAs
+// MMAs), 768 cycles at 128 bytes a cycle, and reading the accumulator back takes another 256 of TMEM's: 1024 one after
+// the other, of which the MMAs' own 512 are half. Measured some 1000 cycles, 2.3 PFLOP/s (8192 x 32000 x 4096 0.90 to 0.94 ms); with K
+// summed in TMEM throughout, which the scales do not allow, 0.74 ms. Tiles of 256 x 256 on pairs of CTAs
 // (cta_group::2) move 64 KB a block, but with two accumulators the way over to the other CTA and back is not
 // hidden (840 cycles from an accumulator's release to the next MMAs on it): 1.30 ms.
 // Every wait is bounded; one that gives up sets bit 0 of *err, and the kernel drains what it issued.
@@ -129,9 +129,9 @@ __device__ __forceinline__ uint32_t pieces(const WideArgs& p) {
 
 // 32 staged rows (128 bytes each, 128-byte swizzle) to rows of out that start anywhere: the first `cols` elements.
 // What costs is the sectors that a store instruction writes in part. So fp32 rows go an element a lane, 128
-// bytes in a row (4096 x 100001 x 512: 710 us, and 824 the other way), and 16-bit rows, eight lanes each, in 16-byte
-// units of out, each put together from two of the staged ones, with the elements before and behind them (515 us,
-// and 627 an element a lane; 289 where rows start on 16 bytes and TMA stores them).
+// bytes in a row (4096 x 100001 x 512: 675 us, the other way 114 more; 410 where rows start on 16 bytes and TMA stores
+// them), and 16-bit rows, eight lanes each, in 16-byte units of out, each put together from two of the staged ones, with
+// the elements before and behind them (508 us, an element a lane 112 more; 284 on 16 bytes).
 template <int OT>
 __device__ __forceinline__ void store_rows(const unsigned char* stage, const WideArgs& p, int64_t r0, int64_t c0, int cols,
                                            int lane) {
@@ -464,10 +464,10 @@ struct Plan {
 };
 
 // The tiles go over the SMs in rounds; those of the last, incomplete round have their K in as many parts as take
-// the least time: a block of K some 0.58 us, with few rows what its 32 KB of b take (0.4 us alone, HBM's rate
+// the least time: a block of K counts 0.58 us (0.53 measured in full rounds), with few rows what its 32 KB of b take (0.4 us alone, HBM's rate
 // together), and for parts a second launch (4 us) and their sums written and read (5 bytes a picosecond). Measured,
-// whole and in parts: 4096 x 4096 x 128256 2155 and 1927 us, 512 x 4096 x 128256 534 and 311, 1 x 4096 x 32000 114
-// and 32, 200 x 1000 x 5003 26 and 12.
+// whole and in parts: 4096 x 4096 x 128256 2020 and 1830 us, 512 x 4096 x 128256 502 and 287, 1 x 4096 x 32000 117
+// and 35, 200 x 1000 x 5003 29 and 15.
 Plan plan_of(int64_t M, int64_t N, int64_t K, int sms) {
     const int64_t KB = (K + BK - 1) / BK, tiles = ((M + WM - 1) / WM) * ((N + WN - 1) / WN), rest = tiles % sms;
     Plan r = {tiles - rest, 1, 0};

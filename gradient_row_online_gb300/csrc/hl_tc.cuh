@@ -1,5 +1,5 @@
-// hl_tc.cuh -- the PTX that tensor-core kernels are made of: mbarriers with bounded waits, TMA
-// copies, tcgen05 with TMEM, clusters.
+// hl_tc.cuh -- the PTX that the 8-bit products are made of: mbarriers with bounded waits, TMA copies,
+// tcgen05 with TMEM, register splits. (lmhead_tc.cu has its own.)
 #pragma once
 #include <cuda.h>
 #include <cudaTypedefs.h>

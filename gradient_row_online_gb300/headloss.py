@@ -756,8 +756,9 @@ class Fp8Head:
     `weight` (V x D, unit column stride) is quantised once, in 128 x 128 blocks of e4m3;
     `set_weight` does so again after an optimiser's step, into the same buffers (order it
     with calls on other streams; a checkpoint's codes are left, the first time, for buffers of
-    the head's own, and kept: a graph captured before goes on reading them).  `grads` is the 8-bit type of the loss's gradient, "e4m3"
-    or "e5m2".  A call's own buffers are made on the stream it runs on."""
+    the head's own, and kept with the head: a graph captured before goes on with them).
+    `grads` is the 8-bit type of the loss's gradient, "e4m3" or "e5m2".  A call's own buffers
+    are made on the stream it runs on."""
 
     _TYPES = {"e4m3": HEADLOSS_E4M3, "e5m2": HEADLOSS_E5M2}
 
@@ -796,8 +797,7 @@ class Fp8Head:
             if train:
                 self.qt = torch.zeros(D, -(-V // 16) * 16, dtype=torch.uint8, device=q.device)
                 self.qt[:, :V].copy_(codes.t())
-                self.ldqt = self.qt.shape[1]
-                self.scales_t = self.scales.t().clone(memory_format=torch.contiguous_format)
+                self.ldqt, self.scales_t = self.qt.shape[1], self.scales.t().contiguous()
         return self
 
     def _setup(self, V, D, like, train, grads):
@@ -817,17 +817,16 @@ class Fp8Head:
         with _on(self.index, None):
             self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
 
-    def _make_codes(self):
-        self.ldq = -(-self.D // 16) * 16
-        self.q = self._empty(self.V, self.ldq, dtype=self._u8, device=self.device)
-        self.scales = self._empty(-(-self.V // 128), -(-self.D // 128), dtype=self._f32, device=self.device)
-
     def _make(self):
-        self._make_codes()
+        u8, f32, dev = self._u8, self._f32, self.device
+        vb, db = -(-self.V // 128), -(-self.D // 128)
+        self.ldq = -(-self.D // 16) * 16
+        self.q = self._empty(self.V, self.ldq, dtype=u8, device=dev)
+        self.scales = self._empty(vb, db, dtype=f32, device=dev)
         if self.train:
             self.ldqt = -(-self.V // 16) * 16
-            self.qt = self._empty(self.D, self.ldqt, dtype=self._u8, device=self.device)
-            self.scales_t = self._empty(-(-self.D // 128), -(-self.V // 128), dtype=self._f32, device=self.device)
+            self.qt = self._empty(self.D, self.ldqt, dtype=u8, device=dev)
+            self.scales_t = self._empty(db, vb, dtype=f32, device=dev)
 
     @staticmethod
     def _matrix(name, a, index):
@@ -880,9 +879,10 @@ class Fp8Head:
         if tuple(weight.shape) != (self.V, self.D):
             raise ValueError(f"weight: {self.V} x {self.D} is wanted")
         if self.held:
-            # kept: the allocator may give freed memory to a stream that does not wait for the calls that read it
-            self.checkpoint = self.q, self.scales
-            self._make_codes()
+            # Kept: the allocator may give freed memory to a stream that does not wait for the calls that read it. And
+            # not written to: their type may be another than the new codes'.
+            self.checkpoint = self.q, self.scales, *((self.qt, self.scales_t) if self.train else ())
+            self._make()
             self.type, self.held = HEADLOSS_E4M3, False
         t, self.weight_dtype = self.train, weight.dtype
         self._quantize(weight, HEADLOSS_E4M3, self.q.data_ptr(), self.ldq, self.scales.data_ptr(), 128,

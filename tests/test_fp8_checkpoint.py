@@ -14,21 +14,23 @@ def test_what_a_call_may_still_read_stays(machine):  # noqa: F811
     h = head_on(machine, 0)
     h.held = True
     refs = [weakref.ref(t) for t in (h.q, h.scales, h.qt, h.scales_t)]
-    addresses = [id(h.qt), id(h.scales_t)]
     h.set_weight(Matrix((300, 200)))
     gc.collect()
     assert all(r() is not None for r in refs)
-    assert h.q is not refs[0]() and h.scales is not refs[1]()
-    assert [id(h.qt), id(h.scales_t)] == addresses  # the head's own: written to in place
+    assert all(new is not r() for new, r in zip((h.q, h.scales, h.qt, h.scales_t), refs))
+    after = h.q, h.qt
+    h.set_weight(Matrix((300, 200)))
+    assert (h.q, h.qt) == after
 
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("V,D", [(300, 208), (100, 256), (1000, 100), (77, 33)])  # one row or column of blocks: scales that turn to themselves
-def test_a_checkpoint_is_read_and_left(V, D):
+@pytest.mark.parametrize("kind", [torch.float8_e4m3fn, torch.float8_e5m2])
+def test_a_checkpoint_is_read_and_left(V, D, kind):
     g = torch.Generator().manual_seed(V)
     w = torch.randn(V, D, generator=g).cuda()
     made = pkg.Fp8Head(w, train=True)
-    q = made.q[:, :D].view(torch.float8_e4m3fn).clone()
+    q = made.q[:, :D].view(torch.float8_e4m3fn).float().to(kind)
     scales = made.scales.clone()
     bits, before = q.view(torch.uint8).clone(), scales.clone()
     held = pkg.Fp8Head.from_quantized(q, scales, train=True)
@@ -37,7 +39,7 @@ def test_a_checkpoint_is_read_and_left(V, D):
     held.logits(x)
     torch.cuda.synchronize()
     with torch.cuda.graph(graph):
-        captured = held.logits(x)
+        captured = held.logits(x), *held.backward(dl, x)
     for head in (made, held):
         head.set_weight(-3 * w)
     assert torch.equal(q.view(torch.uint8), bits) and torch.equal(scales, before)
@@ -49,4 +51,6 @@ def test_a_checkpoint_is_read_and_left(V, D):
     graph.replay()
     torch.cuda.synchronize()
     # the graph goes on with the checkpoint's codes
-    assert torch.equal(captured, pkg.Fp8Head.from_quantized(bits.view(torch.float8_e4m3fn), before).logits(x)) and junk
+    again = pkg.Fp8Head.from_quantized(bits.view(kind), before, train=True)
+    for a, b in zip(captured, (again.logits(x), *again.backward(dl, x))):
+        assert torch.equal(a, b) and junk
